@@ -504,6 +504,135 @@ gm_status gm_dense_refresh_edges(const void *q, const void *k, gm_dtype dtype, c
                                  int32_t *out_idx, float *out_w, cudaStream_t stream);
 
 /*
+ * ---- The dense layers of a hybrid model, and serving -------------------------------------------
+ *
+ * The pages' hybrid models mix sparse layers with dense attention layers (ai.info summary,
+ * "Methodology in Plain English", hybrid paragraph: a Qwen3-0.6B backbone). The calls below are
+ * that dense attention (its lse is what gm_dense_refresh_edges reads) and both layers' form for
+ * single tokens, over a paged key/value cache in 8 bits. The pages have no counterpart to the
+ * window, the sinks or the cache.
+ *
+ * gm_window_attention_forward - causal attention with a sliding window and always-visible first
+ * tokens. Query i of sequence b sees key t iff t <= i < lens[b] and (i - t < window or
+ * t < sinks). For each (b, i, hq) with h = hq / (hq_count / hkv), over the keys it sees:
+ * z_t = scale * <q[b,i,hq], k[b,t,h]>, o[b,i,hq] = sum_t softmax(z)_t v[b,t,h],
+ * lse[b,i,hq] = ln sum_t exp(z_t). Rows at or past lens[b] give o = 0 and lse = -inf.
+ *
+ *   q, k, v   device, `dtype`, [B, n, hq | hkv, d], 16-byte aligned. Rows at or past lens[b] are
+ *             not used and may hold anything, also infinities and NaN
+ *   lens      device int32 [B]: tokens of each sequence, taken as 0..n; NULL: n each
+ *   window    >= 1 (n or more: every earlier token is visible)
+ *   sinks     >= 0 first tokens that stay visible outside the window
+ *   o         device, `dtype`, [B, n, hq, d], 16-byte aligned, written in full
+ *   lse       device fp32 [B, n, hq], written in full; may be NULL
+ *   limits    d in {64, 128}; any hq / hkv; n < 2^30, B * n * hq < 2^31
+ * Scores, softmax statistics and sums are fp32; for GM_BF16 the probabilities are rounded to
+ * bf16 before they meet v. Deterministic.
+ */
+gm_status gm_window_attention_forward(const void *q, const void *k, const void *v, gm_dtype dtype,
+                                      const int32_t *lens, int B, int n, int hq, int hkv, int d,
+                                      int window, int sinks, float scale, void *o, float *lse,
+                                      cudaStream_t stream);
+
+/*
+ * gm_window_attention_backward - gradients of gm_window_attention_forward. With
+ * P = exp(z - lse), delta = <dout, o> and dz_t = P_t (<dout, v_t> - delta):
+ *   dq = scale * sum_t dz_t k_t;   dk_t = scale * sum_i dz_t q_i;   dv_t = sum_i P_t dout_i
+ * (dk, dv summed over the query heads of the group). Rows at or past lens[b] get 0.
+ *
+ *   q, k, v, dtype, lens, window, sinks, scale   as the forward was called
+ *   o, lse       what the forward returned; dout device, `dtype`, [B, n, hq, d]
+ *   dq, dk, dv   device, `dtype` (each element is summed in fp32, in a fixed order without
+ *                atomics, and rounded once), laid out as q, k, v, written in full
+ *   workspace    device scratch owned by the caller, 16-byte aligned, at least
+ *                gm_window_attention_backward_workspace_size(...) bytes; its contents do not
+ *                matter and are garbage on return. Calls that overlap on the GPU need one each
+ *   limits       as the forward; every pointer 16-byte aligned except lens and lse
+ * For GM_BF16, P and dz are rounded to bf16 before their products. Deterministic.
+ */
+gm_status gm_window_attention_backward(const void *q, const void *k, const void *v, const void *o,
+                                       const void *dout, const float *lse, gm_dtype dtype,
+                                       const int32_t *lens, int B, int n, int hq, int hkv, int d,
+                                       int window, int sinks, float scale, void *dq, void *dk,
+                                       void *dv, void *workspace, size_t workspace_bytes,
+                                       cudaStream_t stream);
+
+/* Bytes of workspace gm_window_attention_backward needs. Pure host function; no CUDA call. */
+size_t gm_window_attention_backward_workspace_size(int B, int n, int hq);
+
+/*
+ * gm_kv8_append - put new tokens' keys and values into a paged cache held in 8 bits.
+ *
+ * The cache of one layer: kq, vq [num_pages, hkv, page, d] e4m3 values; kscale, vscale
+ * [num_pages, hkv] fp32, one scale per block (page, KV head): an element stands for
+ * value * scale. table [B, max_pages] int32 lists each sequence's pages in order; token p of
+ * sequence b is row p % page of page table[b, p / page].
+ *
+ * Rows x < new_lens[b] of k and v become tokens lens[b] + x. A block's scale is 2^e with the
+ * smallest e >= -100 such that the largest magnitude it was given is at most 448 * 2^e (448:
+ * the largest e4m3 value), and an element is stored as x / scale rounded to nearest even. A
+ * block that already holds tokens (lens[b] not a multiple of page) never gets a smaller scale;
+ * when it gets a larger one its older elements are rounded again at that scale. A block that is
+ * given an infinity or NaN gets the scale NaN, and everything that reads it gives NaN, until
+ * the page is filled anew from its first row. lens is not changed: the caller adds the new
+ * tokens before the attention calls. Other pages and rows keep their contents.
+ *
+ *   k, v        device, `dtype`, [B, t, hkv, d], 16-byte aligned
+ *   kq, vq      device, 16-byte aligned; kscale, vscale device fp32
+ *   lens        device int32 [B]: tokens that each sequence holds before the call
+ *   new_lens    device int32 [B]: rows of k and v that belong to the sequence, taken as 0..t;
+ *               NULL: t each
+ *   page        16, 32, 64 or 128 tokens; limits: d in {64, 128}
+ * No two sequences may write the same page in one call (fork a page by copying it first). A
+ * page outside [0, num_pages), a negative length, or a token past max_pages * page is not
+ * written and raises the device index-range flag (gm_check_device_errors).
+ */
+gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int t, int hkv, int d,
+                        void *kq, void *vq, float *kscale, float *vscale, int num_pages, int page,
+                        const int32_t *table, int max_pages, const int32_t *lens,
+                        const int32_t *new_lens, cudaStream_t stream);
+
+/*
+ * gm_kv8_attention_forward - gm_window_attention_forward for the last tokens of each sequence,
+ * over the cache of gm_kv8_append. Row x < q_lens[b] of q is the token at position
+ * lens[b] - q_lens[b] + x; it sees the cached tokens by the same rule (window, sinks). Rows at or
+ * past q_lens[b], and rows whose position is negative, give o = 0 and lse = -inf.
+ *
+ *   q           device, `dtype`, [B, t, hq, d], 16-byte aligned; t = 1 for single tokens
+ *   kq .. table as gm_kv8_append (rows of a page past the sequence's end may hold anything)
+ *   lens        device int32 [B]: tokens in the cache, the query rows' own tokens included
+ *   q_lens      device int32 [B], taken as 0..t; NULL: t each
+ *   o, lse      as gm_window_attention_forward ([B, t, hq, d] and [B, t, hq]; lse may be NULL)
+ *   limits      d in {64, 128}; any hq / hkv; page as gm_kv8_append
+ * fp32 scores, statistics and sums; for GM_BF16 probabilities are rounded to fp16 before they
+ * meet the values, for GM_F32 queries and probabilities keep 22 bits. Deterministic. A page
+ * outside [0, num_pages) or a length outside [0, max_pages * page] raises the device
+ * index-range flag (the page is read as page 0, the length is clamped).
+ */
+gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, int hq, int hkv, int d,
+                                   const void *kq, const void *vq, const float *kscale,
+                                   const float *vscale, int num_pages, int page,
+                                   const int32_t *table, int max_pages, const int32_t *lens,
+                                   const int32_t *q_lens, int window, int sinks, float scale,
+                                   void *o, float *lse, cudaStream_t stream);
+
+/*
+ * gm_kv8_sea_forward - gm_sea_forward for the last tokens of each sequence, over the cache of
+ * gm_kv8_append: the row's edges idx/w [B, t, hkv, s] point at cached tokens (1 <= s <= 32), a
+ * slot is active iff w > 0, z_j = scale * <q, k[t_j]> + ln w_j. Rows, lengths, q_lens, outputs
+ * and limits as gm_kv8_attention_forward. An active slot of a row below q_lens[b] whose index
+ * lies outside [0, lens[b]), or whose page lies outside the pool, is skipped and raises the
+ * index-range flag. fp32 arithmetic throughout. Deterministic. The checked build verifies the
+ * edges of the rows below q_lens[b] (weights finite and >= 0, indices at most the row's position).
+ */
+gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, const float *w, int s,
+                             int B, int t, int hq, int hkv, int d, const void *kq, const void *vq,
+                             const float *kscale, const float *vscale, int num_pages, int page,
+                             const int32_t *table, int max_pages, const int32_t *lens,
+                             const int32_t *q_lens, float scale, void *o, float *lse,
+                             cudaStream_t stream);
+
+/*
  * gm_check_device_errors - synchronise `stream`, then read and clear this device's error
  * flag. Returns GM_ERR_INDEX_RANGE if any kernel of this library on the current device met
  * an active slot whose index lay outside [0, n) since the last check, GM_ERR_EDGE_INVALID if

@@ -17,6 +17,12 @@ its Python binding plus the seeded synthetic-input generators (`inputs`).
     gm_ser_sea_backward both backward passes in one call (the referral's inside the attention's)
     gm_dense_refresh_edges
                         refresh edges from a dense attention layer (its top positions)
+    gm_window_attention_forward / _backward
+                        a hybrid model's dense layers: causal attention with a sliding window and
+                        always-visible first tokens
+    gm_kv8_append, gm_kv8_attention_forward, gm_kv8_sea_forward
+                        serving: a paged key/value cache in 8 bits, and both kinds of attention
+                        over it for the last tokens of each sequence
     gm_selftest_wait_timeout
                         diagnostic: one bounded wait that runs out (GM_ERR_WAIT_TIMEOUT)
 """
@@ -30,6 +36,9 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     gm_check_device_errors,
     gm_dense_refresh_edges,
+    gm_kv8_append,
+    gm_kv8_attention_forward,
+    gm_kv8_sea_forward,
     gm_leg_backward,
     gm_leg_sparsify,
     gm_sea_backward,
@@ -48,6 +57,9 @@ from ._binding import (  # noqa: F401
     gm_ser_sea_forward,
     gm_selftest_wait_timeout,
     gm_version,
+    gm_window_attention_backward,
+    gm_window_attention_backward_workspace_size,
+    gm_window_attention_forward,
     load_library,
     status_string,
 )

@@ -8,6 +8,7 @@ call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -57,6 +58,17 @@ SIGNATURES = {
                             _ci, _ci, _ci, _ci, _cf, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                             _ci, _vp],
     "gm_dense_refresh_edges": [_vp, _vp, _ci, _vp, _ci, _ci, _ci, _ci, _ci, _cf, _ci, _vp, _vp, _vp],
+    "gm_window_attention_forward": [_vp, _vp, _vp, _ci, _vp, _ci, _ci, _ci, _ci, _ci, _ci, _ci, _cf, _vp,
+                                    _vp, _vp],
+    "gm_window_attention_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _ci, _vp, _ci, _ci, _ci, _ci, _ci, _ci,
+                                     _ci, _cf, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+    "gm_window_attention_backward_workspace_size": [_ci, _ci, _ci],
+    "gm_kv8_append": [_vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci, _vp, _vp,
+                      _vp],
+    "gm_kv8_attention_forward": [_vp, _ci, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci,
+                                 _vp, _vp, _ci, _ci, _cf, _vp, _vp, _vp],
+    "gm_kv8_sea_forward": [_vp, _ci, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci,
+                           _vp, _ci, _vp, _vp, _cf, _vp, _vp, _vp],
     "gm_check_device_errors": [_vp],
     "gm_status_string": [_ci],
     "gm_version": [],
@@ -95,6 +107,7 @@ def open_library(path: str) -> ctypes.CDLL:
         fn.argtypes = args
         fn.restype = {"gm_status_string": ctypes.c_char_p,
                       "gm_sea_backward_workspace_size": ctypes.c_size_t,
+                      "gm_window_attention_backward_workspace_size": ctypes.c_size_t,
                       "gm_sea_backward_noalloc_max_scratch": ctypes.c_size_t}.get(name, ctypes.c_int)
     return lib
 
@@ -605,6 +618,191 @@ def gm_dense_refresh_edges(q, k, lse, sf: int, scale=None, out_idx=None, out_w=N
         _ptr(out_w, torch.float32, "out_w"), _stream(stream))
     _check(st, "gm_dense_refresh_edges")
     return out_idx, out_w
+
+
+# ---- dense layers and serving ---------------------------------------------------------------------
+
+
+def _on(dev, stream):
+    """Context in which `dev` is current and torch's current stream is the call's: outputs then
+    belong to the stream that writes them."""
+    if stream is None:
+        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _arg(t, shape, dtype, dev, name):
+    """Pointer of a contiguous tensor of this shape, type and device."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _queries(q, hkv):
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, n, hq, d]")
+    if hkv < 1 or q.shape[2] % hkv:
+        raise ValueError(f"{q.shape[2]} query heads do not divide into {hkv} KV heads")
+    return q.device
+
+
+def _window(window, sinks):
+    window = 2**31 - 1 if window is None else int(window)
+    if window < 1 or int(sinks) < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    return min(window, 2**31 - 1), min(int(sinks), 2**31 - 1)
+
+
+def _out(t, shape, dtype, dev, name):
+    """An output: the caller's tensor, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, _arg(t, shape, dtype, dev, name)
+
+
+def gm_window_attention_forward(q, k, v, window=None, sinks: int = 0, lens=None, scale=None, o=None, lse=None,
+                                stream=None):
+    """Causal attention with a sliding window (None: every earlier token) and `sinks` first tokens
+    that stay visible. q [B, n, hq, d], k and v [B, n, hkv, d]; lens int32 [B] or None. Returns
+    (o, lse [B, n, hq] fp32); gm_dense_refresh_edges takes the lse of a call without a window."""
+    hkv, d = k.shape[-2:]
+    dev = _queries(q, hkv)
+    B, n, hq, _ = q.shape
+    dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
+    window, sinks = _window(window, sinks)
+    with _on(dev, stream):
+        o, po = _out(o, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+        st = load_library().gm_window_attention_forward(
+            _arg(q, q.shape, dt, dev, "q"), _arg(k, kv, dt, dev, "k"), _arg(v, kv, dt, dev, "v"), _fdtype(q),
+            None if lens is None else _arg(lens, (B,), torch.int32, dev, "lens"), B, n, hq, hkv, d, window, sinks,
+            _scale(scale, d), po, pl, torch.cuda.current_stream().cuda_stream)
+    _check(st, "gm_window_attention_forward")
+    return o, lse
+
+
+def gm_window_attention_backward_workspace_size(B: int, n: int, hq: int) -> int:
+    """Workspace bytes of gm_window_attention_backward."""
+    return int(load_library().gm_window_attention_backward_workspace_size(B, n, hq))
+
+
+def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int = 0, lens=None, scale=None,
+                                 dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of gm_window_attention_forward from its o and lse. Returns (dq, dk, dv) in the
+    features' dtype. workspace: a uint8 CUDA tensor of at least
+    gm_window_attention_backward_workspace_size(...) bytes; None allocates one."""
+    hkv, d = k.shape[-2:]
+    dev = _queries(q, hkv)
+    B, n, hq, _ = q.shape
+    dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
+    window, sinks = _window(window, sinks)
+    lib = load_library()
+    with _on(dev, stream):
+        dq, pdq = _out(dq, q.shape, dt, dev, "dq")
+        dk, pdk = _out(dk, kv, dt, dev, "dk")
+        dv, pdv = _out(dv, kv, dt, dev, "dv")
+        if workspace is None:
+            workspace = torch.empty(lib.gm_window_attention_backward_workspace_size(B, n, hq), dtype=torch.uint8,
+                                    device=dev)
+        st = lib.gm_window_attention_backward(
+            _arg(q, q.shape, dt, dev, "q"), _arg(k, kv, dt, dev, "k"), _arg(v, kv, dt, dev, "v"),
+            _arg(o, q.shape, dt, dev, "o"), _arg(dout, q.shape, dt, dev, "dout"),
+            _arg(lse, q.shape[:3], torch.float32, dev, "lse"), _fdtype(q),
+            None if lens is None else _arg(lens, (B,), torch.int32, dev, "lens"), B, n, hq, hkv, d, window, sinks,
+            _scale(scale, d), pdq, pdk, pdv, _arg(workspace, workspace.shape, torch.uint8, dev, "workspace"),
+            workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    _check(st, "gm_window_attention_backward")
+    return dq, dk, dv
+
+
+def _cache(kq, vq, kscale, vscale, table, lens, B, d, dev):
+    """The C arguments of a cache (kq .. max_pages, lens), checked."""
+    if kq.dim() != 4 or kq.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("kq must be [num_pages, hkv, page, d] in float8_e4m3fn or uint8")
+    pages, hkv, page, _ = kq.shape
+    if kq.shape[3] != d:
+        raise ValueError(f"the cache has head_dim {kq.shape[3]}, the features {d}")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("table must be [B, max_pages]")
+    f32, i32 = torch.float32, torch.int32
+    return (_arg(kq, kq.shape, kq.dtype, dev, "kq"), _arg(vq, kq.shape, kq.dtype, dev, "vq"),
+            _arg(kscale, kq.shape[:2], f32, dev, "kscale"), _arg(vscale, kq.shape[:2], f32, dev, "vscale"),
+            pages, page, _arg(table, table.shape, i32, dev, "table"), table.shape[1],
+            _arg(lens, (B,), i32, dev, "lens"))
+
+
+def gm_kv8_append(k, v, kq, vq, kscale, vscale, table, lens, new_lens=None, stream=None):
+    """Put new tokens' k and v [B, t, hkv, d] behind the lens[b] tokens each sequence holds, in
+    8 bits with a scale per (page, KV head); kq, vq, kscale, vscale are written in place. lens is
+    not changed: add the new tokens to it before the attention calls."""
+    if not k.is_cuda or k.dim() != 4:
+        raise ValueError("k must be a CUDA tensor [B, t, hkv, d]")
+    B, t, hkv, d = k.shape
+    dev = k.device
+    if kq.dim() != 4 or kq.shape[1] != hkv:
+        raise ValueError(f"kq must be [num_pages, {hkv}, page, {d}]")
+    cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
+    with _on(dev, stream):
+        st = load_library().gm_kv8_append(
+            _arg(k, k.shape, k.dtype, dev, "k"), _arg(v, k.shape, k.dtype, dev, "v"), _fdtype(k), B, t, hkv, d, *cache,
+            None if new_lens is None else _arg(new_lens, (B,), torch.int32, dev, "new_lens"),
+            torch.cuda.current_stream().cuda_stream)
+    _check(st, "gm_kv8_append")
+
+
+def gm_kv8_attention_forward(q, kq, vq, kscale, vscale, table, lens, window=None, sinks: int = 0, q_lens=None,
+                             scale=None, o=None, lse=None, stream=None):
+    """gm_window_attention_forward for the last tokens of each sequence (q [B, t, hq, d]) over the
+    8-bit cache; lens counts the query tokens too. Returns (o, lse [B, t, hq])."""
+    hkv = kq.shape[1]
+    dev = _queries(q, hkv)
+    B, t, hq, d = q.shape
+    dt = q.dtype
+    window, sinks = _window(window, sinks)
+    cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
+    with _on(dev, stream):
+        o, po = _out(o, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+        st = load_library().gm_kv8_attention_forward(
+            _arg(q, q.shape, dt, dev, "q"), _fdtype(q), B, t, hq, hkv, d, *cache,
+            None if q_lens is None else _arg(q_lens, (B,), torch.int32, dev, "q_lens"), window, sinks,
+            _scale(scale, d), po, pl, torch.cuda.current_stream().cuda_stream)
+    _check(st, "gm_kv8_attention_forward")
+    return o, lse
+
+
+def gm_kv8_sea_forward(q, idx, w, kq, vq, kscale, vscale, table, lens, q_lens=None, scale=None, o=None, lse=None,
+                       stream=None):
+    """gm_sea_forward for the last tokens of each sequence (q [B, t, hq, d], idx and w
+    [B, t, hkv, s]) over the 8-bit cache. Returns (o, lse [B, t, hq])."""
+    hkv = kq.shape[1]
+    dev = _queries(q, hkv)
+    B, t, hq, d = q.shape
+    dt, s = q.dtype, idx.shape[-1]
+    edges = torch.Size((B, t, hkv, s))
+    cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
+    with _on(dev, stream):
+        o, po = _out(o, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+        st = load_library().gm_kv8_sea_forward(
+            _arg(q, q.shape, dt, dev, "q"), _fdtype(q), _arg(idx, edges, torch.int32, dev, "idx"),
+            _arg(w, edges, torch.float32, dev, "w"), s, B, t, hq, hkv, d, *cache,
+            None if q_lens is None else _arg(q_lens, (B,), torch.int32, dev, "q_lens"), _scale(scale, d), po, pl,
+            torch.cuda.current_stream().cuda_stream)
+    _check(st, "gm_kv8_sea_forward")
+    return o, lse
 
 
 def gm_check_device_errors(stream=None):

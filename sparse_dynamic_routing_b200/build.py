@@ -2,8 +2,10 @@
 
     python -m sparse_dynamic_routing_b200.build [--force] [--verbose]
 
-One translation unit (csrc/gm_api.cu) with the C ABI of include/gm.h (--checked builds the
-variant that verifies every input edge tensor, libgm_b200_checked.so); the CUDA runtime is
+Two translation units (csrc/gm_api.cu, csrc/gm_attn.cu), compiled side by side, with the C ABI
+of include/gm.h (--checked builds the variant that verifies every input edge tensor,
+libgm_b200_checked.so); an object is compiled again when a file it includes is newer. The CUDA
+runtime is
 linked statically, so the library only needs the NVIDIA driver at run time. No fast-math:
 the referral step relies on IEEE fp32 products and sums (it uses the _rn intrinsics), and
 denormals are kept (-ftz=false).
@@ -27,8 +29,9 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
-    "-Xcompiler", "-fPIC", "-shared", "-cudart", "static",
+    "-Xcompiler", "-fPIC", "-cudart", "static",
 ]
+OBJ_DIR = os.path.join(HERE, "build")
 
 
 def nvcc() -> str:
@@ -50,15 +53,39 @@ def stale(lib: str = LIB) -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _object_is_stale(obj: str, dep: str) -> bool:
+    """Whether an object is older than a file named in its dependency list (as nvcc wrote it)."""
+    if not os.path.exists(obj) or not os.path.exists(dep):
+        return True
+    t = os.path.getmtime(obj)
+    with open(dep) as f:
+        files = f.read().split(":", 1)[-1].replace("\\\n", " ").split()
+    return any(not os.path.exists(x) or os.path.getmtime(x) > t for x in files)
+
+
+def _compile(src: str, variant: str, flags: list[str], force: bool) -> tuple[str, subprocess.Popen | None]:
+    """The object of one source, and the compiler process that is making it (None: up to date)."""
+    obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + variant + ".o")
+    dep = obj + ".d"
+    if not force and not _object_is_stale(obj, dep):
+        return obj, None
+    return obj, subprocess.Popen([nvcc(), *NVCC_FLAGS, *flags, "-MD", "-MF", dep, "-c", src, "-o", obj])
+
+
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     lib = CHECKED_LIB if checked else LIB
     if force or stale(lib):
+        os.makedirs(OBJ_DIR, exist_ok=True)
+        flags = (["-DGM_CHECKED=1"] if checked else []) + (["-Xptxas", "-v"] if verbose else [])
+        made = [_compile(src, "_checked" if checked else "", flags, force)
+                for src in sorted(glob.glob(os.path.join(CSRC, "*.cu")))]
+        for obj, proc in made:
+            if proc is not None and proc.wait() != 0:
+                if os.path.exists(obj):
+                    os.remove(obj)
+                raise subprocess.CalledProcessError(proc.returncode, proc.args)
         tmp = lib + f".tmp{os.getpid()}"
-        cmd = [nvcc(), *NVCC_FLAGS, *(["-DGM_CHECKED=1"] if checked else []),
-               os.path.join(CSRC, "gm_api.cu"), "-o", tmp]
-        if verbose:
-            cmd[1:1] = ["-Xptxas", "-v"]
-        subprocess.run(cmd, check=True)
+        subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *(obj for obj, _ in made), "-o", tmp], check=True)
         os.replace(tmp, lib)
     return lib
 

@@ -11,6 +11,7 @@
 #include "gm_common.cuh"
 #include "gm_dense_refresh.cuh"
 #include "gm_fused_tile.cuh"
+#include "gm_host.cuh"
 #include "gm_leg.cuh"
 #include "gm_leg_tile.cuh"
 #include "gm_sea.cuh"
@@ -30,14 +31,6 @@ constexpr int WPB_SER_THREAD = 4;  // warps per block of the thread-per-row SER 
 constexpr int WPB_SEA = GM_WPB_SEA;
 constexpr int WPB_BWD = GM_WPB_BWD;
 constexpr int MAX_SLOTS = 32;
-constexpr int64_t MAX_ROWS = (int64_t)1 << 31;  // edge rows B*n*heads indexed in 32 bits
-
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-inline gm_status launched()
-{
-    return cudaGetLastError() == cudaSuccess ? GM_OK : GM_ERR_CUDA;
-}
 
 inline unsigned blocks_for(int64_t rows, int wpb) { return (unsigned)((rows + wpb - 1) / wpb); }
 
@@ -521,27 +514,6 @@ template <typename T, int D, int G> struct SeaBwdGather {
 };
 
 // ---- refresh edges from a dense attention layer ----------------------------------------------
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (the library does not link
-// the driver library itself).
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 
 // A bf16 feature tensor [rows, heads, d] as a 3-d TMA map whose boxes are 64 elements of d
 // (128 bytes, the swizzle width) x 1 head x box_rows rows, in the 128-byte swizzle layout.
@@ -1225,9 +1197,12 @@ gm_status gm_check_device_errors(cudaStream_t stream)
     if (cudaStreamSynchronize(stream) != cudaSuccess) return GM_ERR_CUDA;
     unsigned flag = 0;
     if (cudaMemcpyFromSymbol(&flag, gm::g_error_flag, sizeof(flag)) != cudaSuccess) return GM_ERR_CUDA;
-    if (flag == 0) return GM_OK;
     const unsigned zero = 0;
-    if (cudaMemcpyToSymbol(gm::g_error_flag, &zero, sizeof(zero)) != cudaSuccess) return GM_ERR_CUDA;
+    if (flag != 0 && cudaMemcpyToSymbol(gm::g_error_flag, &zero, sizeof(zero)) != cudaSuccess) return GM_ERR_CUDA;
+    unsigned attn = 0;
+    if (!gm_attn_take_errors(&attn)) return GM_ERR_CUDA;
+    flag |= attn;
+    if (flag == 0) return GM_OK;
     if (flag & gm::ERR_WAIT_TIMEOUT) return GM_ERR_WAIT_TIMEOUT;
     return (flag & gm::ERR_EDGE_INVALID) ? GM_ERR_EDGE_INVALID : GM_ERR_INDEX_RANGE;
 }

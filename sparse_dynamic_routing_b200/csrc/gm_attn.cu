@@ -1,0 +1,311 @@
+// gm_attn.cu - host side of the windowed-attention and 8-bit-cache calls of include/gm.h:
+// argument checks, choice of the kernel, launch on the caller's stream. A translation unit of
+// its own so that it compiles beside gm_api.cu.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gm.h"
+#include "gm_common.cuh"
+#include "gm_host.cuh"
+#include "gm_kv8.cuh"
+#include "gm_window.cuh"
+
+#ifndef GM_CHECKED
+#define GM_CHECKED 0
+#endif
+
+bool gm_attn_take_errors(unsigned *flag)
+{
+    if (cudaMemcpyFromSymbol(flag, gm::g_error_flag, sizeof(*flag)) != cudaSuccess) return false;
+    const unsigned zero = 0;
+    return *flag == 0 || cudaMemcpyToSymbol(gm::g_error_flag, &zero, sizeof(zero)) == cudaSuccess;
+}
+
+namespace {
+
+template <typename F> bool raise_smem(F kern, size_t bytes)
+{
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+// ---- windowed attention -------------------------------------------------------------------------
+
+gm_status check_window(gm_dtype dtype, int B, int n, int hq, int hkv, int d, int window, int sinks, float scale)
+{
+    if (B < 0 || n < 0 || hq < 1 || hkv < 1 || d < 1 || hq % hkv != 0) return GM_ERR_INVALID_ARG;
+    if (window < 1 || sinks < 0 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (dtype != GM_F32 && dtype != GM_BF16) return GM_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
+    if (n >= (1 << 30) || (int64_t)B * n >= MAX_ROWS || (int64_t)B * n * hq >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    return GM_OK;
+}
+
+gm::WinArgs window_args(int B, int n, int hq, int hkv, int window, int sinks, float scale, const int32_t *lens)
+{
+    gm::WinArgs a{};
+    a.B = B;
+    a.n = n;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.G = hq / hkv;
+    a.window = std::min(window, n);
+    a.sinks = std::min(sinks, n);
+    a.scale = scale;
+    a.lens = lens;
+    return a;
+}
+
+template <typename T, int D> gm_status window_forward(gm::WinArgs a, cudaStream_t st)
+{
+    constexpr size_t smem = gm::WinF32<D>::fwd_smem;
+    auto kern = gm::win_fwd_f32_kernel<T, D>;
+    if (!raise_smem(kern, smem)) return GM_ERR_CUDA;
+    a.nblk = (a.n + gm::WT - 1) / gm::WT;
+    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
+    return launched();
+}
+
+template <typename T, int D> gm_status window_backward(gm::WinArgs a, cudaStream_t st)
+{
+    constexpr size_t smem = gm::WinF32<D>::bwd_smem;
+    auto kq = gm::win_dq_f32_kernel<T, D>;
+    auto kkv = gm::win_dkv_f32_kernel<T, D>;
+    if (!raise_smem(kq, smem) || !raise_smem(kkv, smem)) return GM_ERR_CUDA;
+    a.nblk = (a.n + gm::WT - 1) / gm::WT;
+    gm::win_delta_kernel<T, D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
+    kq<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
+    kkv<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, smem, st>>>(a);
+    return launched();
+}
+
+// ---- 8-bit cache -----------------------------------------------------------------------------------
+
+gm_status check_cache(gm::Kv8 &c, void *kq, void *vq, float *kscale, float *vscale, int num_pages, int page,
+                      const int32_t *table, int max_pages, const int32_t *lens, int B, int t, int heads, int hkv, int d,
+                      gm_dtype dtype)
+{
+    if (B < 0 || t < 0 || heads < 1 || hkv < 1 || d < 1 || heads % hkv != 0) return GM_ERR_INVALID_ARG;
+    if (num_pages < 0 || max_pages < 0 || page < 1) return GM_ERR_INVALID_ARG;
+    if (dtype != GM_F32 && dtype != GM_BF16) return GM_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
+    if (page != 16 && page != 32 && page != 64 && page != 128) return GM_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page >= MAX_ROWS || (int64_t)B * t * heads >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    if ((int64_t)B * t == 0) return GM_OK;
+    if (!lens || (max_pages > 0 && !table)) return GM_ERR_INVALID_ARG;
+    if (num_pages > 0 && (!kq || !vq || !kscale || !vscale)) return GM_ERR_INVALID_ARG;
+    if (!aligned16(kq) || !aligned16(vq)) return GM_ERR_INVALID_ARG;
+    c.kq = (uint8_t *)kq;
+    c.vq = (uint8_t *)vq;
+    c.kscale = kscale;
+    c.vscale = vscale;
+    c.table = table;
+    c.lens = lens;
+    c.num_pages = num_pages;
+    c.max_pages = num_pages > 0 ? max_pages : 0;  // an empty pool holds no token
+    c.shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+    return GM_OK;
+}
+
+template <typename T, int D> gm_status kv8_append(const gm::Kv8AppendArgs &a, unsigned grid, cudaStream_t st)
+{
+    switch (a.c.shift) {
+    case 4: gm::kv8_append_kernel<T, D, 16><<<grid, 256, 0, st>>>(a); break;
+    case 5: gm::kv8_append_kernel<T, D, 32><<<grid, 256, 0, st>>>(a); break;
+    case 6: gm::kv8_append_kernel<T, D, 64><<<grid, 256, 0, st>>>(a); break;
+    default: gm::kv8_append_kernel<T, D, 128><<<grid, 256, 0, st>>>(a); break;
+    }
+    return launched();
+}
+
+template <typename T, int D, int NT, int W>
+gm_status launch_kv8_attention(const gm::Kv8AttnArgs &a, int64_t items, int cl, cudaStream_t st)
+{
+    using Smem = gm::Kv8Smem<D, NT, sizeof(T) == 4, W>;
+    auto kern = gm::kv8_attention_kernel<T, D, NT, W>;
+    if (!raise_smem(kern, sizeof(Smem))) return GM_ERR_CUDA;
+    if (cl > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return GM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * cl));
+    cfg.blockDim = dim3(W * 32);
+    cfg.dynamicSmemBytes = sizeof(Smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cl;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    (void)cudaLaunchKernelEx(&cfg, kern, a);
+    return launched();
+}
+
+template <typename T, int D> gm_status kv8_attention(gm::Kv8AttnArgs a, int B, int64_t keys, cudaStream_t st)
+{
+    const int64_t flat = (int64_t)a.t * a.G;
+    const int nt = flat <= 8 ? 1 : 2;
+    a.tiles = (int)((flat + 8 * nt - 1) / (8 * nt));
+    const int64_t items = (int64_t)B * a.hkv * a.tiles;
+    // warps per row tile: about 12 per SM over all tiles, each with at least two pieces of keys
+    const int64_t most = std::max<int64_t>(1, (keys + 31) / 32);
+    const int64_t want = std::min<int64_t>((148 * 12 + items - 1) / items, most);
+    const int W = want > 64 ? 16 : 4;
+    int cl = 1;
+    while (cl < 16 && (int64_t)cl * W < want) cl *= 2;
+    if (items * cl >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    if (nt == 1) return W == 4 ? launch_kv8_attention<T, D, 1, 4>(a, items, cl, st) : launch_kv8_attention<T, D, 1, 16>(a, items, cl, st);
+    return W == 4 ? launch_kv8_attention<T, D, 2, 4>(a, items, cl, st) : launch_kv8_attention<T, D, 2, 16>(a, items, cl, st);
+}
+
+template <typename T, int D> gm_status kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((a.rows + 3) / 4);
+    if (a.G == 1)
+        gm::kv8_sea_kernel<T, D, 1><<<grid, 128, 0, st>>>(a, GM_CHECKED);
+    else
+        gm::kv8_sea_kernel<T, D, 2><<<grid, 128, 0, st>>>(a, GM_CHECKED);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+gm_status gm_window_attention_forward(const void *q, const void *k, const void *v, gm_dtype dtype, const int32_t *lens,
+                                      int B, int n, int hq, int hkv, int d, int window, int sinks, float scale,
+                                      void *o, float *lse, cudaStream_t stream)
+{
+    const gm_status st = check_window(dtype, B, n, hq, hkv, d, window, sinks, scale);
+    if (st != GM_OK || (int64_t)B * n == 0) return st;
+    if (!q || !k || !v || !o) return GM_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    gm::WinArgs a = window_args(B, n, hq, hkv, window, sinks, scale, lens);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = o;
+    a.lse = lse;
+    if (dtype == GM_F32) return d == 64 ? window_forward<float, 64>(a, stream) : window_forward<float, 128>(a, stream);
+    return d == 64 ? window_forward<__nv_bfloat16, 64>(a, stream) : window_forward<__nv_bfloat16, 128>(a, stream);
+}
+
+size_t gm_window_attention_backward_workspace_size(int B, int n, int hq)
+{
+    if (B < 1 || n < 1 || hq < 1) return 0;
+    return ((size_t)B * n * hq * 4 + 15) / 16 * 16;
+}
+
+gm_status gm_window_attention_backward(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                                       const float *lse, gm_dtype dtype, const int32_t *lens, int B, int n, int hq,
+                                       int hkv, int d, int window, int sinks, float scale, void *dq, void *dk, void *dv,
+                                       void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const gm_status st = check_window(dtype, B, n, hq, hkv, d, window, sinks, scale);
+    if (st != GM_OK || (int64_t)B * n == 0) return st;
+    if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace) return GM_ERR_INVALID_ARG;
+    for (const void *p : {q, k, v, o, dout, (const void *)dq, (const void *)dk, (const void *)dv, (const void *)workspace})
+        if (!aligned16(p)) return GM_ERR_INVALID_ARG;
+    if (workspace_bytes < gm_window_attention_backward_workspace_size(B, n, hq)) return GM_ERR_INVALID_ARG;
+    gm::WinArgs a = window_args(B, n, hq, hkv, window, sinks, scale, lens);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o_in = o;
+    a.dout = dout;
+    a.lse_in = lse;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.delta = (float *)workspace;
+    if (dtype == GM_F32) return d == 64 ? window_backward<float, 64>(a, stream) : window_backward<float, 128>(a, stream);
+    return d == 64 ? window_backward<__nv_bfloat16, 64>(a, stream) : window_backward<__nv_bfloat16, 128>(a, stream);
+}
+
+gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int t, int hkv, int d, void *kq, void *vq,
+                        float *kscale, float *vscale, int num_pages, int page, const int32_t *table, int max_pages,
+                        const int32_t *lens, const int32_t *new_lens, cudaStream_t stream)
+{
+    gm::Kv8AppendArgs a{};
+    const gm_status st = check_cache(a.c, kq, vq, kscale, vscale, num_pages, page, table, max_pages, lens, B, t, hkv, hkv,
+                                     d, dtype);
+    if (st != GM_OK || (int64_t)B * t == 0) return st;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return GM_ERR_INVALID_ARG;
+    a.k = k;
+    a.v = v;
+    a.new_lens = new_lens;
+    a.B = B;
+    a.t = t;
+    a.hkv = hkv;
+    a.touch = (int)(((int64_t)t + page - 2) / page + 1);
+    const int64_t grid = (int64_t)B * a.touch * hkv * 2;
+    if (grid >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    if (dtype == GM_F32)
+        return d == 64 ? kv8_append<float, 64>(a, (unsigned)grid, stream) : kv8_append<float, 128>(a, (unsigned)grid, stream);
+    return d == 64 ? kv8_append<__nv_bfloat16, 64>(a, (unsigned)grid, stream)
+                   : kv8_append<__nv_bfloat16, 128>(a, (unsigned)grid, stream);
+}
+
+gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, int hq, int hkv, int d, const void *kq,
+                                   const void *vq, const float *kscale, const float *vscale, int num_pages, int page,
+                                   const int32_t *table, int max_pages, const int32_t *lens, const int32_t *q_lens,
+                                   int window, int sinks, float scale, void *o, float *lse, cudaStream_t stream)
+{
+    gm::Kv8AttnArgs a{};
+    const gm_status st = check_cache(a.c, const_cast<void *>(kq), const_cast<void *>(vq), const_cast<float *>(kscale),
+                                     const_cast<float *>(vscale), num_pages, page, table, max_pages, lens, B, t, hq, hkv,
+                                     d, dtype);
+    if (window < 1 || sinks < 0 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (st != GM_OK || (int64_t)B * t == 0) return st;
+    if (!q || !o || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    a.q = q;
+    a.q_lens = q_lens;
+    a.o = o;
+    a.lse = lse;
+    a.t = t;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.G = hq / hkv;
+    const int64_t room = (int64_t)a.c.max_pages * page;
+    a.window = (int)std::min<int64_t>(window, std::max<int64_t>(room, 1));
+    a.sinks = (int)std::min<int64_t>(sinks, room);
+    a.sl2 = scale * gm::LOG2E;
+    const int64_t keys = std::min<int64_t>(room, (int64_t)a.window + a.sinks);
+    if (dtype == GM_F32)
+        return d == 64 ? kv8_attention<float, 64>(a, B, keys, stream) : kv8_attention<float, 128>(a, B, keys, stream);
+    return d == 64 ? kv8_attention<__nv_bfloat16, 64>(a, B, keys, stream)
+                   : kv8_attention<__nv_bfloat16, 128>(a, B, keys, stream);
+}
+
+gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, const float *w, int s, int B, int t,
+                             int hq, int hkv, int d, const void *kq, const void *vq, const float *kscale,
+                             const float *vscale, int num_pages, int page, const int32_t *table, int max_pages,
+                             const int32_t *lens, const int32_t *q_lens, float scale, void *o, float *lse,
+                             cudaStream_t stream)
+{
+    gm::Kv8SeaArgs a{};
+    const gm_status st = check_cache(a.c, const_cast<void *>(kq), const_cast<void *>(vq), const_cast<float *>(kscale),
+                                     const_cast<float *>(vscale), num_pages, page, table, max_pages, lens, B, t, hq, hkv,
+                                     d, dtype);
+    if (s < 1 || s > 32 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (st != GM_OK || (int64_t)B * t == 0) return st;
+    if (!q || !o || !idx || !w || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    a.q = q;
+    a.idx = idx;
+    a.w = w;
+    a.q_lens = q_lens;
+    a.o = o;
+    a.lse = lse;
+    a.t = t;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.G = hq / hkv;
+    a.s = s;
+    a.rows = (int64_t)B * t * hkv;
+    a.scale = scale;
+    if (dtype == GM_F32) return d == 64 ? kv8_sea<float, 64>(a, stream) : kv8_sea<float, 128>(a, stream);
+    return d == 64 ? kv8_sea<__nv_bfloat16, 64>(a, stream) : kv8_sea<__nv_bfloat16, 128>(a, stream);
+}
+
+}  // extern "C"

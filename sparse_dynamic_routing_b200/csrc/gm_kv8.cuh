@@ -1,0 +1,730 @@
+// gm_kv8.cuh - a paged key/value cache held in 8 bits, and the attention that reads it.
+//
+// Pages kq, vq [num_pages, hkv, page, D] hold e4m3 values; kscale, vscale [num_pages, hkv] one
+// fp32 scale per (page, KV head): an element stands for value * scale. Scales are powers of
+// two, 2^e with the smallest e >= -100 such that the block's largest magnitude is at most
+// 448 * 2^e (448: the largest e4m3 value), so dividing by one is exact and an element is off by
+// e4m3's own half step and nothing else. A block that was given a non-finite value has the
+// scale NaN, and so has everything that reads it.
+//
+// table [B, max_pages] lists each sequence's pages in order. Token p of sequence b is row
+// p % page of page table[b, p / page].
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "gm_common.cuh"
+
+namespace gm {
+
+struct Kv8 {
+    uint8_t *kq, *vq;
+    float *kscale, *vscale;
+    const int32_t *table;  // [B, max_pages]
+    const int32_t *lens;   // [B]
+    int num_pages, max_pages, shift;  // page = 1 << shift tokens
+};
+
+constexpr int KV8_MIN_EXP = -100;
+
+// The smallest power of two (exponent at least KV8_MIN_EXP) that 448 times is not below amax,
+// from amax's fp32 bits; NaN for infinities and NaN. 448 = 1.75 * 2^8, so a significand above
+// 1.75 (fraction bits above 0x600000) takes the next power.
+__device__ __forceinline__ float kv8_scale(uint32_t amax_bits)
+{
+    if (amax_bits >= 0x7f800000u) return __uint_as_float(0x7fffffffu);
+    const int e = (int)(amax_bits >> 23) - 127 - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(e, KV8_MIN_EXP) + 127) << 23);
+}
+
+// Four fp32 values to four e4m3 bytes, round to nearest even (callers pass at most 448).
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+
+// ---- appending tokens ---------------------------------------------------------------------------
+//
+// One block per (sequence, touched page, KV head, K or V). The page's new rows stay in registers
+// between the pass that finds their largest magnitude and the pass that rounds them, so every
+// new element is read once and written once: the kernel moves what it must (bound by HBM; for
+// single tokens by launch latency). When a partly filled page's scale grows, its older bytes
+// are rounded again at the new scale.
+
+struct Kv8AppendArgs {
+    Kv8 c;
+    const void *k, *v;        // [B, t, hkv, D]
+    const int32_t *new_lens;  // [B] rows of each sequence that are its own, or null: t each
+    int B, t, hkv, touch;     // touch: pages a sequence may touch
+};
+
+template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv8_append_kernel(Kv8AppendArgs a)
+{
+    constexpr int VEC = Vec<T>::N, C = D / VEC;       // 16-byte chunks per row
+    constexpr int NCH = (PAGE * C + 255) / 256;       // chunks per thread
+    __shared__ uint32_t samax[8];
+    const int kv = blockIdx.x & 1;
+    unsigned x = blockIdx.x >> 1;
+    const int h = (int)(x % (unsigned)a.hkv);
+    x /= (unsigned)a.hkv;
+    const int jp = (int)(x % (unsigned)a.touch), b = (int)(x / (unsigned)a.touch);
+    const int have = __ldg(a.c.lens + b);
+    const int n = a.new_lens ? min(max(__ldg(a.new_lens + b), 0), a.t) : a.t;
+    if (n == 0) return;
+    if (have < 0) {
+        if (threadIdx.x == 0) raise_index_error();
+        return;
+    }
+    const int pg = (have >> a.c.shift) + jp;  // page of the sequence, and its rows this call writes
+    const int64_t first = (int64_t)pg << a.c.shift;
+    const int r0 = (int)max((int64_t)have - first, (int64_t)0);
+    const int r1 = (int)min((int64_t)have + n - first, (int64_t)PAGE);
+    if (r1 <= r0) return;
+    int id = -1;
+    if (pg < a.c.max_pages) id = __ldg(a.c.table + (size_t)b * a.c.max_pages + pg);
+    if (id < 0 || id >= a.c.num_pages) {
+        if (threadIdx.x == 0) raise_index_error();
+        return;
+    }
+    const size_t blk = (size_t)id * a.hkv + h;
+    // row r of the page is new token first + r - have
+    const T *src = (const T *)(kv ? a.v : a.k) + (((size_t)b * a.t + (size_t)(first - have + r0)) * a.hkv + h) * D;
+    uint4 u[NCH];
+    uint32_t amax = 0;
+    const int nch = (r1 - r0) * C;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int ch = threadIdx.x + 256 * i, r = ch / C;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (ch < nch) u[i] = ld16_stream(src + (size_t)r * a.hkv * D + (ch - r * C) * VEC);
+    }
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        float f[VEC];
+        unpack<T>(u[i], f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
+    }
+    amax = __reduce_max_sync(FULL, amax);
+    if ((threadIdx.x & 31) == 0) samax[threadIdx.x >> 5] = amax;
+    float *scales = kv ? a.c.vscale : a.c.kscale;
+    const float old = r0 > 0 ? scales[blk] : 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, samax[i]);
+    float scale = kv8_scale(amax);
+    // an older block keeps its scale unless the new rows need a larger one (NaN stays)
+    if (r0 > 0 && !(scale > old) && scale == scale) scale = old;
+    if (r0 > 0 && old != old) scale = old;
+    if (threadIdx.x == 0) scales[blk] = scale;
+    uint8_t *dst = (kv ? a.c.vq : a.c.kq) + blk * ((size_t)PAGE * D);
+    if (r0 > 0 && scale != old && scale == scale) {
+        const float f = old / scale;  // a power of two
+        for (int ch = threadIdx.x; ch < r0 * D / 16; ch += 256) {
+            uint4 w = *(reinterpret_cast<uint4 *>(dst) + ch);
+            uint32_t *wp = &w.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 lo = from_e4m3x2(wp[e] & 0xffffu), hi = from_e4m3x2(wp[e] >> 16);
+                wp[e] = to_e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+            }
+            *(reinterpret_cast<uint4 *>(dst) + ch) = w;
+        }
+    }
+    const float inv = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int ch = threadIdx.x + 256 * i;
+        if (ch < nch) {
+            float f[VEC];
+            unpack<T>(u[i], f);
+            uint32_t w[VEC / 4];
+#pragma unroll
+            for (int e = 0; e < VEC / 4; ++e)
+                w[e] = to_e4m3x4(f[4 * e] * inv, f[4 * e + 1] * inv, f[4 * e + 2] * inv, f[4 * e + 3] * inv);
+            uint8_t *p = dst + (size_t)r0 * D + (size_t)ch * VEC;  // rows of a block are contiguous
+            if constexpr (VEC == 8)
+                *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t *>(p) = w[0];
+        }
+    }
+}
+
+// ---- attention over the cache ---------------------------------------------------------------------
+//
+// Query row x < q_lens[b] of sequence b stands at position lens[b] - q_lens[b] + x and sees the
+// cached tokens that the windowed attention's rule allows (t <= i, i - t < window or t < sinks).
+//
+// A call reads every visible byte of K and V once, so HBM bounds it. One row tile (up to
+// 8 NT query rows of one KV head: the group's heads times the sequence's rows) is worked on by
+// CL blocks of one cluster and their warps; each warp takes every (CL * warps)-th piece of 16
+// keys, keeps its own softmax maximum and sum, and the partial outputs are joined in shared
+// memory, across the cluster through distributed shared memory: one launch, no workspace, and
+// a fixed order of additions.
+//
+// Arithmetic. mma.sync m16n8k16 with fp16 operands and fp32 sums, computed transposed
+// (S^T = K q^T, O^T = V^T P^T) so that the 16-row operand is the cache and a single token's few
+// query rows fill an 8-column operand. The bytes go from global memory to registers in the
+// order the operands want (any permutation of d, and of the output's columns, is as good) and
+// become fp16 with shifts: an e4m3 byte moved under fp16's exponent is the value times 2^-8,
+// exactly, subnormals included. Query rows are scaled by a power of two into fp16's upper range
+// (bf16's 8 bits fit its 11; what falls below fp16's subnormals is 2^-38 of the row's largest
+// element), probabilities by 2^14 likewise. The fp16 rounding of a probability (2^-12) lies below the bf16
+// rounding of the output (2^-9). fp32 queries and probabilities are split in two fp16 terms,
+// which leaves 2^-22.
+
+struct Kv8AttnArgs {
+    Kv8 c;
+    const void *q;          // [B, t, hq, D]
+    const int32_t *q_lens;  // [B] or null: t each
+    void *o;                // [B, t, hq, D]
+    float *lse;             // [B, t, hq] or null
+    int t, hq, hkv, G, tiles;  // row tiles per (sequence, KV head)
+    int window, sinks;
+    float sl2;              // scale * log2(e)
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two e4m3 bytes of the pair (x, y), chosen by a byte selector whose nibbles 1 and 3 name them,
+// as fp16 values times 2^-8.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x, uint32_t y, uint32_t sel)
+{
+    const uint32_t w = __byte_perm(x, y, sel);
+    return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float x, float y)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// x and y less the fp16 values packed in `hi`
+__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t hi)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+    return pack_half2(x - f.x, y - f.y);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// A float of another block of the cluster, at the same shared-memory address as here.
+__device__ __forceinline__ float peer_float(const float *p, uint32_t rank)
+{
+    float v;
+    asm volatile(
+        "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
+        : "=f"(v)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+template <int D, int NT, bool SPLIT, int W> struct Kv8Smem {
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int QTERMS = SPLIT ? 2 : 1;
+    __half q[QTERMS][ROWS][D + 8];           // rows 4 banks apart
+    float qscale[ROWS];                      // score factor of a row (powers of two undone)
+    int pos[ROWS];                           // position, -1: no such row
+    float m[W][ROWS], l[W][ROWS];
+    float part[W][ROWS][D + 4];      // the warps' outputs
+    float cm[ROWS], cl[ROWS];                // the block's
+};
+
+template <typename T, int D, int NT, int W>
+__global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
+{
+    constexpr bool SPLIT = sizeof(T) == 4;
+    using Smem = Kv8Smem<D, NT, SPLIT, W>;
+    constexpr int ROWS = Smem::ROWS;
+    constexpr int KS = D / 16;            // k steps of the scores
+    constexpr int NK = D / 64;            // 16-byte chunks of a key row per lane
+    constexpr int VW = D / 32;            // 4-byte words of a value row per lane
+    extern __shared__ __align__(16) unsigned char kv8_smem[];
+    Smem &sm = *reinterpret_cast<Smem *>(kv8_smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;
+    const uint32_t rank = cluster_rank(), ncl = cluster_size();
+    unsigned x = blockIdx.x / ncl;
+    const int rt = (int)(x % (unsigned)a.tiles);
+    x /= (unsigned)a.tiles;
+    const int h = (int)(x % (unsigned)a.hkv), b = (int)(x / (unsigned)a.hkv);
+
+    int len = __ldg(a.c.lens + b);
+    const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
+    if (len < 0 || len > room) {
+        if (threadIdx.x == 0 && rank == 0) raise_index_error();
+        len = len < 0 ? 0 : (int)room;
+    }
+    const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
+    const int nrows = min(a.t * a.G - rt * ROWS, ROWS);  // rows of this tile that the tensors have
+
+    // ---- query rows to shared memory, scaled into fp16 ------------------------------------
+    for (int r = warp; r < ROWS; r += W) {
+        const int f = rt * ROWS + r, xq = f / a.G, hq = h * a.G + f - xq * a.G;
+        const int pos = r < nrows && xq < ql ? len - ql + xq : -1;
+        constexpr int PER = D / 32;
+        float v[PER];
+        float big = 0.0f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) v[e] = 0.0f;
+        if (pos >= 0) {
+            const T *q = (const T *)a.q + (((size_t)b * a.t + xq) * a.hq + hq) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) v[e] = (float)q[e];
+        }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) big = fmaxf(big, fabsf(v[e]));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, s));
+        // 2^(14 - exponent of the largest), the exponent held in [-100, 127]
+        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(127 + 14 - min(e2, 127)) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - 14 + min(e2, 127)) << 23);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const __half hi = __float2half_rn(v[e] * up);
+            sm.q[0][r][lane * PER + e] = hi;
+            if constexpr (SPLIT) sm.q[1][r][lane * PER + e] = __float2half_rn(v[e] * up - __half2float(hi));
+        }
+        if (lane == 0) {
+            sm.qscale[r] = down * 256.0f * a.sl2;  // 2^8: the bytes' fp16 form
+            sm.pos[r] = pos;
+        }
+    }
+    __syncthreads();
+
+    // ---- the pieces of 16 keys that some row sees --------------------------------------------
+    // rows are in ascending position, so the first and last of the tile bound them
+    const int xa = rt * ROWS / a.G, xb = min((rt * ROWS + nrows - 1) / a.G, ql - 1);
+    const int pmin = max(len - ql + xa, 0), pmax = len - ql + xb;
+    int na = 0, p0 = 0, np = 0;
+    if (xa <= xb && pmax >= 0) {
+        const int lo = max(0, pmin - a.window + 1);
+        p0 = lo >> 4;
+        na = min((min(a.sinks, lo) + 15) >> 4, p0);
+        np = na + (pmax >> 4) + 1 - p0;
+    }
+    const int stride = (int)ncl * W;
+    const size_t row_bytes = (size_t)D;
+
+    int mypos[NT][2];
+    float myq[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            mypos[n][e] = sm.pos[n * 8 + 2 * c + e];
+            myq[n][e] = sm.qscale[n * 8 + 2 * c + e];
+        }
+    float m[NT][2], mv[NT][2], l[NT][2];
+    float acc[NT][D / 16][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, mv[n][e] = -INFINITY, l[n][e] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][j][e] = 0.0f;
+    }
+
+    const auto piece = [&](int i) { return i < na ? i : p0 + i - na; };
+    bool bad = false;
+    const auto page_of = [&](int i) {  // a page outside the pool is read as page 0 and raises the flag
+        if (i >= np) return 0;
+        const int id = __ldg(a.c.table + (size_t)b * a.c.max_pages + ((piece(i) << 4) >> a.c.shift));
+        if (id >= 0 && id < a.c.num_pages) return id;
+        bad = true;
+        return 0;
+    };
+    uint4 kr[2][NK];      // two keys (g, g + 8), this lane's chunks
+    uint32_t vr[4][VW];   // keys 2c, 2c+1, 2c+8, 2c+9
+    float ksc = 0.0f, vsc = 0.0f;
+    const auto where = [&](int i, int id) {  // offset of the piece's first row, in rows
+        const int t0 = piece(i) << 4;
+        return (((size_t)id * a.hkv + h) << a.c.shift) + (size_t)(t0 & ((1 << a.c.shift) - 1));
+    };
+    const auto load_k = [&](int i, int id) {
+        const uint8_t *p = a.c.kq + where(i, id) * row_bytes + c * 16;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int e = 0; e < NK; ++e) kr[s][e] = ld16_stream(p + (size_t)(g + 8 * s) * D + e * 64);
+        ksc = __ldg(a.c.kscale + (size_t)id * a.hkv + h);
+    };
+    const auto load_v = [&](int i, int id) {
+        const uint8_t *p = a.c.vq + where(i, id) * row_bytes + g * (D / 8);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint8_t *pr = p + (size_t)(2 * c + (s & 1) + 8 * (s >> 1)) * D;
+            if constexpr (VW == 4) {
+                const uint4 u = ld16_stream(pr);
+                vr[s][0] = u.x, vr[s][1] = u.y, vr[s][2] = u.z, vr[s][3] = u.w;
+            } else {
+                const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(pr));
+                vr[s][0] = u.x, vr[s][1] = u.y;
+            }
+        }
+        vsc = __ldg(a.c.vscale + (size_t)id * a.hkv + h);
+    };
+
+    int i = (int)rank * W + warp;
+    int id = page_of(i), id_next = page_of(i + stride);
+    if (i < np) {
+        load_k(i, id);
+        load_v(i, id);
+    }
+    for (; i < np; i += stride) {
+        const int t0 = piece(i) << 4;
+        // S^T = K q^T
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const uint32_t w0 = (&kr[0][ks >> 2].x)[ks & 3], w1 = (&kr[1][ks >> 2].x)[ks & 3];
+            const uint32_t a0 = e4m3_pair(w0, w0, 0x1000), a2 = e4m3_pair(w0, w0, 0x3020);
+            const uint32_t a1 = e4m3_pair(w1, w1, 0x1000), a3 = e4m3_pair(w1, w1, 0x3020);
+            const int d = (ks >> 2) * 64 + c * 16 + (ks & 3) * 4;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint2 q0 = *reinterpret_cast<const uint2 *>(&sm.q[0][n * 8 + g][d]);
+                mma_f16(s[n], a0, a1, a2, a3, q0.x, q0.y);
+                if constexpr (SPLIT) {
+                    const uint2 q1 = *reinterpret_cast<const uint2 *>(&sm.q[1][n * 8 + g][d]);
+                    mma_f16(s[n], a0, a1, a2, a3, q1.x, q1.y);
+                }
+            }
+        }
+        const float kf = ksc, vf = vsc;
+        const int nid = id_next;
+        if (i + stride < np) {  // the next piece's keys are on their way during the softmax
+            load_k(i + stride, nid);
+            id_next = page_of(i + 2 * stride);
+        }
+        // softmax of the piece: rows 2c + e, keys t0 + g and t0 + g + 8
+        const float lv = (float)((int)((__float_as_uint(vf) >> 23) & 255u) - 127);
+        uint32_t pt[NT][2], pl[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float p[4], mx[2], f[2], up[2];
+            bool see[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = t0 + g + 8 * (e >> 1), ps = mypos[n][e & 1];
+                see[e] = t <= ps && (ps - t < a.window || t < a.sinks);
+                p[e] = see[e] ? s[n][e] * (myq[n][e & 1] * kf) : -INFINITY;
+            }
+            bool moved = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mx[e] = fmaxf(p[e], p[e + 2]);
+#pragma unroll
+                for (int sft = 4; sft < 32; sft <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], sft));
+                const float mn = fmaxf(m[n][e], mx[e]), vn = fmaxf(mv[n][e], mx[e] + lv);
+                const float mb = mn == -INFINITY ? 0.0f : mn, vb = vn == -INFINITY ? 0.0f : vn;
+                l[n][e] *= ex2(m[n][e] - mb);
+                f[e] = ex2(mv[n][e] - vb);
+                moved |= vn != mv[n][e];
+                m[n][e] = mn;
+                mv[n][e] = vn;
+                mx[e] = mb;
+                up[e] = vf * ex2(mb - vb) * 0x1p14f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                p[e] = see[e] ? ex2(p[e] - mx[e & 1]) : 0.0f;
+                l[n][e & 1] += p[e];
+                p[e] = see[e] ? p[e] * up[e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
+            }
+            if (__any_sync(FULL, moved)) {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[n][j][e] *= f[e & 1];
+            }
+            const uint32_t h0 = pack_half2(p[0], p[1]), h1 = pack_half2(p[2], p[3]);
+            pt[n][0] = transpose8x8(h0);
+            pt[n][1] = transpose8x8(h1);
+            if constexpr (SPLIT) {
+                pl[n][0] = transpose8x8(pack_rest(p[0], p[1], h0));
+                pl[n][1] = transpose8x8(pack_rest(p[2], p[3], h1));
+            }
+        }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {  // output columns g * (D/8) + 2j and + 2j + 1
+            const uint32_t sel0 = (j & 1) ? 0x6020u : 0x4000u, sel1 = (j & 1) ? 0x7030u : 0x5010u;
+            const uint32_t a0 = e4m3_pair(vr[0][j >> 1], vr[1][j >> 1], sel0);
+            const uint32_t a1 = e4m3_pair(vr[0][j >> 1], vr[1][j >> 1], sel1);
+            const uint32_t a2 = e4m3_pair(vr[2][j >> 1], vr[3][j >> 1], sel0);
+            const uint32_t a3 = e4m3_pair(vr[2][j >> 1], vr[3][j >> 1], sel1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_f16(acc[n][j], a0, a1, a2, a3, pt[n][0], pt[n][1]);
+                if constexpr (SPLIT) mma_f16(acc[n][j], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+            }
+        }
+        if (i + stride < np) load_v(i + stride, nid);
+    }
+    if (bad && lane == 0) raise_index_error();
+
+    // ---- join: warps in shared memory, blocks through the cluster ---------------------------
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = n * 8 + 2 * c + e;
+#pragma unroll
+            for (int sft = 4; sft < 32; sft <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], sft);
+            if (r < nrows) {
+                // back from the values' own maximum: 2^8 of the bytes' form, 2^-14 of the weights
+                const float u = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-6f;
+                if (g == 0) {
+                    sm.m[warp][r] = m[n][e];
+                    sm.l[warp][r] = l[n][e];
+                }
+                float *dst = &sm.part[warp][r][g * (D / 8)];
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                    *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(acc[n][j][e] * u, acc[n][j][2 + e] * u);
+            }
+        }
+    __syncthreads();
+    for (int y = threadIdx.x; y < nrows * D; y += W * 32) {
+        const int r = y / D, d = y - r * D;
+        float mx = sm.m[0][r];
+#pragma unroll
+        for (int w = 1; w < W; ++w) mx = fmaxf(mx, sm.m[w][r]);
+        const float mb = mx == -INFINITY ? 0.0f : mx;
+        float o = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = ex2(sm.m[w][r] - mb);
+            o += sm.part[w][r][d] * f;
+            sum += sm.l[w][r] * f;
+        }
+        // only this thread reads or writes column d of row r; m and l are rewritten elsewhere
+        sm.part[0][r][d] = o;
+        if (d == 0) {
+            sm.cm[r] = mx;
+            sm.cl[r] = sum;
+        }
+    }
+    if (ncl > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    for (int y = (int)(rank * W * 32) + threadIdx.x; y < nrows * D; y += (int)ncl * W * 32) {
+        const int r = y / D, d = y - r * D;
+        float mx = -INFINITY;
+        for (uint32_t p = 0; p < ncl; ++p) mx = fmaxf(mx, peer_float(&sm.cm[r], p));
+        const float mb = mx == -INFINITY ? 0.0f : mx;
+        float o = 0.0f, sum = 0.0f;
+        for (uint32_t p = 0; p < ncl; ++p) {
+            const float f = ex2(peer_float(&sm.cm[r], p) - mb);
+            o += peer_float(&sm.part[0][r][d], p) * f;
+            sum += peer_float(&sm.cl[r], p) * f;
+        }
+        const int f = rt * ROWS + r, xq = f / a.G, hq = h * a.G + f - xq * a.G;
+        const size_t row = ((size_t)b * a.t + xq) * a.hq + hq;
+        const bool none = sm.pos[r] < 0;
+        const float out = none ? 0.0f : o / sum;
+        if constexpr (SPLIT)
+            ((float *)a.o)[row * D + d] = out;
+        else
+            ((__nv_bfloat16 *)a.o)[row * D + d] = __float2bfloat16_rn(out);
+        if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mx + lg2(sum)) * LN2;
+    }
+    if (ncl > 1) cluster_sync();  // the blocks' shared memory outlives its readers
+}
+
+// ---- sparse edge attention over the cache -----------------------------------------------------------
+//
+// As gm_sea_forward for the last rows of each sequence: row x has edges idx/w [B, t, hkv, s] into
+// the cached tokens, z_j = scale <q, k_{t_j}> + ln w_j, o = sum softmax(z)_j v_{t_j}. One warp per
+// (b, x, KV head): the C = D/16 lanes of a segment hold one slot's 16-byte chunks of K and V, so
+// 32 / C slots are gathered at once, each segment keeping its own softmax; the segments are
+// joined with shuffles at the end. fp32 arithmetic throughout. Bound by the gather's latency for
+// single tokens (edges -> page -> rows is a chain of three loads), by q, o and the L2 for
+// prompts.
+
+struct Kv8SeaArgs {
+    Kv8 c;
+    const void *q;
+    const int32_t *idx;
+    const float *w;
+    const int32_t *q_lens;
+    void *o;
+    float *lse;
+    int t, hq, hkv, G, s;
+    int64_t rows;  // B * t * hkv
+    float scale;
+};
+
+template <typename T, int D, int GC>
+__global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
+{
+    constexpr int C = D / 16, SEG = 32 / C;
+    constexpr int VEC = Vec<T>::N, NV = 16 / VEC;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
+    const int lane = threadIdx.x & 31, seg = lane / C, ch = lane - seg * C;
+    const int64_t bx = row / a.hkv;
+    const int h = (int)(row - bx * a.hkv);
+    const int b = (int)(bx / a.t), xq = (int)(bx - (int64_t)b * a.t);
+    int len = __ldg(a.c.lens + b);
+    const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
+    if (len < 0 || len > room) {
+        if (lane == 0) raise_index_error();
+        len = len < 0 ? 0 : (int)room;
+    }
+    const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
+    const int pos = xq < ql ? len - ql + xq : -1;
+    const int32_t *idx = a.idx + row * a.s;
+    const float *w = a.w + row * a.s;
+    for (int g0 = 0; g0 < a.G; g0 += GC) {
+        float q[GC][16], acc[GC][16], m[GC], l[GC];
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+            m[g] = -INFINITY, l[g] = 0.0f;
+            const T *src = (const T *)a.q + ((size_t)bx * a.hq + h * a.G + min(g0 + g, a.G - 1)) * D + ch * 16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) q[g][e] = 0.0f, acc[g][e] = 0.0f;
+            if (pos >= 0) {
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    float f[VEC];
+                    unpack<T>(ld16(src + e * VEC), f);
+#pragma unroll
+                    for (int y = 0; y < VEC; ++y) q[g][e * VEC + y] = f[y] * (a.scale * LOG2E);
+                }
+            }
+        }
+        for (int j0 = 0; pos >= 0 && j0 < a.s; j0 += SEG) {
+            const int j = j0 + seg;
+            float wj = 0.0f;
+            int t = 0;
+            if (j < a.s) {
+                wj = __ldg(w + j);
+                t = __ldg(idx + j);
+            }
+            int id = 0;
+            bool on = wj > 0.0f;
+            if (on) {
+                on = t >= 0 && t < len;
+                if (on) {
+                    id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
+                    on = id >= 0 && id < a.c.num_pages;
+                }
+                if (!on && ch == 0 && g0 == 0) raise_index_error();
+            }
+            if (checked && ch == 0 && g0 == 0 && j < a.s) {
+                const bool bad_w = !(wj >= 0.0f) || isinf(wj);
+                if (bad_w || (wj > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
+            }
+            uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
+            float ksc = 0.0f, vsc = 0.0f;
+            if (on) {
+                const size_t blk = (size_t)id * a.hkv + h;
+                const size_t at = ((blk << a.c.shift) + (size_t)(t & ((1 << a.c.shift) - 1))) * D + ch * 16;
+                ku = ld16(a.c.kq + at);
+                vu = ld16(a.c.vq + at);
+                ksc = __ldg(a.c.kscale + blk);
+                vsc = __ldg(a.c.vscale + blk);
+            }
+            float kf[16], vf[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 x = from_e4m3x2((&ku.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
+                const float2 y = from_e4m3x2((&vu.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
+                kf[2 * e] = x.x, kf[2 * e + 1] = x.y;
+                vf[2 * e] = y.x, vf[2 * e + 1] = y.y;
+            }
+            const float lw = on ? log2f(wj) : 0.0f;
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                float z = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z = fmaf(q[g][e], kf[e], z);
+                z = seg_sum<C>(z);
+                if (on) {
+                    z = fmaf(z, ksc, lw);
+                    const float mn = fmaxf(m[g], z);
+                    const float f = ex2(m[g] - mn), p = ex2(z - mn), pv = p * vsc;
+                    l[g] = l[g] * f + p;
+                    m[g] = mn;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[g][e] = fmaf(pv, vf[e], acc[g][e] * f);
+                }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+            float mx = m[g];
+#pragma unroll
+            for (int o = C; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+            const float f = mx == -INFINITY ? 0.0f : ex2(m[g] - mx);
+            const float sum = cross_seg_sum<C>(l[g] * f);
+            const float inv = sum > 0.0f ? 1.0f / sum : sum;  // an empty row stays 0, a NaN stays
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[g][e] = cross_seg_sum<C>(acc[g][e] * f) * inv;
+            if (seg == 0 && g0 + g < a.G) {
+                const size_t r = (size_t)bx * a.hq + h * a.G + g0 + g;
+                T *dst = (T *)a.o + r * D + ch * 16;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) {
+                    float y[VEC];
+#pragma unroll
+                    for (int z = 0; z < VEC; ++z) y[z] = acc[g][e * VEC + z];
+                    *reinterpret_cast<uint4 *>(dst + e * VEC) = pack<T>(y);
+                }
+                if (a.lse && ch == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mx + lg2(sum)) * LN2;
+            }
+        }
+    }
+}
+
+}  // namespace gm

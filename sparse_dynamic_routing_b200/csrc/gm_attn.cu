@@ -10,6 +10,7 @@
 #include "gm_host.cuh"
 #include "gm_kv8.cuh"
 #include "gm_window.cuh"
+#include "gm_window_umma.cuh"
 
 #ifndef GM_CHECKED
 #define GM_CHECKED 0
@@ -76,6 +77,57 @@ template <typename T, int D> gm_status window_backward(gm::WinArgs a, cudaStream
     gm::win_delta_kernel<T, D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
     kq<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
     kkv<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, smem, st>>>(a);
+    return launched();
+}
+
+// A bf16 feature tensor [B, n, heads, d] as a 4-d TMA map whose boxes are 64 elements of d (128
+// bytes, the swizzle width) x 1 head x 128 rows of one sequence; rows past n read as zeros and are
+// not written.
+bool sequence_tmap(CUtensorMap &m, const void *ptr, int B, int n, int heads, int d)
+{
+    const EncodeTiledFn f = encode_tiled();
+    if (f == nullptr) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n, (cuuint64_t)B};
+    const cuuint64_t row = (cuuint64_t)heads * d * 2;
+    const cuuint64_t strides[3] = {(cuuint64_t)d * 2, row, row * n};
+    const cuuint32_t box[4] = {64, 1, gm::UW, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return f(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Score factor in base 2. A scale of 0 becomes one so small that every score rounds to 0 after
+// the maximum is taken off: the kernels hide keys with an infinite score, which 0 would make NaN.
+float base2_scale(float scale)
+{
+    const float s = scale * gm::LOG2E;
+    return s == 0.0f ? 0x1p-120f : s;
+}
+
+// Pairs of 128-row tiles that share their keys (gm_window_umma.cuh).
+int64_t window_pairs(gm::WinArgs &a, gm::WinPairs &p)
+{
+    p.heads = a.G % 2 == 0;
+    p.per = p.heads ? a.B * (a.hq / 2) : a.B * a.hq;
+    const int rows = p.heads ? gm::UW : 2 * gm::UW;
+    a.nblk = (a.n + rows - 1) / rows;
+    return (int64_t)a.nblk * p.per;
+}
+
+template <int D> gm_status window_forward_bf16(gm::WinArgs a, cudaStream_t st)
+{
+    using Geo = gm::WinFwdGeom<D>;
+    CUtensorMap tq, tk, tv, to;
+    if (!sequence_tmap(tq, a.q, a.B, a.n, a.hq, D) || !sequence_tmap(tk, a.k, a.B, a.n, a.hkv, D) ||
+        !sequence_tmap(tv, a.v, a.B, a.n, a.hkv, D) || !sequence_tmap(to, a.o, a.B, a.n, a.hq, D))
+        return GM_ERR_CUDA;
+    auto kern = gm::win_fwd_umma_kernel<D>;
+    if (!raise_smem(kern, Geo::SMEM)) return GM_ERR_CUDA;
+    gm::WinPairs wp;
+    const int64_t grid = window_pairs(a, wp);
+    a.scale = base2_scale(a.scale);
+    kern<<<(unsigned)grid, Geo::THREADS, Geo::SMEM, st>>>(tq, tk, tv, to, a, wp);
     return launched();
 }
 
@@ -188,7 +240,7 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
     a.o = o;
     a.lse = lse;
     if (dtype == GM_F32) return d == 64 ? window_forward<float, 64>(a, stream) : window_forward<float, 128>(a, stream);
-    return d == 64 ? window_forward<__nv_bfloat16, 64>(a, stream) : window_forward<__nv_bfloat16, 128>(a, stream);
+    return d == 64 ? window_forward_bf16<64>(a, stream) : window_forward_bf16<128>(a, stream);
 }
 
 size_t gm_window_attention_backward_workspace_size(int B, int n, int hq)

@@ -1,6 +1,7 @@
 // gm_umma.cuh - the sm_100a tensor-core, tensor-memory and tensor-copy primitives the dense
-// refresh-edge kernel uses: tcgen05 MMA with its operands in shared memory and its accumulator
-// in tensor memory (TMEM), TMEM allocation and loads, and 3-d tiled TMA loads. Inline PTX;
+// refresh-edge and windowed-attention kernels use: tcgen05 MMA with its accumulator in tensor
+// memory (TMEM), B in shared memory and A in either, TMEM allocation, loads and stores, and 3-d
+// and 4-d tiled TMA copies. Inline PTX;
 // the descriptor layouts follow the PTX ISA's tcgen05 "shared memory descriptor" and
 // "instruction descriptor" tables (the bit positions are checked on the host against
 // CUTLASS's definitions by tests/test_umma_desc.py).
@@ -33,7 +34,31 @@ __host__ __device__ constexpr uint64_t sdesc_sw128_kmajor(uint32_t smem_addr)
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The same descriptor with B held MN-major (bit 16): B's N runs along the contiguous dimension.
+__host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
+
+// Shared-memory matrix descriptor of an MN-major operand in the 128-byte swizzle layout: rows of
+// 128 bytes hold 64 bf16 along M/N, one row per K index, eight-row groups of 1024 bytes stacked
+// along K. Leading byte offset: from one 64-element block of M/N to the next; stride byte
+// offset: between eight-row groups. A K step of 16 rows advances the start address by 2048 bytes.
+__host__ __device__ constexpr uint64_t sdesc_sw128_mnmajor(uint32_t smem_addr, uint32_t block_bytes)
+{
+    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
 #if defined(__CUDACC__)
+
+// A in TMEM: lane = row of A, 32-bit column c = the bf16 pair (2c, 2c + 1) along K.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
 
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          bool accumulate)
@@ -85,6 +110,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr)
         : "memory");
 }
+// 32 consecutive 32-bit columns of this thread's TMEM lane written; completes at tmem_wait_st.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 
 // Tiled 3-d TMA load of one box into shared memory, completion counted on `bar`. The innermost
@@ -97,6 +145,30 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+
+// Tiled 4-d TMA load of one box into shared memory, completion counted on `bar`; elements outside
+// the tensor become zeros.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+// Tiled 4-d TMA store of one box from shared memory (elements outside the tensor are not
+// written), its commit, and the wait until the committed stores have read their sources.
+__device__ __forceinline__ void tma_store_4d(const void *tmap, uint32_t src, int x, int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+// Makes this thread's shared-memory writes visible to the asynchronous proxy (TMA, tensor cores).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
 #endif  // __CUDACC__
 

@@ -10,6 +10,7 @@
 #include "gm_host.cuh"
 #include "gm_kv8.cuh"
 #include "gm_window.cuh"
+#include "gm_window_bwd_umma.cuh"
 #include "gm_window_umma.cuh"
 
 #ifndef GM_CHECKED
@@ -57,24 +58,24 @@ gm::WinArgs window_args(int B, int n, int hq, int hkv, int window, int sinks, fl
     return a;
 }
 
-template <typename T, int D> gm_status window_forward(gm::WinArgs a, cudaStream_t st)
+template <int D> gm_status window_forward(gm::WinArgs a, cudaStream_t st)
 {
     constexpr size_t smem = gm::WinF32<D>::fwd_smem;
-    auto kern = gm::win_fwd_f32_kernel<T, D>;
+    auto kern = gm::win_fwd_f32_kernel<D>;
     if (!raise_smem(kern, smem)) return GM_ERR_CUDA;
     a.nblk = (a.n + gm::WT - 1) / gm::WT;
     kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
     return launched();
 }
 
-template <typename T, int D> gm_status window_backward(gm::WinArgs a, cudaStream_t st)
+template <int D> gm_status window_backward(gm::WinArgs a, cudaStream_t st)
 {
     constexpr size_t smem = gm::WinF32<D>::bwd_smem;
-    auto kq = gm::win_dq_f32_kernel<T, D>;
-    auto kkv = gm::win_dkv_f32_kernel<T, D>;
+    auto kq = gm::win_dq_f32_kernel<D>;
+    auto kkv = gm::win_dkv_f32_kernel<D>;
     if (!raise_smem(kq, smem) || !raise_smem(kkv, smem)) return GM_ERR_CUDA;
     a.nblk = (a.n + gm::WT - 1) / gm::WT;
-    gm::win_delta_kernel<T, D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
+    gm::win_delta_kernel<D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
     kq<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
     kkv<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, smem, st>>>(a);
     return launched();
@@ -128,6 +129,34 @@ template <int D> gm_status window_forward_bf16(gm::WinArgs a, cudaStream_t st)
     const int64_t grid = window_pairs(a, wp);
     a.scale = base2_scale(a.scale);
     kern<<<(unsigned)grid, Geo::THREADS, Geo::SMEM, st>>>(tq, tk, tv, to, a, wp);
+    return launched();
+}
+
+template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream_t st)
+{
+    using Geo = gm::WinBwdGeom<D>;
+    CUtensorMap tq, tdo, tk, tv, tdq, tdk, tdv;
+    if (!sequence_tmap(tq, w.q, w.B, w.n, w.hq, D) || !sequence_tmap(tdo, w.dout, w.B, w.n, w.hq, D) ||
+        !sequence_tmap(tk, w.k, w.B, w.n, w.hkv, D) || !sequence_tmap(tv, w.v, w.B, w.n, w.hkv, D) ||
+        !sequence_tmap(tdq, w.dq, w.B, w.n, w.hq, D) || !sequence_tmap(tdk, w.dk, w.B, w.n, w.hkv, D) ||
+        !sequence_tmap(tdv, w.dv, w.B, w.n, w.hkv, D))
+        return GM_ERR_CUDA;
+    auto kq = gm::win_dq_umma_kernel<D>;
+    auto kkv = gm::win_dkv_umma_kernel<D>;
+    if (!raise_smem(kq, Geo::SMEM) || !raise_smem(kkv, Geo::SMEM)) return GM_ERR_CUDA;
+    gm::WinBwdArgs a{};
+    a.w = w;
+    a.scale = w.scale;
+    a.w.scale = base2_scale(w.scale);
+    a.w.nblk = (w.n + gm::UW - 1) / gm::UW;
+    a.npad = a.w.nblk * gm::UW;
+    const int64_t rows = (int64_t)w.B * a.npad * w.hq;
+    float *nl = w.delta, *delta = w.delta + rows;
+    a.nl = nl;
+    a.delta = delta;
+    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(a, nl, delta);
+    kq<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hq), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdq, a);
+    kkv<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hkv), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdk, tdv, a);
     return launched();
 }
 
@@ -239,14 +268,15 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
     a.v = v;
     a.o = o;
     a.lse = lse;
-    if (dtype == GM_F32) return d == 64 ? window_forward<float, 64>(a, stream) : window_forward<float, 128>(a, stream);
+    if (dtype == GM_F32) return d == 64 ? window_forward<64>(a, stream) : window_forward<128>(a, stream);
     return d == 64 ? window_forward_bf16<64>(a, stream) : window_forward_bf16<128>(a, stream);
 }
 
 size_t gm_window_attention_backward_workspace_size(int B, int n, int hq)
 {
     if (B < 1 || n < 1 || hq < 1) return 0;
-    return ((size_t)B * n * hq * 4 + 15) / 16 * 16;
+    // two fp32 values per row of sequences padded to whole 128-row blocks
+    return (size_t)B * (((size_t)n + 127) / 128 * 128) * hq * 8;
 }
 
 gm_status gm_window_attention_backward(const void *q, const void *k, const void *v, const void *o, const void *dout,
@@ -271,8 +301,8 @@ gm_status gm_window_attention_backward(const void *q, const void *k, const void 
     a.dk = dk;
     a.dv = dv;
     a.delta = (float *)workspace;
-    if (dtype == GM_F32) return d == 64 ? window_backward<float, 64>(a, stream) : window_backward<float, 128>(a, stream);
-    return d == 64 ? window_backward<__nv_bfloat16, 64>(a, stream) : window_backward<__nv_bfloat16, 128>(a, stream);
+    if (dtype == GM_F32) return d == 64 ? window_backward<64>(a, stream) : window_backward<128>(a, stream);
+    return d == 64 ? window_backward_bf16<64>(a, stream) : window_backward_bf16<128>(a, stream);
 }
 
 gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int t, int hkv, int d, void *kq, void *vq,

@@ -89,31 +89,16 @@ template <int D> struct WinF32 {
     static constexpr size_t bwd_smem = (size_t)(4 * WT * LD + 2 * WT * WLP) * 4;
 };
 
-// Four elements of a feature row.
-__device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
-{
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ void store4(float *p, float4 f) { *reinterpret_cast<float4 *>(p) = f; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 f)
-{
-    __nv_bfloat162 x[2] = {__floats2bfloat162_rn(f.x, f.y), __floats2bfloat162_rn(f.z, f.w)};
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(x);
-}
-
 // Rows [r0, r0 + 64) of one head of a [.., heads, D] tensor into a tile; rows at or past `end`
 // (padding may hold anything) become zeros.
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float *dst, const T *src, size_t row_stride, int r0, int end)
+template <int D>
+__device__ __forceinline__ void load_tile(float *dst, const float *src, size_t row_stride, int r0, int end)
 {
     constexpr int C = D / 4;
     for (int x = threadIdx.x; x < WT * C; x += 256) {
         const int r = x / C, c = x - r * C;
         float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r0 + r < end) f = load4(src + (size_t)(r0 + r) * row_stride + c * 4);
+        if (r0 + r < end) f = __ldg(reinterpret_cast<const float4 *>(src + (size_t)(r0 + r) * row_stride) + c);
         *reinterpret_cast<float4 *>(dst + r * WinF32<D>::LD + c * 4) = f;
     }
 }
@@ -190,7 +175,7 @@ __device__ __forceinline__ float row_max(float x)
     return x;
 }
 
-template <typename T, int D> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinArgs a)
+template <int D> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinArgs a)
 {
     using S = WinF32<D>;
     constexpr int NC = S::NC;
@@ -204,9 +189,9 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_fwd_f32_
     const int b = bh / a.hq, hq = bh - b * a.hq, h = hq / a.G;
     const int len = win_len(a, b), i0 = blk * WT;
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
-    const T *q = (const T *)a.q + (size_t)b * a.n * qs + (size_t)hq * D;
-    const T *k = (const T *)a.k + (size_t)b * a.n * ks + (size_t)h * D;
-    const T *v = (const T *)a.v + (size_t)b * a.n * ks + (size_t)h * D;
+    const float *q = (const float *)a.q + (size_t)b * a.n * qs + (size_t)hq * D;
+    const float *k = (const float *)a.k + (size_t)b * a.n * ks + (size_t)h * D;
+    const float *v = (const float *)a.v + (size_t)b * a.n * ks + (size_t)h * D;
     const KeyBlocks kb(i0, WT, len, a.window, a.sinks, WT);
     const float sl2 = a.scale * LOG2E;
 
@@ -258,7 +243,7 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_fwd_f32_
         __syncwarp();  // a score row belongs to one half of a warp
         tile_accumulate<D, true>(sp, sv, ty, tx, acc);
     }
-    T *o = (T *)a.o + (size_t)b * a.n * qs + (size_t)hq * D;
+    float *o = (float *)a.o + (size_t)b * a.n * qs + (size_t)hq * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int qi = i0 + ty * 4 + i;
@@ -267,27 +252,25 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_fwd_f32_
         const float inv = qi < len ? 1.0f / sum : 0.0f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            store4(o + (size_t)qi * qs + tx * 4 + 64 * c, make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv, acc[i][c].w * inv));
+            *reinterpret_cast<float4 *>(o + (size_t)qi * qs + tx * 4 + 64 * c) =
+                make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv, acc[i][c].w * inv);
         if (a.lse && tx == 0)
             a.lse[((size_t)b * a.n + qi) * a.hq + hq] = qi < len ? m[i] * LN2 + logf(sum) : -INFINITY;
     }
 }
 
 // delta[b, hq, i] = <dout[b, i, hq], o[b, i, hq]>; one warp per row.
-template <typename T, int D> __global__ void __launch_bounds__(256) win_delta_kernel(WinArgs a)
+template <int D> __global__ void __launch_bounds__(256) win_delta_kernel(WinArgs a)
 {
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // (b, i, hq)
     const int lane = threadIdx.x & 31;
     if (row >= (int64_t)a.B * a.n * a.hq) return;
-    constexpr int VEC = Vec<T>::N, C = D / VEC;
-    const T *o = (const T *)a.o_in + row * D, *g = (const T *)a.dout + row * D;
+    constexpr int C = D / 4;
+    const float4 *o = (const float4 *)((const float *)a.o_in + row * D), *g = (const float4 *)((const float *)a.dout + row * D);
     float x = 0.0f;
     if (lane < C) {
-        float fo[VEC], fg[VEC];
-        unpack<T>(ld16(o + lane * VEC), fo);
-        unpack<T>(ld16(g + lane * VEC), fg);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x += fo[e] * fg[e];
+        const float4 fo = __ldg(o + lane), fg = __ldg(g + lane);
+        x = fo.x * fg.x + fo.y * fg.y + fo.z * fg.z + fo.w * fg.w;
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(FULL, x, s);
@@ -334,7 +317,7 @@ __device__ __forceinline__ void row_stats(const WinArgs &a, int b, int hq, int i
     }
 }
 
-template <typename T, int D> __global__ void __launch_bounds__(256) win_dq_f32_kernel(WinArgs a)
+template <int D> __global__ void __launch_bounds__(256) win_dq_f32_kernel(WinArgs a)
 {
     using S = WinF32<D>;
     constexpr int NC = S::NC;
@@ -349,8 +332,8 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_dq_f32_k
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
     const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D, ko = (size_t)b * a.n * ks + (size_t)h * D;
     const KeyBlocks kb(i0, WT, len, a.window, a.sinks, WT);
-    load_tile<D>(sq, (const T *)a.q + qo, qs, i0, len);
-    load_tile<D>(sdo, (const T *)a.dout + qo, qs, i0, len);
+    load_tile<D>(sq, (const float *)a.q + qo, qs, i0, len);
+    load_tile<D>(sdo, (const float *)a.dout + qo, qs, i0, len);
     float nl[4], dl[4];
     row_stats(a, b, hq, i0, len, ty, nl, dl);
     float4 acc[4][NC];
@@ -358,26 +341,27 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_dq_f32_k
     for (int j = 0; j < kb.na + kb.nb; ++j) {
         const int t0 = kb.start(j, WT), t1 = kb.end(j, WT);
         __syncthreads();
-        load_tile<D>(sk, (const T *)a.k + ko, ks, t0, t1);
-        load_tile<D>(sv, (const T *)a.v + ko, ks, t0, t1);
+        load_tile<D>(sk, (const float *)a.k + ko, ks, t0, t1);
+        load_tile<D>(sv, (const float *)a.v + ko, ks, t0, t1);
         __syncthreads();
         bwd_scores<D, false>(a, sq, sk, sdo, sv, nullptr, sd, i0, len, t0, t1, nl, dl, ty, tx);
         __syncwarp();
         tile_accumulate<D, true>(sd, sk, ty, tx, acc);
     }
-    T *dq = (T *)a.dq + qo;
+    float *dq = (float *)a.dq + qo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int qi = i0 + ty * 4 + i;
         if (qi >= a.n) continue;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
-            store4(dq + (size_t)qi * qs + tx * 4 + 64 * c, make_float4(
-                acc[i][c].x * a.scale, acc[i][c].y * a.scale, acc[i][c].z * a.scale, acc[i][c].w * a.scale));
+            *reinterpret_cast<float4 *>(dq + (size_t)qi * qs + tx * 4 + 64 * c) =
+                make_float4(
+                acc[i][c].x * a.scale, acc[i][c].y * a.scale, acc[i][c].z * a.scale, acc[i][c].w * a.scale);
     }
 }
 
-template <typename T, int D> __global__ void __launch_bounds__(256) win_dkv_f32_kernel(WinArgs a)
+template <int D> __global__ void __launch_bounds__(256) win_dkv_f32_kernel(WinArgs a)
 {
     using S = WinF32<D>;
     constexpr int NC = S::NC;
@@ -392,8 +376,8 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_dkv_f32_
     const int len = win_len(a, b), t0 = blk * WT, t1 = min(t0 + WT, len);
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
     const size_t ko = (size_t)b * a.n * ks + (size_t)h * D;
-    load_tile<D>(sk, (const T *)a.k + ko, ks, t0, len);
-    load_tile<D>(sv, (const T *)a.v + ko, ks, t0, len);
+    load_tile<D>(sk, (const float *)a.k + ko, ks, t0, len);
+    load_tile<D>(sv, (const float *)a.v + ko, ks, t0, len);
     float4 gk[4][NC], gv[4][NC];
     zero(gk);
     zero(gv);
@@ -403,8 +387,8 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_dkv_f32_
         const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D;
         for (int i0 = t0; i0 < qend; i0 += WT) {
             __syncthreads();
-            load_tile<D>(sq, (const T *)a.q + qo, qs, i0, len);
-            load_tile<D>(sdo, (const T *)a.dout + qo, qs, i0, len);
+            load_tile<D>(sq, (const float *)a.q + qo, qs, i0, len);
+            load_tile<D>(sdo, (const float *)a.dout + qo, qs, i0, len);
             float nl[4], dl[4];
             row_stats(a, b, hq, i0, len, ty, nl, dl);
             __syncthreads();
@@ -414,16 +398,17 @@ template <typename T, int D> __global__ void __launch_bounds__(256) win_dkv_f32_
             tile_accumulate<D, false>(sd, sq, ty, tx, gk);
         }
     }
-    T *dk = (T *)a.dk + ko, *dv = (T *)a.dv + ko;
+    float *dk = (float *)a.dk + ko, *dv = (float *)a.dv + ko;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + ty * 4 + i;
         if (t >= a.n) continue;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            store4(dk + (size_t)t * ks + tx * 4 + 64 * c, make_float4(
-                gk[i][c].x * a.scale, gk[i][c].y * a.scale, gk[i][c].z * a.scale, gk[i][c].w * a.scale));
-            store4(dv + (size_t)t * ks + tx * 4 + 64 * c, gv[i][c]);
+            *reinterpret_cast<float4 *>(dk + (size_t)t * ks + tx * 4 + 64 * c) =
+                make_float4(
+                gk[i][c].x * a.scale, gk[i][c].y * a.scale, gk[i][c].z * a.scale, gk[i][c].w * a.scale);
+            *reinterpret_cast<float4 *>(dv + (size_t)t * ks + tx * 4 + 64 * c) = gv[i][c];
         }
     }
 }

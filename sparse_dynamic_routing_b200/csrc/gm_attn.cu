@@ -172,6 +172,8 @@ gm_status check_cache(gm::Kv8 &c, void *kq, void *vq, float *kscale, float *vsca
     if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
     if (page != 16 && page != 32 && page != 64 && page != 128) return GM_ERR_UNSUPPORTED;
     if ((int64_t)max_pages * page >= MAX_ROWS || (int64_t)B * t * heads >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    // pool rows are counted in 32 bits (2^32 of them are 256 GB and more)
+    if ((int64_t)num_pages * hkv >= ((int64_t)1 << 32) / page) return GM_ERR_UNSUPPORTED;
     if ((int64_t)B * t == 0) return GM_OK;
     if (!lens || (max_pages > 0 && !table)) return GM_ERR_INVALID_ARG;
     if (num_pages > 0 && (!kq || !vq || !kscale || !vscale)) return GM_ERR_INVALID_ARG;
@@ -242,11 +244,16 @@ template <typename T, int D> gm_status kv8_attention(gm::Kv8AttnArgs a, int B, i
 
 template <typename T, int D> gm_status kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((a.rows + 3) / 4);
+    const int64_t warps = (a.rows + a.rw - 1) / a.rw;
+    const unsigned grid = (unsigned)((warps + 3) / 4);
+    // query heads held at once: fp32 queries take twice the registers
+    constexpr int MANY = sizeof(T) == 4 ? 2 : 4;
     if (a.G == 1)
         gm::kv8_sea_kernel<T, D, 1><<<grid, 128, 0, st>>>(a, GM_CHECKED);
-    else
+    else if (a.G == 2 || MANY == 2)
         gm::kv8_sea_kernel<T, D, 2><<<grid, 128, 0, st>>>(a, GM_CHECKED);
+    else
+        gm::kv8_sea_kernel<T, D, MANY><<<grid, 128, 0, st>>>(a, GM_CHECKED);
     return launched();
 }
 
@@ -380,12 +387,16 @@ gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, 
     a.o = o;
     a.lse = lse;
     a.t = t;
-    a.hq = hq;
     a.hkv = hkv;
     a.G = hq / hkv;
     a.s = s;
+    while ((1 << a.s_shift) < s) ++a.s_shift;
     a.rows = (int64_t)B * t * hkv;
-    a.scale = scale;
+    // several rows per warp once there are enough rows to keep 16 warps per SM busy all the same
+    a.rw = (int)std::max<int64_t>(1, std::min<int64_t>(32 >> a.s_shift, a.rows / (148 * 16)));
+    a.div_h = gm::FastDiv((uint32_t)hkv);
+    a.div_t = gm::FastDiv((uint32_t)t);
+    a.sl2 = scale * gm::LOG2E;
     if (dtype == GM_F32) return d == 64 ? kv8_sea<float, 64>(a, stream) : kv8_sea<float, 128>(a, stream);
     return d == 64 ? kv8_sea<__nv_bfloat16, 64>(a, stream) : kv8_sea<__nv_bfloat16, 128>(a, stream);
 }

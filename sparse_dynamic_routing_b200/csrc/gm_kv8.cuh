@@ -584,12 +584,16 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
 // ---- sparse edge attention over the cache -----------------------------------------------------------
 //
 // As gm_sea_forward for the last rows of each sequence: row x has edges idx/w [B, t, hkv, s] into
-// the cached tokens, z_j = scale <q, k_{t_j}> + ln w_j, o = sum softmax(z)_j v_{t_j}. One warp per
-// (b, x, KV head): the C = D/16 lanes of a segment hold one slot's 16-byte chunks of K and V, so
-// 32 / C slots are gathered at once, each segment keeping its own softmax; the segments are
-// joined with shuffles at the end. fp32 arithmetic throughout. Bound by the gather's latency for
-// single tokens (edges -> page -> rows is a chain of three loads), by q, o and the L2 for
-// prompts.
+// the cached tokens, z_j = scale <q, k_{t_j}> + ln w_j, o = sum softmax(z)_j v_{t_j}.
+//
+// A warp takes up to 32 / s consecutive rows (b, x, KV head). First every lane resolves one slot
+// of one row (edge -> page -> row of the pool and its scales), so that chain of dependent loads
+// is waited for once per warp. Then the rows follow one after another, the next row's q, K and V
+// asked for before the current one is computed. For the scores the C = D/16 lanes of a segment
+// hold one slot's 16-byte chunks of K, so 32 / C slots are scored at once; for the output every
+// lane owns D/32 columns and reads its bytes of each slot's V row, so nothing is summed across
+// lanes there. fp32 arithmetic throughout. Single tokens take one row per warp: there latency is
+// all, while prompts are bound by the instructions that widen and multiply the gathered bytes.
 
 struct Kv8SeaArgs {
     Kv8 c;
@@ -599,129 +603,188 @@ struct Kv8SeaArgs {
     const int32_t *q_lens;
     void *o;
     float *lse;
-    int t, hq, hkv, G, s;
+    int t, hkv, G, s;
+    int s_shift;   // slots of a row take 1 << s_shift lanes
+    int rw;        // rows per warp, at most 32 >> s_shift
     int64_t rows;  // B * t * hkv
-    float scale;
+    FastDiv div_h, div_t;
+    float sl2;     // scale * log2(e)
 };
 
 template <typename T, int D, int GC>
 __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
 {
-    constexpr int C = D / 16, SEG = 32 / C;
+    constexpr int C = D / 16, SEG = 32 / C;      // lanes per slot, slots per pass
     constexpr int VEC = Vec<T>::N, NV = 16 / VEC;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
+    constexpr int OW = D / 32;                   // output columns per lane
+    constexpr uint32_t NONE = 0xffffffffu;
+    const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * a.rw;
+    if (row0 >= a.rows) return;
     const int lane = threadIdx.x & 31, seg = lane / C, ch = lane - seg * C;
-    const int64_t bx = row / a.hkv;
-    const int h = (int)(row - bx * a.hkv);
-    const int b = (int)(bx / a.t), xq = (int)(bx - (int64_t)b * a.t);
-    int len = __ldg(a.c.lens + b);
-    const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
-    if (len < 0 || len > room) {
-        if (lane == 0) raise_index_error();
-        len = len < 0 ? 0 : (int)room;
+    const int n = (int)min((int64_t)a.rw, a.rows - row0);
+
+    // ---- this lane's slot: its row of the pool, and what it adds to the score ------------------
+    uint32_t rix = NONE;
+    float zs = 0.0f, lw = 0.0f, vs = 0.0f;
+    {
+        const int lr = lane >> a.s_shift, j = lane & ((1 << a.s_shift) - 1);
+        if (lr < n && j < a.s) {
+            const uint32_t row = (uint32_t)(row0 + lr);  // rows < 2^31
+            const uint32_t bx = a.div_h.div(row), h = row - bx * a.div_h.d;
+            const uint32_t b = a.div_t.div(bx), x = bx - b * a.div_t.d;
+            const float w = __ldg(a.w + (size_t)row * a.s + j);
+            const int t = __ldg(a.idx + (size_t)row * a.s + j);
+            int len = __ldg(a.c.lens + b);
+            const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
+            const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
+            if (len < 0 || len > room) {
+                raise_index_error();
+                len = len < 0 ? 0 : (int)room;
+            }
+            const int pos = (int)x < ql ? len - ql + (int)x : -1;
+            if (checked && pos >= 0) {
+                const bool bad_w = !(w >= 0.0f) || isinf(w);
+                if (bad_w || (w > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
+            }
+            if (pos >= 0 && w > 0.0f) {
+                int id = -1;
+                if (t >= 0 && t < len) id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
+                if (id >= 0 && id < a.c.num_pages) {
+                    const uint32_t blk = (uint32_t)id * (uint32_t)a.hkv + h;  // pool rows < 2^32
+                    rix = (blk << a.c.shift) + (uint32_t)(t & ((1 << a.c.shift) - 1));
+                    zs = __ldg(a.c.kscale + blk) * a.sl2;
+                    vs = __ldg(a.c.vscale + blk);
+                    lw = lg2(w);
+                } else {
+                    raise_index_error();
+                }
+            }
+        }
     }
-    const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
-    const int pos = xq < ql ? len - ql + xq : -1;
-    const int32_t *idx = a.idx + row * a.s;
-    const float *w = a.w + row * a.s;
+
+    // ---- the rows, SEG slots at a time ------------------------------------------------------------
+    struct Stage {
+        uint4 k;
+        uint32_t v[SEG];
+        uint4 q[GC][NV];
+    };
+    const int sp = 1 << a.s_shift, np = (sp + SEG - 1) / SEG;
     for (int g0 = 0; g0 < a.G; g0 += GC) {
-        float q[GC][16], acc[GC][16], m[GC], l[GC];
+        const auto load = [&](int it) {
+            Stage st;
+            const int r = it / np, first = (r << a.s_shift) + (it - r * np) * SEG;
+            const uint32_t rk = __shfl_sync(FULL, rix, first + min(seg, sp - 1));
+            st.k = make_uint4(0, 0, 0, 0);
+            if (seg < sp && rk != NONE) st.k = ld16(a.c.kq + (size_t)rk * D + ch * 16);
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-            m[g] = -INFINITY, l[g] = 0.0f;
-            const T *src = (const T *)a.q + ((size_t)bx * a.hq + h * a.G + min(g0 + g, a.G - 1)) * D + ch * 16;
+            for (int y = 0; y < SEG; ++y) {
+                const uint32_t rv = __shfl_sync(FULL, rix, first + min(y, sp - 1));
+                st.v[y] = 0;
+                if (y < sp && rv != NONE) {
+                    const uint8_t *p = a.c.vq + (size_t)rv * D + lane * OW;
+                    if constexpr (OW == 4)
+                        st.v[y] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                    else
+                        st.v[y] = __ldg(reinterpret_cast<const uint16_t *>(p));
+                }
+            }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) q[g][e] = 0.0f, acc[g][e] = 0.0f;
-            if (pos >= 0) {
+            for (int g = 0; g < GC; ++g) {
+                const T *src = (const T *)a.q + ((size_t)(row0 + r) * a.G + min(g0 + g, a.G - 1)) * D + ch * 16;
+#pragma unroll
+                for (int e = 0; e < NV; ++e) st.q[g][e] = ld16(src + e * VEC);
+            }
+            return st;
+        };
+        float m[GC], l[GC], acc[GC][OW];
+        Stage next = load(0);
+        for (int it = 0; it < n * np; ++it) {
+            const Stage st = next;
+            if (it + 1 < n * np) next = load(it + 1);
+            const int r = it / np, pass = it - r * np, first = (r << a.s_shift) + pass * SEG;
+            if (pass == 0) {
+#pragma unroll
+                for (int g = 0; g < GC; ++g) {
+                    m[g] = -INFINITY, l[g] = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < OW; ++e) acc[g][e] = 0.0f;
+                }
+            }
+            const int src = first + min(seg, sp - 1);
+            const bool on = __shfl_sync(FULL, rix, src) != NONE && seg < sp;
+            const float zk = __shfl_sync(FULL, zs, src), zw = __shfl_sync(FULL, lw, src), vk = __shfl_sync(FULL, vs, src);
+            float2 kf[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kf[e] = from_e4m3x2((&st.k.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
+            float pv[GC];
+#pragma unroll
+            for (int g = 0; g < GC; ++g) {
+                float2 z2 = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int e = 0; e < NV; ++e) {
                     float f[VEC];
-                    unpack<T>(ld16(src + e * VEC), f);
+                    unpack<T>(st.q[g][e], f);
 #pragma unroll
-                    for (int y = 0; y < VEC; ++y) q[g][e * VEC + y] = f[y] * (a.scale * LOG2E);
+                    for (int y = 0; y < VEC / 2; ++y)
+                        z2 = __ffma2_rn(make_float2(f[2 * y], f[2 * y + 1]), kf[e * (VEC / 2) + y], z2);
+                }
+                float z = seg_sum<C>(z2.x + z2.y);
+                z = on ? fmaf(z, zk, zw) : -INFINITY;
+                float mx = z;
+#pragma unroll
+                for (int o = C; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+                const float mn = fmaxf(m[g], mx), mb = mn == -INFINITY ? 0.0f : mn;
+                const float f = ex2(m[g] - mb), p = ex2(z - mb);
+                m[g] = mn;
+                l[g] = l[g] * f + p;
+                pv[g] = on ? p * vk : 0.0f;
+                if (np > 1) {
+#pragma unroll
+                    for (int e = 0; e < OW; ++e) acc[g][e] *= f;
                 }
             }
-        }
-        for (int j0 = 0; pos >= 0 && j0 < a.s; j0 += SEG) {
-            const int j = j0 + seg;
-            float wj = 0.0f;
-            int t = 0;
-            if (j < a.s) {
-                wj = __ldg(w + j);
-                t = __ldg(idx + j);
-            }
-            int id = 0;
-            bool on = wj > 0.0f;
-            if (on) {
-                on = t >= 0 && t < len;
-                if (on) {
-                    id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
-                    on = id >= 0 && id < a.c.num_pages;
-                }
-                if (!on && ch == 0 && g0 == 0) raise_index_error();
-            }
-            if (checked && ch == 0 && g0 == 0 && j < a.s) {
-                const bool bad_w = !(wj >= 0.0f) || isinf(wj);
-                if (bad_w || (wj > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
-            }
-            uint4 ku = make_uint4(0, 0, 0, 0), vu = ku;
-            float ksc = 0.0f, vsc = 0.0f;
-            if (on) {
-                const size_t blk = (size_t)id * a.hkv + h;
-                const size_t at = ((blk << a.c.shift) + (size_t)(t & ((1 << a.c.shift) - 1))) * D + ch * 16;
-                ku = ld16(a.c.kq + at);
-                vu = ld16(a.c.vq + at);
-                ksc = __ldg(a.c.kscale + blk);
-                vsc = __ldg(a.c.vscale + blk);
-            }
-            float kf[16], vf[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 x = from_e4m3x2((&ku.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
-                const float2 y = from_e4m3x2((&vu.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
-                kf[2 * e] = x.x, kf[2 * e + 1] = x.y;
-                vf[2 * e] = y.x, vf[2 * e + 1] = y.y;
+            for (int y = 0; y < SEG; ++y) {
+                float2 vf[OW / 2];
+#pragma unroll
+                for (int e = 0; e < OW / 2; ++e) vf[e] = from_e4m3x2(st.v[y] >> (e * 16) & 0xffffu);
+#pragma unroll
+                for (int g = 0; g < GC; ++g) {
+                    const float p = __shfl_sync(FULL, pv[g], y * C);
+#pragma unroll
+                    for (int e = 0; e < OW / 2; ++e) {
+                        acc[g][2 * e] = fmaf(p, vf[e].x, acc[g][2 * e]);
+                        acc[g][2 * e + 1] = fmaf(p, vf[e].y, acc[g][2 * e + 1]);
+                    }
+                }
             }
-            const float lw = on ? log2f(wj) : 0.0f;
+            if (pass < np - 1) continue;
 #pragma unroll
             for (int g = 0; g < GC; ++g) {
-                float z = 0.0f;
+                const float sum = cross_seg_sum<C>(l[g]);
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // an empty row is 0, a NaN stays
+                if (g0 + g < a.G) {
+                    const size_t ro = (size_t)(row0 + r) * a.G + g0 + g;  // row of o: (b, x, query head)
+                    if constexpr (sizeof(T) == 4) {
+                        float *dst = (float *)a.o + ro * D + lane * OW;
+                        if constexpr (OW == 4)
+                            *reinterpret_cast<float4 *>(dst) =
+                                make_float4(acc[g][0] * inv, acc[g][1] * inv, acc[g][2] * inv, acc[g][3] * inv);
+                        else
+                            *reinterpret_cast<float2 *>(dst) = make_float2(acc[g][0] * inv, acc[g][1] * inv);
+                    } else {
+                        __nv_bfloat162 x[OW / 2];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) z = fmaf(q[g][e], kf[e], z);
-                z = seg_sum<C>(z);
-                if (on) {
-                    z = fmaf(z, ksc, lw);
-                    const float mn = fmaxf(m[g], z);
-                    const float f = ex2(m[g] - mn), p = ex2(z - mn), pv = p * vsc;
-                    l[g] = l[g] * f + p;
-                    m[g] = mn;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[g][e] = fmaf(pv, vf[e], acc[g][e] * f);
+                        for (int e = 0; e < OW / 2; ++e)
+                            x[e] = __floats2bfloat162_rn(acc[g][2 * e] * inv, acc[g][2 * e + 1] * inv);
+                        __nv_bfloat16 *dst = (__nv_bfloat16 *)a.o + ro * D + lane * OW;
+                        if constexpr (OW == 4)
+                            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(x);
+                        else
+                            *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(x);
+                    }
+                    if (a.lse && lane == 0) a.lse[ro] = sum == 0.0f ? -INFINITY : (m[g] + lg2(sum)) * LN2;
                 }
-            }
-        }
-#pragma unroll
-        for (int g = 0; g < GC; ++g) {
-            float mx = m[g];
-#pragma unroll
-            for (int o = C; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-            const float f = mx == -INFINITY ? 0.0f : ex2(m[g] - mx);
-            const float sum = cross_seg_sum<C>(l[g] * f);
-            const float inv = sum > 0.0f ? 1.0f / sum : sum;  // an empty row stays 0, a NaN stays
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[g][e] = cross_seg_sum<C>(acc[g][e] * f) * inv;
-            if (seg == 0 && g0 + g < a.G) {
-                const size_t r = (size_t)bx * a.hq + h * a.G + g0 + g;
-                T *dst = (T *)a.o + r * D + ch * 16;
-#pragma unroll
-                for (int e = 0; e < NV; ++e) {
-                    float y[VEC];
-#pragma unroll
-                    for (int z = 0; z < VEC; ++z) y[z] = acc[g][e * VEC + z];
-                    *reinterpret_cast<uint4 *>(dst + e * VEC) = pack<T>(y);
-                }
-                if (a.lse && ch == 0) a.lse[r] = sum == 0.0f ? -INFINITY : (mx + lg2(sum)) * LN2;
             }
         }
     }

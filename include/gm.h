@@ -622,7 +622,8 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
  * slot is active iff w > 0, z_j = scale * <q, k[t_j]> + ln w_j. Rows, lengths, q_lens, outputs
  * and limits as gm_kv8_attention_forward. An active slot of a row below q_lens[b] whose index
  * lies outside [0, lens[b]), or whose page lies outside the pool, is skipped and raises the
- * index-range flag. fp32 arithmetic throughout. Deterministic. The checked build verifies the
+ * index-range flag. fp32 scores, statistics and sums; fp32 queries and the weights that meet the
+ * values keep 22 bits. Deterministic. The checked build verifies the
  * edges of the rows below q_lens[b] (weights finite and >= 0, indices at most the row's position).
  */
 gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, const float *w, int s,

@@ -244,16 +244,12 @@ template <typename T, int D> gm_status kv8_attention(gm::Kv8AttnArgs a, int B, i
 
 template <typename T, int D> gm_status kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
 {
-    const int64_t warps = (a.rows + a.rw - 1) / a.rw;
-    const unsigned grid = (unsigned)((warps + 3) / 4);
-    // query heads held at once: fp32 queries take twice the registers
-    constexpr int MANY = sizeof(T) == 4 ? 2 : 4;
-    if (a.G == 1)
+    // up to 16 warps per SM, each taking tile after tile
+    const unsigned grid = (unsigned)std::min<int64_t>((a.tiles + 3) / 4, 148 * 4);
+    if (a.s <= 16)
         gm::kv8_sea_kernel<T, D, 1><<<grid, 128, 0, st>>>(a, GM_CHECKED);
-    else if (a.G == 2 || MANY == 2)
-        gm::kv8_sea_kernel<T, D, 2><<<grid, 128, 0, st>>>(a, GM_CHECKED);
     else
-        gm::kv8_sea_kernel<T, D, MANY><<<grid, 128, 0, st>>>(a, GM_CHECKED);
+        gm::kv8_sea_kernel<T, D, 2><<<grid, 128, 0, st>>>(a, GM_CHECKED);
     return launched();
 }
 
@@ -392,8 +388,9 @@ gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, 
     a.s = s;
     while ((1 << a.s_shift) < s) ++a.s_shift;
     a.rows = (int64_t)B * t * hkv;
-    // several rows per warp once there are enough rows to keep 16 warps per SM busy all the same
-    a.rw = (int)std::max<int64_t>(1, std::min<int64_t>(32 >> a.s_shift, a.rows / (148 * 16)));
+    while (a.g_shift < 3 && (1 << a.g_shift) < a.G) ++a.g_shift;
+    a.rt = std::min(std::max(16 >> a.s_shift, 1), 8 >> a.g_shift);
+    a.tiles = (a.rows + a.rt - 1) / a.rt;
     a.div_h = gm::FastDiv((uint32_t)hkv);
     a.div_t = gm::FastDiv((uint32_t)t);
     a.sl2 = scale * gm::LOG2E;

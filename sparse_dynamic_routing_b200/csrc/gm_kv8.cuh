@@ -140,7 +140,9 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
             *(reinterpret_cast<uint4 *>(dst) + ch) = w;
         }
     }
-    const float inv = 1.0f / scale;
+    // the elements of a block whose scale is NaN are 0: no byte of a token is itself a NaN, so a
+    // reader's weight of 0 always gives 0
+    const float inv = scale == scale ? 1.0f / scale : 0.0f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int ch = threadIdx.x + 256 * i;
@@ -150,7 +152,7 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
             uint32_t w[VEC / 4];
 #pragma unroll
             for (int e = 0; e < VEC / 4; ++e)
-                w[e] = to_e4m3x4(f[4 * e] * inv, f[4 * e + 1] * inv, f[4 * e + 2] * inv, f[4 * e + 3] * inv);
+                w[e] = inv == 0.0f ? 0u : to_e4m3x4(f[4 * e] * inv, f[4 * e + 1] * inv, f[4 * e + 2] * inv, f[4 * e + 3] * inv);
             uint8_t *p = dst + (size_t)r0 * D + (size_t)ch * VEC;  // rows of a block are contiguous
             if constexpr (VEC == 8)
                 *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
@@ -176,8 +178,7 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
 // (S^T = K q^T, O^T = V^T P^T) so that the 16-row operand is the cache and a single token's few
 // query rows fill an 8-column operand. The bytes go from global memory to registers in the
 // order the operands want (any permutation of d, and of the output's columns, is as good) and
-// become fp16 with shifts: an e4m3 byte moved under fp16's exponent is the value times 2^-8,
-// exactly, subnormals included. Query rows are scaled by a power of two into fp16's upper range
+// become fp16, which holds every e4m3 value. Query rows are scaled by a power of two into fp16's upper range
 // (bf16's 8 bits fit its 11; what falls below fp16's subnormals is 2^-38 of the row's largest
 // element), probabilities by 2^14 likewise. The fp16 rounding of a probability (2^-12) lies below the bf16
 // rounding of the output (2^-9). fp32 queries and probabilities are split in two fp16 terms,
@@ -211,12 +212,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// Two e4m3 bytes of the pair (x, y), chosen by a byte selector whose nibbles 1 and 3 name them,
-// as fp16 values times 2^-8.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t x, uint32_t y, uint32_t sel)
+// Two e4m3 bytes (bits 0-15) as fp16 values, exactly. One instruction at half rate; building the
+// same bits with shifts takes four (the decode of 64 sequences of 8192 tokens: 162 against 100 us).
+__device__ __forceinline__ uint32_t half2_of(uint32_t two)
 {
-    const uint32_t w = __byte_perm(x, y, sel);
-    return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float x, float y)
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
             if constexpr (SPLIT) sm.q[1][r][lane * PER + e] = __float2half_rn(v[e] * up - __half2float(hi));
         }
         if (lane == 0) {
-            sm.qscale[r] = down * 256.0f * a.sl2;  // 2^8: the bytes' fp16 form
+            sm.qscale[r] = down * a.sl2;
             sm.pos[r] = pos;
         }
     }
@@ -425,8 +426,8 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
             const uint32_t w0 = (&kr[0][ks >> 2].x)[ks & 3], w1 = (&kr[1][ks >> 2].x)[ks & 3];
-            const uint32_t a0 = e4m3_pair(w0, w0, 0x1000), a2 = e4m3_pair(w0, w0, 0x3020);
-            const uint32_t a1 = e4m3_pair(w1, w1, 0x1000), a3 = e4m3_pair(w1, w1, 0x3020);
+            const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
+            const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
             const int d = (ks >> 2) * 64 + c * 16 + (ks & 3) * 4;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -493,14 +494,23 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
                 pl[n][1] = transpose8x8(pack_rest(p[2], p[3], h1));
             }
         }
+        if (t0 + 16 > len) {  // rows past the sequence's end may hold any bytes, NaN among them
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t0 + 2 * c + (e & 1) + 8 * (e >> 1) >= len) {
+#pragma unroll
+                    for (int y = 0; y < VW; ++y) vr[e][y] = 0;
+                }
+        }
         // O^T += V^T P^T
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {  // output columns g * (D/8) + 2j and + 2j + 1
-            const uint32_t sel0 = (j & 1) ? 0x6020u : 0x4000u, sel1 = (j & 1) ? 0x7030u : 0x5010u;
-            const uint32_t a0 = e4m3_pair(vr[0][j >> 1], vr[1][j >> 1], sel0);
-            const uint32_t a1 = e4m3_pair(vr[0][j >> 1], vr[1][j >> 1], sel1);
-            const uint32_t a2 = e4m3_pair(vr[2][j >> 1], vr[3][j >> 1], sel0);
-            const uint32_t a3 = e4m3_pair(vr[2][j >> 1], vr[3][j >> 1], sel1);
+            // byte pairs (key, next key) of column 2j in the low half, of column 2j + 1 in the high
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
+            const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
+            const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
+            const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 mma_f16(acc[n][j], a0, a1, a2, a3, pt[n][0], pt[n][1]);
@@ -520,8 +530,8 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
 #pragma unroll
             for (int sft = 4; sft < 32; sft <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], sft);
             if (r < nrows) {
-                // back from the values' own maximum: 2^8 of the bytes' form, 2^-14 of the weights
-                const float u = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-6f;
+                // back from the values' own maximum and the weights' 2^14
+                const float u = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-14f;
                 if (g == 0) {
                     sm.m[warp][r] = m[n][e];
                     sm.l[warp][r] = l[n][e];
@@ -586,14 +596,15 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
 // As gm_sea_forward for the last rows of each sequence: row x has edges idx/w [B, t, hkv, s] into
 // the cached tokens, z_j = scale <q, k_{t_j}> + ln w_j, o = sum softmax(z)_j v_{t_j}.
 //
-// A warp takes up to 32 / s consecutive rows (b, x, KV head). First every lane resolves one slot
-// of one row (edge -> page -> row of the pool and its scales), so that chain of dependent loads
-// is waited for once per warp. Then the rows follow one after another, the next row's q, K and V
-// asked for before the current one is computed. For the scores the C = D/16 lanes of a segment
-// hold one slot's 16-byte chunks of K, so 32 / C slots are scored at once; for the output every
-// lane owns D/32 columns and reads its bytes of each slot's V row, so nothing is summed across
-// lanes there. fp32 arithmetic throughout. Single tokens take one row per warp: there latency is
-// all, while prompts are bound by the instructions that widen and multiply the gathered bytes.
+// The same operands as in the attention above, with 16 gathered slots in the place of 16 keys: a
+// tile is RT consecutive rows (b, x, KV head), their slots in the 16-row operand and their query
+// heads in the 8-column one (4 rows of 4 slots and 2 heads fill both). Scores and weights off
+// the rows' own diagonal blocks are masked away; the tensor cores have the time. Against fp32
+// multiplications on the gathered bytes this takes a fifth of the instructions, which had been
+// the bound. Weights enter as two fp16 terms (22 bits; the second costs a tile 8 of its 24 mma),
+// so the output's rounding is the only one that shows. Each lane resolves one slot of the next tile (edge -> page -> row of the pool,
+// scales: a chain of dependent loads) while the current tile is computed. Weights get a power of
+// two per query row that puts the largest product of weight and value scale at 2^14.
 
 struct Kv8SeaArgs {
     Kv8 c;
@@ -604,187 +615,262 @@ struct Kv8SeaArgs {
     void *o;
     float *lse;
     int t, hkv, G, s;
-    int s_shift;   // slots of a row take 1 << s_shift lanes
-    int rw;        // rows per warp, at most 32 >> s_shift
-    int64_t rows;  // B * t * hkv
+    int s_shift, g_shift;  // slots and heads of a row take 1 << shift operand rows and columns
+    int rt;                // rows per tile
+    int64_t rows, tiles;   // B * t * hkv, and tiles of rt rows
     FastDiv div_h, div_t;
-    float sl2;     // scale * log2(e)
+    float sl2;             // scale * log2(e)
 };
 
-template <typename T, int D, int GC>
+// What one slot of a row adds: its row of the pool (NONE: inactive), score factor, ln w, value scale.
+struct Kv8Slot {
+    static constexpr uint32_t NONE = 0xffffffffu;
+    uint32_t row;
+    float zs, lw, vs;
+};
+
+__device__ __forceinline__ Kv8Slot kv8_slot(const Kv8SeaArgs &a, int64_t at, int j, bool report, int checked)
+{
+    Kv8Slot s{Kv8Slot::NONE, 0.0f, 0.0f, 0.0f};
+    if (at >= a.rows || j >= a.s) return s;
+    const uint32_t row = (uint32_t)at;  // rows < 2^31
+    const uint32_t bx = a.div_h.div(row), h = row - bx * a.div_h.d;
+    const uint32_t b = a.div_t.div(bx), x = bx - b * a.div_t.d;
+    const float w = __ldg(a.w + (size_t)row * a.s + j);
+    const int t = __ldg(a.idx + (size_t)row * a.s + j);
+    int len = __ldg(a.c.lens + b);
+    const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
+    const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
+    if (len < 0 || len > room) {
+        if (report) raise_index_error();
+        len = len < 0 ? 0 : (int)room;
+    }
+    const int pos = (int)x < ql ? len - ql + (int)x : -1;
+    if (checked && report && pos >= 0) {
+        const bool bad_w = !(w >= 0.0f) || isinf(w);
+        if (bad_w || (w > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
+    }
+    if (pos < 0 || !(w > 0.0f)) return s;
+    int id = -1;
+    if (t >= 0 && t < len) id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
+    if (id < 0 || id >= a.c.num_pages) {
+        if (report) raise_index_error();
+        return s;
+    }
+    const uint32_t blk = (uint32_t)id * (uint32_t)a.hkv + h;  // pool rows < 2^32
+    s.row = (blk << a.c.shift) + (uint32_t)(t & ((1 << a.c.shift) - 1));
+    s.zs = __ldg(a.c.kscale + blk) * a.sl2;
+    s.vs = __ldg(a.c.vscale + blk);
+    s.lw = lg2(w);
+    return s;
+}
+
+// NP: pieces of 16 slots per row (2 for more than 16 slots).
+template <typename T, int D, int NP>
 __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
 {
-    constexpr int C = D / 16, SEG = 32 / C;      // lanes per slot, slots per pass
-    constexpr int VEC = Vec<T>::N, NV = 16 / VEC;
-    constexpr int OW = D / 32;                   // output columns per lane
-    constexpr uint32_t NONE = 0xffffffffu;
-    const int64_t row0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * a.rw;
-    if (row0 >= a.rows) return;
-    const int lane = threadIdx.x & 31, seg = lane / C, ch = lane - seg * C;
-    const int n = (int)min((int64_t)a.rw, a.rows - row0);
-
-    // ---- this lane's slot: its row of the pool, and what it adds to the score ------------------
-    uint32_t rix = NONE;
-    float zs = 0.0f, lw = 0.0f, vs = 0.0f;
-    {
-        const int lr = lane >> a.s_shift, j = lane & ((1 << a.s_shift) - 1);
-        if (lr < n && j < a.s) {
-            const uint32_t row = (uint32_t)(row0 + lr);  // rows < 2^31
-            const uint32_t bx = a.div_h.div(row), h = row - bx * a.div_h.d;
-            const uint32_t b = a.div_t.div(bx), x = bx - b * a.div_t.d;
-            const float w = __ldg(a.w + (size_t)row * a.s + j);
-            const int t = __ldg(a.idx + (size_t)row * a.s + j);
-            int len = __ldg(a.c.lens + b);
-            const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
-            const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
-            if (len < 0 || len > room) {
-                raise_index_error();
-                len = len < 0 ? 0 : (int)room;
-            }
-            const int pos = (int)x < ql ? len - ql + (int)x : -1;
-            if (checked && pos >= 0) {
-                const bool bad_w = !(w >= 0.0f) || isinf(w);
-                if (bad_w || (w > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
-            }
-            if (pos >= 0 && w > 0.0f) {
-                int id = -1;
-                if (t >= 0 && t < len) id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
-                if (id >= 0 && id < a.c.num_pages) {
-                    const uint32_t blk = (uint32_t)id * (uint32_t)a.hkv + h;  // pool rows < 2^32
-                    rix = (blk << a.c.shift) + (uint32_t)(t & ((1 << a.c.shift) - 1));
-                    zs = __ldg(a.c.kscale + blk) * a.sl2;
-                    vs = __ldg(a.c.vscale + blk);
-                    lw = lg2(w);
-                } else {
-                    raise_index_error();
-                }
-            }
+    constexpr bool SPLIT = sizeof(T) == 4;
+    constexpr int VEC = Vec<T>::N, KS = D / 16, NK = D / 64, VW = D / 32;
+    constexpr int QV = 16 / VEC;  // 16-byte vectors of 16 query elements
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int64_t step = (int64_t)gridDim.x * 4;
+    int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (tile >= a.tiles) return;
+    // slot `lane & 15` of a tile: row (lane & 15) >> s_shift (at most 16 slots per piece)
+    const int ssh = min(a.s_shift, 4), sr = (lane & 15) >> ssh, sj = (lane & 15) & ((1 << ssh) - 1);
+    const auto resolve = [&](int64_t ti, Kv8Slot (&s)[NP]) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            s[p] = Kv8Slot{Kv8Slot::NONE, 0.0f, 0.0f, 0.0f};
+            if (ti < a.tiles && sr < a.rt) s[p] = kv8_slot(a, ti * a.rt + sr, p * 16 + sj, lane < 16, checked);
         }
-    }
-
-    // ---- the rows, SEG slots at a time ------------------------------------------------------------
-    struct Stage {
-        uint4 k;
-        uint32_t v[SEG];
-        uint4 q[GC][NV];
     };
-    const int sp = 1 << a.s_shift, np = (sp + SEG - 1) / SEG;
-    for (int g0 = 0; g0 < a.G; g0 += GC) {
-        const auto load = [&](int it) {
-            Stage st;
-            const int r = it / np, first = (r << a.s_shift) + (it - r * np) * SEG;
-            const uint32_t rk = __shfl_sync(FULL, rix, first + min(seg, sp - 1));
-            st.k = make_uint4(0, 0, 0, 0);
-            if (seg < sp && rk != NONE) st.k = ld16(a.c.kq + (size_t)rk * D + ch * 16);
+    Kv8Slot next[NP];
+    resolve(tile, next);
+    for (; tile < a.tiles; tile += step) {
+        Kv8Slot cur[NP];
 #pragma unroll
-            for (int y = 0; y < SEG; ++y) {
-                const uint32_t rv = __shfl_sync(FULL, rix, first + min(y, sp - 1));
-                st.v[y] = 0;
-                if (y < sp && rv != NONE) {
-                    const uint8_t *p = a.c.vq + (size_t)rv * D + lane * OW;
-                    if constexpr (OW == 4)
-                        st.v[y] = __ldg(reinterpret_cast<const uint32_t *>(p));
-                    else
-                        st.v[y] = __ldg(reinterpret_cast<const uint16_t *>(p));
+        for (int p = 0; p < NP; ++p) cur[p] = next[p];
+        const int64_t row0 = tile * a.rt;
+        for (int g0 = 0; g0 < a.G; g0 += 8) {
+            // ---- loads: K rows of slots g, g + 8; V rows of slots 2c, 2c+1, 2c+8, 2c+9; q of column g
+            uint4 kr[NP][2][NK];
+            uint32_t vr[NP][4][VW];
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const uint32_t r = __shfl_sync(FULL, cur[p].row, g + 8 * s);
+#pragma unroll
+                    for (int e = 0; e < NK; ++e) {
+                        kr[p][s][e] = make_uint4(0, 0, 0, 0);
+                        if (r != Kv8Slot::NONE) kr[p][s][e] = ld16(a.c.kq + (size_t)r * D + c * 16 + e * 64);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t r = __shfl_sync(FULL, cur[p].row, 2 * c + (s & 1) + 8 * (s >> 1));
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) vr[p][s][e] = 0;
+                    if (r != Kv8Slot::NONE) {
+                        const uint8_t *src = a.c.vq + (size_t)r * D + g * (D / 8);
+                        if constexpr (VW == 4) {
+                            const uint4 u = ld16(src);
+                            vr[p][s][0] = u.x, vr[p][s][1] = u.y, vr[p][s][2] = u.z, vr[p][s][3] = u.w;
+                        } else {
+                            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
+                            vr[p][s][0] = u.x, vr[p][s][1] = u.y;
+                        }
+                    }
                 }
             }
+            // column n of the tile: row n >> g_shift, head g0 + (n & (2^g_shift - 1))
+            const auto column = [&](int n, int64_t &row, int &head) {
+                row = row0 + (n >> a.g_shift);
+                head = g0 + (n & ((1 << a.g_shift) - 1));
+                return (n >> a.g_shift) < a.rt && row < a.rows && head < a.G;
+            };
+            uint32_t qh[KS][2], ql[SPLIT ? KS : 1][2];
+            float qdown;
+            {
+                int64_t row;
+                int head;
+                const bool in = column(g, row, head);
+                const T *src = (const T *)a.q + ((size_t)row * a.G + head) * D + c * 16;
+                uint4 u[NK][QV];
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                const T *src = (const T *)a.q + ((size_t)(row0 + r) * a.G + min(g0 + g, a.G - 1)) * D + ch * 16;
+                for (int e = 0; e < NK; ++e)
 #pragma unroll
-                for (int e = 0; e < NV; ++e) st.q[g][e] = ld16(src + e * VEC);
-            }
-            return st;
-        };
-        float m[GC], l[GC], acc[GC][OW];
-        Stage next = load(0);
-        for (int it = 0; it < n * np; ++it) {
-            const Stage st = next;
-            if (it + 1 < n * np) next = load(it + 1);
-            const int r = it / np, pass = it - r * np, first = (r << a.s_shift) + pass * SEG;
-            if (pass == 0) {
+                    for (int y = 0; y < QV; ++y) u[e][y] = in ? ld16(src + e * 64 + y * VEC) : make_uint4(0, 0, 0, 0);
+                float big = 0.0f;
 #pragma unroll
-                for (int g = 0; g < GC; ++g) {
-                    m[g] = -INFINITY, l[g] = 0.0f;
+                for (int e = 0; e < NK; ++e)
 #pragma unroll
-                    for (int e = 0; e < OW; ++e) acc[g][e] = 0.0f;
-                }
-            }
-            const int src = first + min(seg, sp - 1);
-            const bool on = __shfl_sync(FULL, rix, src) != NONE && seg < sp;
-            const float zk = __shfl_sync(FULL, zs, src), zw = __shfl_sync(FULL, lw, src), vk = __shfl_sync(FULL, vs, src);
-            float2 kf[8];
+                    for (int y = 0; y < QV; ++y) {
+                        float f[VEC];
+                        unpack<T>(u[e][y], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) kf[e] = from_e4m3x2((&st.k.x)[e >> 1] >> ((e & 1) * 16) & 0xffffu);
-            float pv[GC];
+                        for (int z = 0; z < VEC; ++z) big = fmaxf(big, fabsf(f[z]));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
+                const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                qdown = __uint_as_float((uint32_t)(127 - 14 + e2) << 23);
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                float2 z2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int e = 0; e < NV; ++e) {
+                for (int ks = 0; ks < KS; ++ks) {
                     float f[VEC];
-                    unpack<T>(st.q[g][e], f);
+                    unpack<T>(u[ks >> 2][(ks & 3) * 4 / VEC], f);
+                    const int o = (ks & 3) * 4 % VEC;
 #pragma unroll
-                    for (int y = 0; y < VEC / 2; ++y)
-                        z2 = __ffma2_rn(make_float2(f[2 * y], f[2 * y + 1]), kf[e * (VEC / 2) + y], z2);
-                }
-                float z = seg_sum<C>(z2.x + z2.y);
-                z = on ? fmaf(z, zk, zw) : -INFINITY;
-                float mx = z;
-#pragma unroll
-                for (int o = C; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-                const float mn = fmaxf(m[g], mx), mb = mn == -INFINITY ? 0.0f : mn;
-                const float f = ex2(m[g] - mb), p = ex2(z - mb);
-                m[g] = mn;
-                l[g] = l[g] * f + p;
-                pv[g] = on ? p * vk : 0.0f;
-                if (np > 1) {
-#pragma unroll
-                    for (int e = 0; e < OW; ++e) acc[g][e] *= f;
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < SEG; ++y) {
-                float2 vf[OW / 2];
-#pragma unroll
-                for (int e = 0; e < OW / 2; ++e) vf[e] = from_e4m3x2(st.v[y] >> (e * 16) & 0xffffu);
-#pragma unroll
-                for (int g = 0; g < GC; ++g) {
-                    const float p = __shfl_sync(FULL, pv[g], y * C);
-#pragma unroll
-                    for (int e = 0; e < OW / 2; ++e) {
-                        acc[g][2 * e] = fmaf(p, vf[e].x, acc[g][2 * e]);
-                        acc[g][2 * e + 1] = fmaf(p, vf[e].y, acc[g][2 * e + 1]);
+                    for (int y = 0; y < 2; ++y) {
+                        const float lo = f[o + 2 * y] * up, hi = f[o + 2 * y + 1] * up;
+                        qh[ks][y] = pack_half2(lo, hi);
+                        if constexpr (SPLIT) ql[ks][y] = pack_rest(lo, hi, qh[ks][y]);
                     }
                 }
             }
-            if (pass < np - 1) continue;
+            if (g0 == 0) resolve(tile + step, next);
+            // ---- scores of slots g, g + 8 for columns 2c, 2c + 1 --------------------------------
+            float z[NP][4];
 #pragma unroll
-            for (int g = 0; g < GC; ++g) {
-                const float sum = cross_seg_sum<C>(l[g]);
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // an empty row is 0, a NaN stays
-                if (g0 + g < a.G) {
-                    const size_t ro = (size_t)(row0 + r) * a.G + g0 + g;  // row of o: (b, x, query head)
-                    if constexpr (sizeof(T) == 4) {
-                        float *dst = (float *)a.o + ro * D + lane * OW;
-                        if constexpr (OW == 4)
-                            *reinterpret_cast<float4 *>(dst) =
-                                make_float4(acc[g][0] * inv, acc[g][1] * inv, acc[g][2] * inv, acc[g][3] * inv);
-                        else
-                            *reinterpret_cast<float2 *>(dst) = make_float2(acc[g][0] * inv, acc[g][1] * inv);
-                    } else {
-                        __nv_bfloat162 x[OW / 2];
+            for (int p = 0; p < NP; ++p) {
 #pragma unroll
-                        for (int e = 0; e < OW / 2; ++e)
-                            x[e] = __floats2bfloat162_rn(acc[g][2 * e] * inv, acc[g][2 * e + 1] * inv);
-                        __nv_bfloat16 *dst = (__nv_bfloat16 *)a.o + ro * D + lane * OW;
-                        if constexpr (OW == 4)
-                            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(x);
-                        else
-                            *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(x);
-                    }
-                    if (a.lse && lane == 0) a.lse[ro] = sum == 0.0f ? -INFINITY : (m[g] + lg2(sum)) * LN2;
+                for (int e = 0; e < 4; ++e) z[p][e] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t w0 = (&kr[p][0][ks >> 2].x)[ks & 3], w1 = (&kr[p][1][ks >> 2].x)[ks & 3];
+                    const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
+                    const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
+                    mma_f16(z[p], a0, a1, a2, a3, qh[ks][0], qh[ks][1]);
+                    if constexpr (SPLIT) mma_f16(z[p], a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
                 }
+            }
+            const float qd[2] = {__shfl_sync(FULL, qdown, 8 * c), __shfl_sync(FULL, qdown, 8 * c + 4)};
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, mu[2] = {0.0f, 0.0f}, vs[NP][2];
+            bool see[NP][4];
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int k = g + 8 * s;
+                    const bool on = __shfl_sync(FULL, cur[p].row, k) != Kv8Slot::NONE;
+                    const float zs = __shfl_sync(FULL, cur[p].zs, k), lw = __shfl_sync(FULL, cur[p].lw, k);
+                    vs[p][s] = __shfl_sync(FULL, cur[p].vs, k);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        see[p][2 * s + e] = on && (k >> ssh) == ((2 * c + e) >> a.g_shift);
+                        z[p][2 * s + e] = see[p][2 * s + e] ? fmaf(z[p][2 * s + e], qd[e] * zs, lw) : -INFINITY;
+                        m[e] = fmaxf(m[e], z[p][2 * s + e]);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = ex2(z[p][e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
+                    l[e & 1] += x;
+                    z[p][e] = see[p][e] ? x * vs[p][e >> 1] : 0.0f;
+                    mu[e & 1] = fmaxf(mu[e & 1], z[p][e]);
+                }
+            float up[2], inv[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    l[e] += __shfl_xor_sync(FULL, l[e], o);
+                    mu[e] = fmaxf(mu[e], __shfl_xor_sync(FULL, mu[e], o));
+                }
+                const int e2 = min(max((int)(__float_as_uint(mu[e]) >> 23) - 127, -100), 127);
+                up[e] = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                // an empty row is 0, a NaN stays
+                inv[e] = l[e] == 0.0f ? 0.0f : __uint_as_float((uint32_t)(127 - 14 + e2) << 23) / l[e];
+            }
+            // ---- output ---------------------------------------------------------------------------
+            float acc[D / 16][4];
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const float p0 = z[p][0] * up[0], p1 = z[p][1] * up[1], p2 = z[p][2] * up[0], p3 = z[p][3] * up[1];
+                const uint32_t h0 = pack_half2(p0, p1), h1 = pack_half2(p2, p3);
+                const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+                const uint32_t r0 = transpose8x8(pack_rest(p0, p1, h0)), r1 = transpose8x8(pack_rest(p2, p3, h1));
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                    const uint32_t x = __byte_perm(vr[p][0][j >> 1], vr[p][1][j >> 1], sel);
+                    const uint32_t y = __byte_perm(vr[p][2][j >> 1], vr[p][3][j >> 1], sel);
+                    const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
+                    const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
+                    mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
+                    mma_f16(acc[j], a0, a1, a2, a3, r0, r1);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                int64_t row;
+                int head;
+                if (!column(2 * c + e, row, head)) continue;
+                const size_t ro = (size_t)row * a.G + head;  // row of o: (b, x, query head)
+                T *dst = (T *)a.o + ro * D + g * (D / 8);
+#pragma unroll
+                for (int y = 0; y < D / 8 / VEC; ++y) {
+                    float f[VEC];
+#pragma unroll
+                    for (int x = 0; x < VEC; ++x) {
+                        const int d = y * VEC + x;  // column g * (D/8) + d of the output
+                        f[x] = acc[d >> 1][(d & 1) * 2 + e] * inv[e];
+                    }
+                    *reinterpret_cast<uint4 *>(dst + y * VEC) = pack<T>(f);
+                }
+                if (a.lse && g == 0) a.lse[ro] = l[e] == 0.0f ? -INFINITY : (m[e] + lg2(l[e])) * LN2;
             }
         }
     }

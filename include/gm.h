@@ -603,6 +603,9 @@ gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int
  *   lens        device int32 [B]: tokens in the cache, the query rows' own tokens included
  *   q_lens      device int32 [B], taken as 0..t; NULL: t each
  *   o, lse      as gm_window_attention_forward ([B, t, hq, d] and [B, t, hq]; lse may be NULL)
+ *   workspace   device scratch owned by the caller, 16-byte aligned, at least
+ *               gm_kv8_attention_workspace_size(...) bytes (NULL where that is 0); garbage on
+ *               return. Calls that overlap on the GPU need one each
  *   limits      d in {64, 128}; any hq / hkv; page as gm_kv8_append
  * fp32 scores, statistics and sums; for GM_BF16 probabilities are rounded to fp16 before they
  * meet the values, for GM_F32 queries and probabilities keep 22 bits. Deterministic. A page
@@ -614,7 +617,13 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
                                    const float *vscale, int num_pages, int page,
                                    const int32_t *table, int max_pages, const int32_t *lens,
                                    const int32_t *q_lens, int window, int sinks, float scale,
-                                   void *o, float *lse, cudaStream_t stream);
+                                   void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                   cudaStream_t stream);
+
+/* Bytes of workspace gm_kv8_attention_forward needs for this shape; 0: none (pass NULL). Pure
+ * host function; no CUDA call. */
+size_t gm_kv8_attention_workspace_size(int B, int t, int hq, int hkv, int d, int page, int max_pages,
+                                       int window, int sinks);
 
 /*
  * gm_kv8_sea_forward - gm_sea_forward for the last tokens of each sequence, over the cache of

@@ -38,6 +38,7 @@ from ._binding import (  # noqa: F401
     gm_dense_refresh_edges,
     gm_kv8_append,
     gm_kv8_attention_forward,
+    gm_kv8_attention_workspace_size,
     gm_kv8_sea_forward,
     gm_leg_backward,
     gm_leg_sparsify,

@@ -66,7 +66,8 @@ SIGNATURES = {
     "gm_kv8_append": [_vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci, _vp, _vp,
                       _vp],
     "gm_kv8_attention_forward": [_vp, _ci, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci,
-                                 _vp, _vp, _ci, _ci, _cf, _vp, _vp, _vp],
+                                 _vp, _vp, _ci, _ci, _cf, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+    "gm_kv8_attention_workspace_size": [_ci] * 9,
     "gm_kv8_sea_forward": [_vp, _ci, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci,
                            _vp, _ci, _vp, _vp, _cf, _vp, _vp, _vp],
     "gm_check_device_errors": [_vp],
@@ -108,6 +109,7 @@ def open_library(path: str) -> ctypes.CDLL:
         fn.restype = {"gm_status_string": ctypes.c_char_p,
                       "gm_sea_backward_workspace_size": ctypes.c_size_t,
                       "gm_window_attention_backward_workspace_size": ctypes.c_size_t,
+                      "gm_kv8_attention_workspace_size": ctypes.c_size_t,
                       "gm_sea_backward_noalloc_max_scratch": ctypes.c_size_t}.get(name, ctypes.c_int)
     return lib
 
@@ -762,23 +764,37 @@ def gm_kv8_append(k, v, kq, vq, kscale, vscale, table, lens, new_lens=None, stre
     _check(st, "gm_kv8_append")
 
 
+def gm_kv8_attention_workspace_size(B: int, t: int, hq: int, hkv: int, d: int, page: int, max_pages: int,
+                                    window=None, sinks: int = 0) -> int:
+    """Workspace bytes of gm_kv8_attention_forward (0: none needed)."""
+    window, sinks = _window(window, sinks)
+    return int(load_library().gm_kv8_attention_workspace_size(B, t, hq, hkv, d, page, max_pages, window, sinks))
+
+
 def gm_kv8_attention_forward(q, kq, vq, kscale, vscale, table, lens, window=None, sinks: int = 0, q_lens=None,
-                             scale=None, o=None, lse=None, stream=None):
+                             scale=None, o=None, lse=None, workspace=None, stream=None):
     """gm_window_attention_forward for the last tokens of each sequence (q [B, t, hq, d]) over the
-    8-bit cache; lens counts the query tokens too. Returns (o, lse [B, t, hq])."""
+    8-bit cache; lens counts the query tokens too. Returns (o, lse [B, t, hq]). workspace: a uint8
+    CUDA tensor of at least gm_kv8_attention_workspace_size(...) bytes; None allocates one."""
     hkv = kq.shape[1]
     dev = _queries(q, hkv)
     B, t, hq, d = q.shape
     dt = q.dtype
     window, sinks = _window(window, sinks)
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
+    lib = load_library()
     with _on(dev, stream):
         o, po = _out(o, q.shape, dt, dev, "o")
         lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
-        st = load_library().gm_kv8_attention_forward(
+        if workspace is None:
+            need = lib.gm_kv8_attention_workspace_size(B, t, hq, hkv, d, kq.shape[2], table.shape[1], window, sinks)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        ws, size = (None, 0) if workspace is None else (
+            _arg(workspace, workspace.shape, torch.uint8, dev, "workspace"), workspace.numel())
+        st = lib.gm_kv8_attention_forward(
             _arg(q, q.shape, dt, dev, "q"), _fdtype(q), B, t, hq, hkv, d, *cache,
             None if q_lens is None else _arg(q_lens, (B,), torch.int32, dev, "q_lens"), window, sinks,
-            _scale(scale, d), po, pl, torch.cuda.current_stream().cuda_stream)
+            _scale(scale, d), po, pl, ws, size, torch.cuda.current_stream().cuda_stream)
     _check(st, "gm_kv8_attention_forward")
     return o, lse
 

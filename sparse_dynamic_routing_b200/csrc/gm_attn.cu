@@ -201,45 +201,73 @@ template <typename T, int D> gm_status kv8_append(const gm::Kv8AppendArgs &a, un
     return launched();
 }
 
-template <typename T, int D, int NT, int W>
-gm_status launch_kv8_attention(const gm::Kv8AttnArgs &a, int64_t items, int cl, cudaStream_t st)
+// How a call of gm_kv8_attention_forward is cut up: row tiles of 8 nt query rows, and the blocks
+// that share the keys of one (gm_kv8.cuh).
+struct Kv8Plan {
+    int nt, tiles, splits;
+    int64_t items;
+    size_t part_bytes, bytes;  // workspace: partial outputs, then maxima and sums
+};
+
+Kv8Plan kv8_plan(int B, int t, int hq, int hkv, int d, int64_t keys)
 {
-    using Smem = gm::Kv8Smem<D, NT, sizeof(T) == 4, W>;
-    auto kern = gm::kv8_attention_kernel<T, D, NT, W>;
+    Kv8Plan p{};
+    const int64_t flat = (int64_t)t * (hq / hkv);
+    p.nt = flat <= 8 ? 1 : 2;
+    p.tiles = (int)((flat + 8 * p.nt - 1) / (8 * p.nt));
+    p.items = (int64_t)B * hkv * p.tiles;
+    // Rounds of blocks that the GPU takes, times what one round lasts: a block's units of 32 keys
+    // per warp and a start and end worth about four of them. The splits with the least of it.
+    const int64_t room = 148 * gm::KV8_PER_SM, units = (keys + 31) / 32;
+    const int64_t most = std::min<int64_t>(room, std::max<int64_t>(1, units / (2 * gm::KV8_W)));
+    int64_t best = INT64_MAX;
+    for (int64_t s = 1; s <= most; ++s) {
+        if (s > 1 && p.items * s > 8 * room) break;
+        const int64_t cost = ((p.items * s + room - 1) / room) * ((units + s * gm::KV8_W - 1) / (s * gm::KV8_W) + 4);
+        if (cost < best) {
+            best = cost;
+            p.splits = (int)s;
+        }
+    }
+    if (p.splits > 1) {
+        const size_t rows = (size_t)p.items * p.splits * 8 * p.nt;
+        p.part_bytes = rows * d * 4;
+        p.bytes = p.part_bytes + rows * 8;
+    }
+    return p;
+}
+
+// Keys that one row tile can see at most.
+int64_t kv8_keys(int64_t room, int window, int sinks, int t)
+{
+    return std::min<int64_t>(room, (int64_t)window + sinks + t);
+}
+
+template <typename T, int D, int NT> gm_status launch_kv8_attention(const gm::Kv8AttnArgs &a, int B, int64_t items, cudaStream_t st)
+{
+    using Smem = gm::Kv8Smem<D, NT, sizeof(T) == 4>;
+    auto kern = gm::kv8_attention_kernel<T, D, NT>;
     if (!raise_smem(kern, sizeof(Smem))) return GM_ERR_CUDA;
-    if (cl > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return GM_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * cl));
-    cfg.blockDim = dim3(W * 32);
-    cfg.dynamicSmemBytes = sizeof(Smem);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cl;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    (void)cudaLaunchKernelEx(&cfg, kern, a);
+    kern<<<(unsigned)(items * a.splits), gm::KV8_W * 32, sizeof(Smem), st>>>(a);
+    if (a.splits > 1) {
+        const int64_t rows = (int64_t)B * a.t * a.hq;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+        cfg.blockDim = dim3(128);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        (void)cudaLaunchKernelEx(&cfg, gm::kv8_join_kernel<T, D, NT>, a, rows);
+    }
     return launched();
 }
 
-template <typename T, int D> gm_status kv8_attention(gm::Kv8AttnArgs a, int B, int64_t keys, cudaStream_t st)
+template <typename T, int D> gm_status kv8_attention(const gm::Kv8AttnArgs &a, int B, const Kv8Plan &p, cudaStream_t st)
 {
-    const int64_t flat = (int64_t)a.t * a.G;
-    const int nt = flat <= 8 ? 1 : 2;
-    a.tiles = (int)((flat + 8 * nt - 1) / (8 * nt));
-    const int64_t items = (int64_t)B * a.hkv * a.tiles;
-    // warps per row tile: about 12 per SM over all tiles, each with at least two pieces of keys
-    const int64_t most = std::max<int64_t>(1, (keys + 31) / 32);
-    const int64_t want = std::min<int64_t>((148 * 12 + items - 1) / items, most);
-    const int W = want > 64 ? 16 : 4;
-    int cl = 1;
-    while (cl < 16 && (int64_t)cl * W < want) cl *= 2;
-    if (items * cl >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
-    if (nt == 1) return W == 4 ? launch_kv8_attention<T, D, 1, 4>(a, items, cl, st) : launch_kv8_attention<T, D, 1, 16>(a, items, cl, st);
-    return W == 4 ? launch_kv8_attention<T, D, 2, 4>(a, items, cl, st) : launch_kv8_attention<T, D, 2, 16>(a, items, cl, st);
+    return p.nt == 1 ? launch_kv8_attention<T, D, 1>(a, B, p.items, st) : launch_kv8_attention<T, D, 2>(a, B, p.items, st);
 }
 
 template <typename T, int D> gm_status kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
@@ -332,10 +360,18 @@ gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int
                    : kv8_append<__nv_bfloat16, 128>(a, (unsigned)grid, stream);
 }
 
+size_t gm_kv8_attention_workspace_size(int B, int t, int hq, int hkv, int d, int page, int max_pages, int window, int sinks)
+{
+    if (B < 1 || t < 1 || hkv < 1 || hq < hkv || hq % hkv != 0 || d < 1 || page < 1 || max_pages < 0 || window < 1 || sinks < 0)
+        return 0;
+    return kv8_plan(B, t, hq, hkv, d, kv8_keys((int64_t)max_pages * page, window, sinks, t)).bytes;
+}
+
 gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, int hq, int hkv, int d, const void *kq,
                                    const void *vq, const float *kscale, const float *vscale, int num_pages, int page,
                                    const int32_t *table, int max_pages, const int32_t *lens, const int32_t *q_lens,
-                                   int window, int sinks, float scale, void *o, float *lse, cudaStream_t stream)
+                                   int window, int sinks, float scale, void *o, float *lse, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream)
 {
     gm::Kv8AttnArgs a{};
     const gm_status st = check_cache(a.c, const_cast<void *>(kq), const_cast<void *>(vq), const_cast<float *>(kscale),
@@ -344,6 +380,9 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
     if (window < 1 || sinks < 0 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
     if (st != GM_OK || (int64_t)B * t == 0) return st;
     if (!q || !o || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    const Kv8Plan p = kv8_plan(B, t, hq, hkv, d, kv8_keys((int64_t)max_pages * page, window, sinks, t));
+    if (p.items * p.splits >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return GM_ERR_INVALID_ARG;
     a.q = q;
     a.q_lens = q_lens;
     a.o = o;
@@ -352,15 +391,17 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
     a.hq = hq;
     a.hkv = hkv;
     a.G = hq / hkv;
+    a.tiles = p.tiles;
+    a.splits = p.splits;
+    a.part = (float *)workspace;
+    a.ml = (float2 *)((char *)workspace + p.part_bytes);
     const int64_t room = (int64_t)a.c.max_pages * page;
     a.window = (int)std::min<int64_t>(window, std::max<int64_t>(room, 1));
     a.sinks = (int)std::min<int64_t>(sinks, room);
     a.sl2 = scale * gm::LOG2E;
-    const int64_t keys = std::min<int64_t>(room, (int64_t)a.window + a.sinks);
     if (dtype == GM_F32)
-        return d == 64 ? kv8_attention<float, 64>(a, B, keys, stream) : kv8_attention<float, 128>(a, B, keys, stream);
-    return d == 64 ? kv8_attention<__nv_bfloat16, 64>(a, B, keys, stream)
-                   : kv8_attention<__nv_bfloat16, 128>(a, B, keys, stream);
+        return d == 64 ? kv8_attention<float, 64>(a, B, p, stream) : kv8_attention<float, 128>(a, B, p, stream);
+    return d == 64 ? kv8_attention<__nv_bfloat16, 64>(a, B, p, stream) : kv8_attention<__nv_bfloat16, 128>(a, B, p, stream);
 }
 
 gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, const float *w, int s, int B, int t,

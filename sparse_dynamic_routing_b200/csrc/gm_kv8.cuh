@@ -168,11 +168,17 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
 // cached tokens that the windowed attention's rule allows (t <= i, i - t < window or t < sinks).
 //
 // A call reads every visible byte of K and V once, so HBM bounds it. One row tile (up to
-// 8 NT query rows of one KV head: the group's heads times the sequence's rows) is worked on by
-// CL blocks of one cluster and their warps; each warp takes every (CL * warps)-th piece of 16
-// keys, keeps its own softmax maximum and sum, and the partial outputs are joined in shared
-// memory, across the cluster through distributed shared memory: one launch, no workspace, and
-// a fixed order of additions.
+// 8 NT query rows of one KV head: the group's heads times the sequence's rows) is split over
+// `splits` blocks of four warps; every warp takes every (4 splits)-th unit of 32 keys (two pieces
+// of 16, each inside one page), copies it into its own two-stage ring in shared memory while it
+// computes the one before, and keeps its own softmax maximum and sum. A warp's computation on a
+// unit is one long chain of dependent steps, so bandwidth comes from many warps: 12 per SM, and
+// two pieces per step (one piece per step: 1400 cycles a piece whatever the memory does). The
+// warps are joined in shared memory; with more than one split the blocks write partial outputs
+// to the workspace and a second kernel joins those, in a fixed order. (A cluster that joins
+// through distributed shared memory needs no workspace, but a GPU holds only 7 clusters of 16 such
+// blocks, and one sequence of 8 KV heads then waits for two rounds: 72 us against 35 us for 65536
+// tokens.)
 //
 // Arithmetic. mma.sync m16n8k16 with fp16 operands and fp32 sums, computed transposed
 // (S^T = K q^T, O^T = V^T P^T) so that the 16-row operand is the cache and a single token's few
@@ -193,6 +199,9 @@ struct Kv8AttnArgs {
     int t, hq, hkv, G, tiles;  // row tiles per (sequence, KV head)
     int window, sinks;
     float sl2;              // scale * log2(e)
+    int splits;             // blocks per row tile
+    float *part;            // splits > 1: [items, splits, 8 NT, D] outputs, scaled by each split's own sum
+    float2 *ml;             // [items, splits, 8 NT] maximum (base 2) and sum
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -232,50 +241,54 @@ __device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t hi)
     return pack_half2(x - f.x, y - f.y);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank()
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void *src)
 {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-    return r;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_size()
+__device__ __forceinline__ void cp_async4_at(uint32_t dst, const void *src)
 {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
-// A float of another block of the cluster, at the same shared-memory address as here.
-__device__ __forceinline__ float peer_float(const float *p, uint32_t rank)
-{
-    float v;
-    asm volatile(
-        "{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n"
-        : "=f"(v)
-        : "r"(smem_u32(p)), "r"(rank)
-        : "memory");
-    return v;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-template <int D, int NT, bool SPLIT, int W> struct Kv8Smem {
+// Four elements of a query row's output, and its lse (by the thread of column 0).
+template <typename T>
+__device__ __forceinline__ void kv8_store_row(const Kv8AttnArgs &a, size_t row, int D, int d, float4 o, float mx, float sum,
+                                              bool none)
+{
+    const float inv = none ? 0.0f : 1.0f / sum;
+    o = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>((float *)a.o + row * D + d) = o;
+    } else {
+        const __nv_bfloat162 x[2] = {__floats2bfloat162_rn(o.x, o.y), __floats2bfloat162_rn(o.z, o.w)};
+        *reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.o + row * D + d) = *reinterpret_cast<const uint2 *>(x);
+    }
+    if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mx + lg2(sum)) * LN2;
+}
+
+constexpr int KV8_W = 4;       // warps per block
+constexpr int KV8_PER_SM = 3;  // blocks per SM (shared memory: the rings)
+
+template <int D, int NT, bool SPLIT> struct Kv8Smem {
     static constexpr int ROWS = 8 * NT;
     static constexpr int QTERMS = SPLIT ? 2 : 1;
-    __half q[QTERMS][ROWS][D + 8];           // rows 4 banks apart
-    float qscale[ROWS];                      // score factor of a row (powers of two undone)
-    int pos[ROWS];                           // position, -1: no such row
-    float m[W][ROWS], l[W][ROWS];
-    float part[W][ROWS][D + 4];      // the warps' outputs
-    float cm[ROWS], cl[ROWS];                // the block's
+    union {
+        uint8_t ring[KV8_W][2][2][2][16 * D];  // [stage][piece][K, V]: rows, 16-byte chunks swizzled
+        float part[KV8_W][ROWS][D + 4];        // afterwards: the warps' outputs
+    };
+    float scales[KV8_W][2][2][2];
+    __half q[QTERMS][ROWS][D + 8];  // rows 4 banks apart
+    float qscale[ROWS];             // score factor of a row (powers of two undone)
+    int pos[ROWS];                  // position, -1: no such row
+    float m[KV8_W][ROWS], l[KV8_W][ROWS];
 };
 
-template <typename T, int D, int NT, int W>
-__global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(Kv8AttnArgs a)
 {
+    constexpr int W = KV8_W;
     constexpr bool SPLIT = sizeof(T) == 4;
-    using Smem = Kv8Smem<D, NT, SPLIT, W>;
+    using Smem = Kv8Smem<D, NT, SPLIT>;
     constexpr int ROWS = Smem::ROWS;
     constexpr int KS = D / 16;            // k steps of the scores
     constexpr int NK = D / 64;            // 16-byte chunks of a key row per lane
@@ -284,8 +297,9 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
     Smem &sm = *reinterpret_cast<Smem *>(kv8_smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    const uint32_t rank = cluster_rank(), ncl = cluster_size();
-    unsigned x = blockIdx.x / ncl;
+    unsigned x = blockIdx.x / (unsigned)a.splits;
+    const int rank = (int)(blockIdx.x - x * (unsigned)a.splits);
+    const unsigned item = x;
     const int rt = (int)(x % (unsigned)a.tiles);
     x /= (unsigned)a.tiles;
     const int h = (int)(x % (unsigned)a.hkv), b = (int)(x / (unsigned)a.hkv);
@@ -345,8 +359,8 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
         na = min((min(a.sinks, lo) + 15) >> 4, p0);
         np = na + (pmax >> 4) + 1 - p0;
     }
-    const int stride = (int)ncl * W;
-    const size_t row_bytes = (size_t)D;
+    const int nu = (np + 1) >> 1;  // units of two pieces
+    const int stride = a.splits * W;
 
     int mypos[NT][2];
     float myq[NT][2];
@@ -370,158 +384,202 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
     }
 
     const auto piece = [&](int i) { return i < na ? i : p0 + i - na; };
+    const auto raw_page = [&](int i) {  // page of piece i (0 past the end), not yet checked
+        return i < np ? __ldg(a.c.table + (size_t)b * a.c.max_pages + ((piece(i) << 4) >> a.c.shift)) : 0;
+    };
     bool bad = false;
-    const auto page_of = [&](int i) {  // a page outside the pool is read as page 0 and raises the flag
-        if (i >= np) return 0;
-        const int id = __ldg(a.c.table + (size_t)b * a.c.max_pages + ((piece(i) << 4) >> a.c.shift));
-        if (id >= 0 && id < a.c.num_pages) return id;
-        bad = true;
-        return 0;
-    };
-    uint4 kr[2][NK];      // two keys (g, g + 8), this lane's chunks
-    uint32_t vr[4][VW];   // keys 2c, 2c+1, 2c+8, 2c+9
-    float ksc = 0.0f, vsc = 0.0f;
-    const auto where = [&](int i, int id) {  // offset of the piece's first row, in rows
-        const int t0 = piece(i) << 4;
-        return (((size_t)id * a.hkv + h) << a.c.shift) + (size_t)(t0 & ((1 << a.c.shift) - 1));
-    };
-    const auto load_k = [&](int i, int id) {
-        const uint8_t *p = a.c.kq + where(i, id) * row_bytes + c * 16;
+    const uint32_t ring = smem_u32(&sm.ring[warp][0][0][0][0]);
+    constexpr int CH = D / 16;  // 16-byte chunks of a row
+    // Unit u into its stage. Chunk col of row r sits at col ^ f(r), which spreads the rows that
+    // one load instruction of the computation reads over the banks.
+    const auto issue = [&](int u, int st, const int (&ids)[2]) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int e = 0; e < NK; ++e) kr[s][e] = ld16_stream(p + (size_t)(g + 8 * s) * D + e * 64);
-        ksc = __ldg(a.c.kscale + (size_t)id * a.hkv + h);
-    };
-    const auto load_v = [&](int i, int id) {
-        const uint8_t *p = a.c.vq + where(i, id) * row_bytes + g * (D / 8);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint8_t *pr = p + (size_t)(2 * c + (s & 1) + 8 * (s >> 1)) * D;
-            if constexpr (VW == 4) {
-                const uint4 u = ld16_stream(pr);
-                vr[s][0] = u.x, vr[s][1] = u.y, vr[s][2] = u.z, vr[s][3] = u.w;
-            } else {
-                const uint2 u = __ldcs(reinterpret_cast<const uint2 *>(pr));
-                vr[s][0] = u.x, vr[s][1] = u.y;
+        for (int p = 0; p < 2; ++p) {
+            const int i = 2 * u + p;
+            int id = ids[p];
+            if (i >= np) continue;
+            if (id < 0 || id >= a.c.num_pages) {  // read page 0 and raise the flag
+                bad = true;
+                id = 0;
             }
+            const size_t blk = (size_t)id * a.hkv + h;
+            const size_t at = ((blk << a.c.shift) + (size_t)((piece(i) << 4) & ((1 << a.c.shift) - 1))) * D;
+            const uint32_t dst = ring + (st * 2 + p) * (32 * D);
+            const uint8_t *ks = a.c.kq + at + lane * 16, *vs = a.c.vq + at + lane * 16;
+#pragma unroll
+            for (int y = 0; y < CH / 2; ++y) {
+                const int x = lane + 32 * y, r = x / CH, col = x - r * CH;
+                const int fk = D == 128 ? (r & 1) * 4 : 0, fv = D == 128 ? ((r >> 1) & 3) * 2 : (r >> 1) & 3;
+                cp_async16_at(dst + r * D + (col ^ fk) * 16, ks + y * 512);
+                cp_async16_at(dst + 16 * D + r * D + (col ^ fv) * 16, vs + y * 512);
+            }
+            if (lane < 2) cp_async4_at(smem_u32(&sm.scales[warp][st][p][lane]), (lane ? a.c.vscale : a.c.kscale) + blk);
         }
-        vsc = __ldg(a.c.vscale + (size_t)id * a.hkv + h);
+        cp_async_commit();
     };
 
-    int i = (int)rank * W + warp;
-    int id = page_of(i), id_next = page_of(i + stride);
-    if (i < np) {
-        load_k(i, id);
-        load_v(i, id);
-    }
-    for (; i < np; i += stride) {
-        const int t0 = piece(i) << 4;
+    int u = rank * W + warp;
+    int ids[2] = {raw_page(2 * u), raw_page(2 * u + 1)};
+    issue(u, 0, ids);
+    ids[0] = raw_page(2 * (u + stride));
+    ids[1] = raw_page(2 * (u + stride) + 1);
+    for (int st = 0; u < nu; u += stride, st ^= 1) {
+        __syncwarp();  // every lane is done with the other stage
+        issue(u + stride, st ^ 1, ids);
+        ids[0] = raw_page(2 * (u + 2 * stride));
+        ids[1] = raw_page(2 * (u + 2 * stride) + 1);
+        cp_async_wait<1>();
+        __syncwarp();  // the unit is complete
+        // a second piece past the end starts where nothing is seen
+        const int t0[2] = {piece(2 * u) << 4, 2 * u + 1 < np ? piece(2 * u + 1) << 4 : 0x3fffffff};
+        const float kf[2] = {sm.scales[warp][st][0][0], sm.scales[warp][st][1][0]};
+        const float vf[2] = {sm.scales[warp][st][0][1], sm.scales[warp][st][1][1]};
         // S^T = K q^T
-        float s[NT][4];
+        float s[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t w0 = (&kr[0][ks >> 2].x)[ks & 3], w1 = (&kr[1][ks >> 2].x)[ks & 3];
-            const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
-            const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
-            const int d = (ks >> 2) * 64 + c * 16 + (ks & 3) * 4;
+                for (int e = 0; e < 4; ++e) s[p][n][e] = 0.0f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint2 q0 = *reinterpret_cast<const uint2 *>(&sm.q[0][n * 8 + g][d]);
-                mma_f16(s[n], a0, a1, a2, a3, q0.x, q0.y);
-                if constexpr (SPLIT) {
-                    const uint2 q1 = *reinterpret_cast<const uint2 *>(&sm.q[1][n * 8 + g][d]);
-                    mma_f16(s[n], a0, a1, a2, a3, q1.x, q1.y);
+        for (int e = 0; e < NK; ++e) {
+            uint4 kr[2][2];  // [piece][keys g, g + 8]: this lane's chunk
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    kr[p][y] = *reinterpret_cast<const uint4 *>(
+                        &sm.ring[warp][st][p][0][(g + 8 * y) * D + ((c + 4 * e) ^ (D == 128 ? (g & 1) * 4 : 0)) * 16]);
+#pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4) {
+                const int d = e * 64 + c * 16 + k4 * 4;
+                uint2 q0[NT], q1[SPLIT ? NT : 1];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    q0[n] = *reinterpret_cast<const uint2 *>(&sm.q[0][n * 8 + g][d]);
+                    if constexpr (SPLIT) q1[n] = *reinterpret_cast<const uint2 *>(&sm.q[1][n * 8 + g][d]);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const uint32_t w0 = (&kr[p][0].x)[k4], w1 = (&kr[p][1].x)[k4];
+                    const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
+                    const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(s[p][n], a0, a1, a2, a3, q0[n].x, q0[n].y);
+                        if constexpr (SPLIT) mma_f16(s[p][n], a0, a1, a2, a3, q1[n].x, q1[n].y);
+                    }
                 }
             }
         }
-        const float kf = ksc, vf = vsc;
-        const int nid = id_next;
-        if (i + stride < np) {  // the next piece's keys are on their way during the softmax
-            load_k(i + stride, nid);
-            id_next = page_of(i + 2 * stride);
-        }
-        // softmax of the piece: rows 2c + e, keys t0 + g and t0 + g + 8
-        const float lv = (float)((int)((__float_as_uint(vf) >> 23) & 255u) - 127);
-        uint32_t pt[NT][2], pl[NT][2];
+        // softmax: rows 2c + e, keys t0 + g and t0 + g + 8 of both pieces
+        float lv[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) lv[p] = (float)((int)((__float_as_uint(vf[p]) >> 23) & 255u) - 127);
+        uint32_t pt[2][NT][2], pl[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float p[4], mx[2], f[2], up[2];
-            bool see[4];
+            float mb[2], up[2][2], f[2];
+            bool see[2][4], moved = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = t0 + g + 8 * (e >> 1), ps = mypos[n][e & 1];
-                see[e] = t <= ps && (ps - t < a.window || t < a.sinks);
-                p[e] = see[e] ? s[n][e] * (myq[n][e & 1] * kf) : -INFINITY;
-            }
-            bool moved = false;
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = t0[p] + g + 8 * (e >> 1), ps = mypos[n][e & 1];
+                    see[p][e] = t <= ps && (ps - t < a.window || t < a.sinks);
+                    s[p][n][e] = see[p][e] ? s[p][n][e] * (myq[n][e & 1] * kf[p]) : -INFINITY;
+                }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                mx[e] = fmaxf(p[e], p[e + 2]);
+                float m0 = fmaxf(s[0][n][e], s[0][n][e + 2]), m1 = fmaxf(s[1][n][e], s[1][n][e + 2]);
 #pragma unroll
-                for (int sft = 4; sft < 32; sft <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(FULL, mx[e], sft));
-                const float mn = fmaxf(m[n][e], mx[e]), vn = fmaxf(mv[n][e], mx[e] + lv);
-                const float mb = mn == -INFINITY ? 0.0f : mn, vb = vn == -INFINITY ? 0.0f : vn;
-                l[n][e] *= ex2(m[n][e] - mb);
+                for (int sft = 4; sft < 32; sft <<= 1) {
+                    m0 = fmaxf(m0, __shfl_xor_sync(FULL, m0, sft));
+                    m1 = fmaxf(m1, __shfl_xor_sync(FULL, m1, sft));
+                }
+                const float mn = fmaxf(m[n][e], fmaxf(m0, m1)), vn = fmaxf(mv[n][e], fmaxf(m0 + lv[0], m1 + lv[1]));
+                const float vb = vn == -INFINITY ? 0.0f : vn;
+                mb[e] = mn == -INFINITY ? 0.0f : mn;
+                l[n][e] *= ex2(m[n][e] - mb[e]);
                 f[e] = ex2(mv[n][e] - vb);
                 moved |= vn != mv[n][e];
                 m[n][e] = mn;
                 mv[n][e] = vn;
-                mx[e] = mb;
-                up[e] = vf * ex2(mb - vb) * 0x1p14f;
+                const float x = ex2(mb[e] - vb) * 0x1p14f;
+                up[0][e] = vf[0] * x;
+                up[1][e] = vf[1] * x;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                p[e] = see[e] ? ex2(p[e] - mx[e & 1]) : 0.0f;
-                l[n][e & 1] += p[e];
-                p[e] = see[e] ? p[e] * up[e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
-            }
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = see[p][e] ? ex2(s[p][n][e] - mb[e & 1]) : 0.0f;
+                    l[n][e & 1] += x;
+                    s[p][n][e] = see[p][e] ? x * up[p][e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
+                }
             if (__any_sync(FULL, moved)) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[n][j][e] *= f[e & 1];
             }
-            const uint32_t h0 = pack_half2(p[0], p[1]), h1 = pack_half2(p[2], p[3]);
-            pt[n][0] = transpose8x8(h0);
-            pt[n][1] = transpose8x8(h1);
-            if constexpr (SPLIT) {
-                pl[n][0] = transpose8x8(pack_rest(p[0], p[1], h0));
-                pl[n][1] = transpose8x8(pack_rest(p[2], p[3], h1));
-            }
-        }
-        if (t0 + 16 > len) {  // rows past the sequence's end may hold any bytes, NaN among them
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t0 + 2 * c + (e & 1) + 8 * (e >> 1) >= len) {
-#pragma unroll
-                    for (int y = 0; y < VW; ++y) vr[e][y] = 0;
+            for (int p = 0; p < 2; ++p) {
+                const uint32_t h0 = pack_half2(s[p][n][0], s[p][n][1]), h1 = pack_half2(s[p][n][2], s[p][n][3]);
+                pt[p][n][0] = transpose8x8(h0);
+                pt[p][n][1] = transpose8x8(h1);
+                if constexpr (SPLIT) {
+                    pl[p][n][0] = transpose8x8(pack_rest(s[p][n][0], s[p][n][1], h0));
+                    pl[p][n][1] = transpose8x8(pack_rest(s[p][n][2], s[p][n][3], h1));
                 }
+            }
         }
         // O^T += V^T P^T
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {  // output columns g * (D/8) + 2j and + 2j + 1
-            // byte pairs (key, next key) of column 2j in the low half, of column 2j + 1 in the high
-            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-            const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
-            const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
-            const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
-            const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
+        for (int p = 0; p < 2; ++p) {
+            const uint8_t *vp = sm.ring[warp][st][p][1];
+            uint32_t vr[4][VW];  // keys 2c, 2c+1, 2c+8, 2c+9: columns g * (D/8) ..
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_f16(acc[n][j], a0, a1, a2, a3, pt[n][0], pt[n][1]);
-                if constexpr (SPLIT) mma_f16(acc[n][j], a0, a1, a2, a3, pl[n][0], pl[n][1]);
+            for (int y = 0; y < 4; ++y) {
+                const int r = 2 * c + (y & 1) + 8 * (y >> 1);
+                if constexpr (VW == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(vp + r * D + (g ^ (((r >> 1) & 3) * 2)) * 16);
+                    vr[y][0] = x.x, vr[y][1] = x.y, vr[y][2] = x.z, vr[y][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(vp + r * D + ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8);
+                    vr[y][0] = x.x, vr[y][1] = x.y;
+                }
+            }
+            if (t0[p] + 16 > len) {  // rows past the sequence's end may hold any bytes, NaN among them
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (t0[p] + 2 * c + (y & 1) + 8 * (y >> 1) >= len) {
+#pragma unroll
+                        for (int z = 0; z < VW; ++z) vr[y][z] = 0;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {  // output columns g * (D/8) + 2j and + 2j + 1
+                // byte pairs (key, next key) of column 2j in the low half, of column 2j + 1 in the high
+                const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
+                const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
+                const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
+                const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_f16(acc[n][j], a0, a1, a2, a3, pt[p][n][0], pt[p][n][1]);
+                    if constexpr (SPLIT) mma_f16(acc[n][j], a0, a1, a2, a3, pl[p][n][0], pl[p][n][1]);
+                }
             }
         }
-        if (i + stride < np) load_v(i + stride, nid);
     }
     if (bad && lane == 0) raise_index_error();
+    cp_async_wait<0>();
+    __syncthreads();  // the rings become the warps' outputs
 
-    // ---- join: warps in shared memory, blocks through the cluster ---------------------------
+    // ---- join the warps ---------------------------------------------------------------------
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -531,7 +589,7 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
             for (int sft = 4; sft < 32; sft <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], sft);
             if (r < nrows) {
                 // back from the values' own maximum and the weights' 2^14
-                const float u = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-14f;
+                const float x = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-14f;
                 if (g == 0) {
                     sm.m[warp][r] = m[n][e];
                     sm.l[warp][r] = l[n][e];
@@ -539,56 +597,67 @@ __global__ void __launch_bounds__(W * 32) kv8_attention_kernel(Kv8AttnArgs a)
                 float *dst = &sm.part[warp][r][g * (D / 8)];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
-                    *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(acc[n][j][e] * u, acc[n][j][2 + e] * u);
+                    *reinterpret_cast<float2 *>(dst + 2 * j) = make_float2(acc[n][j][e] * x, acc[n][j][2 + e] * x);
             }
         }
     __syncthreads();
-    for (int y = threadIdx.x; y < nrows * D; y += W * 32) {
-        const int r = y / D, d = y - r * D;
+    for (int y = threadIdx.x; y < nrows * (D / 4); y += W * 32) {
+        const int r = y / (D / 4), d = (y - r * (D / 4)) * 4;
         float mx = sm.m[0][r];
 #pragma unroll
         for (int w = 1; w < W; ++w) mx = fmaxf(mx, sm.m[w][r]);
         const float mb = mx == -INFINITY ? 0.0f : mx;
-        float o = 0.0f, sum = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const float f = ex2(sm.m[w][r] - mb);
-            o += sm.part[w][r][d] * f;
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.part[w][r][d]);
+            o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
             sum += sm.l[w][r] * f;
         }
-        // only this thread reads or writes column d of row r; m and l are rewritten elsewhere
-        sm.part[0][r][d] = o;
-        if (d == 0) {
-            sm.cm[r] = mx;
-            sm.cl[r] = sum;
+        if (a.splits > 1) {
+            const size_t at = ((size_t)item * a.splits + rank) * ROWS + r;
+            *reinterpret_cast<float4 *>(a.part + at * D + d) = o;
+            if (d == 0) a.ml[at] = make_float2(mx, sum);
+        } else {
+            const int f = rt * ROWS + r, xq = f / a.G, hq = h * a.G + f - xq * a.G;
+            kv8_store_row<T>(a, ((size_t)b * a.t + xq) * a.hq + hq, D, d, o, mx, sum, sm.pos[r] < 0);
         }
     }
-    if (ncl > 1)
-        cluster_sync();
-    else
-        __syncthreads();
-    for (int y = (int)(rank * W * 32) + threadIdx.x; y < nrows * D; y += (int)ncl * W * 32) {
-        const int r = y / D, d = y - r * D;
-        float mx = -INFINITY;
-        for (uint32_t p = 0; p < ncl; ++p) mx = fmaxf(mx, peer_float(&sm.cm[r], p));
-        const float mb = mx == -INFINITY ? 0.0f : mx;
-        float o = 0.0f, sum = 0.0f;
-        for (uint32_t p = 0; p < ncl; ++p) {
-            const float f = ex2(peer_float(&sm.cm[r], p) - mb);
-            o += peer_float(&sm.part[0][r][d], p) * f;
-            sum += peer_float(&sm.cl[r], p) * f;
+}
+
+// Joins the splits of every row tile: one warp per row, its lanes across D.
+template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_join_kernel(Kv8AttnArgs a, int64_t rows)
+{
+    constexpr int ROWS = 8 * NT;
+    pdl_wait();
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // (b, x, hq)
+    const int lane = threadIdx.x & 31, d = lane * 4;
+    if (row >= rows) return;
+    const int64_t bx = row / a.hq;
+    const int hq = (int)(row - bx * a.hq), h = hq / a.G;
+    const int64_t b = bx / a.t;
+    const int f = (int)(bx - b * a.t) * a.G + hq - h * a.G;  // row of the (sequence, KV head)
+    const size_t at = (((size_t)(b * a.hkv + h) * a.tiles + f / ROWS) * a.splits) * ROWS + f % ROWS;
+    float mx = -INFINITY;
+    for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, a.ml[at + (size_t)s * ROWS].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+    const float mb = mx == -INFINITY ? 0.0f : mx;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 ml = a.ml[at + (size_t)s * ROWS];
+        const float w = ex2(ml.x - mb);
+        sum += ml.y * w;
+        if (d < D) {
+            const float4 v = *reinterpret_cast<const float4 *>(a.part + (at + (size_t)s * ROWS) * D + d);
+            o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
         }
-        const int f = rt * ROWS + r, xq = f / a.G, hq = h * a.G + f - xq * a.G;
-        const size_t row = ((size_t)b * a.t + xq) * a.hq + hq;
-        const bool none = sm.pos[r] < 0;
-        const float out = none ? 0.0f : o / sum;
-        if constexpr (SPLIT)
-            ((float *)a.o)[row * D + d] = out;
-        else
-            ((__nv_bfloat16 *)a.o)[row * D + d] = __float2bfloat16_rn(out);
-        if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mx + lg2(sum)) * LN2;
     }
-    if (ncl > 1) cluster_sync();  // the blocks' shared memory outlives its readers
+    if (d < D) kv8_store_row<T>(a, (size_t)row, D, d, o, mx, sum, sum == 0.0f);
 }
 
 // ---- sparse edge attention over the cache -----------------------------------------------------------

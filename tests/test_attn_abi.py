@@ -69,7 +69,7 @@ def append(lib, **kw):
 
 def attention(lib, **kw):
     a = dict(q=FAKE, dtype=bnd.GM_BF16, B=1, t=1, hq=4, hkv=2, d=64, **CACHE, ql=NULL, window=3, sinks=0, scale=0.1,
-             o=FAKE + 8, lse=NULL, stream=NULL)
+             o=FAKE + 8, lse=NULL, ws=NULL, size=0, stream=NULL)
     a.update(kw)
     return lib.gm_kv8_attention_forward(*a.values())
 
@@ -106,3 +106,14 @@ def test_cache_own_arguments(lib):
         assert sea(lib, **kw) == bnd.GM_ERR_INVALID_ARG
     assert append(lib, k=NULL) == bnd.GM_ERR_INVALID_ARG
     assert append(lib, k=FAKE, v=FAKE + 2) == bnd.GM_ERR_INVALID_ARG
+
+
+def test_cache_workspace(lib):
+    size = lib.gm_kv8_attention_workspace_size
+    assert size(512, 1, 16, 8, 128, 64, 4, 1 << 30, 0) == 0  # many rows of few keys: nothing to join
+    need = size(1, 1, 16, 8, 128, 64, 1024, 1 << 30, 0)
+    assert need > 0
+    a = dict(maxp=1024, page=64, d=128, hq=16, hkv=8, window=1 << 30, o=FAKE)
+    for kw in (dict(ws=NULL, size=need), dict(ws=FAKE, size=need - 1), dict(ws=FAKE + 4, size=need)):
+        assert attention(lib, **a, **kw) == bnd.GM_ERR_INVALID_ARG
+    assert size(0, 1, 16, 8, 128, 64, 4, 1, 0) == 0 and size(1, 1, 3, 2, 128, 64, 4, 1, 0) == 0

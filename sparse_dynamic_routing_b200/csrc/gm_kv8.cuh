@@ -221,12 +221,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-// Two e4m3 bytes (bits 0-15) as fp16 values, exactly. One instruction at half rate; building the
-// same bits with shifts takes four (the decode of 64 sequences of 8192 tokens: 162 against 100 us).
-__device__ __forceinline__ uint32_t half2_of(uint32_t two)
+// The two low / high e4m3 bytes of a word as fp16 values, exactly. The conversion runs at half
+// rate; building the same bits with shifts and masks takes four such instructions.
+__device__ __forceinline__ uint32_t half2_lo(uint32_t w)
 {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+    uint32_t h;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(h) : "r"(w));
+    return h;
+}
+__device__ __forceinline__ uint32_t half2_hi(uint32_t w)
+{
+    uint32_t h;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}\n" : "=r"(h) : "r"(w));
+    return h;
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float x, float y)
@@ -463,8 +470,8 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     const uint32_t w0 = (&kr[p][0].x)[k4], w1 = (&kr[p][1].x)[k4];
-                    const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
-                    const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
+                    const uint32_t a0 = half2_lo(w0), a2 = half2_hi(w0);
+                    const uint32_t a1 = half2_lo(w1), a3 = half2_hi(w1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         mma_f16(s[p][n], a0, a1, a2, a3, q0[n].x, q0[n].y);
@@ -565,8 +572,8 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
                 const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
                 const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
                 const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
-                const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
-                const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
+                const uint32_t a0 = half2_lo(x), a1 = half2_hi(x);
+                const uint32_t a2 = half2_lo(y), a3 = half2_hi(y);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     mma_f16(acc[n][j], a0, a1, a2, a3, pt[p][n][0], pt[p][n][1]);
@@ -849,8 +856,8 @@ __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const uint32_t w0 = (&kr[p][0][ks >> 2].x)[ks & 3], w1 = (&kr[p][1][ks >> 2].x)[ks & 3];
-                    const uint32_t a0 = half2_of(w0 & 0xffffu), a2 = half2_of(w0 >> 16);
-                    const uint32_t a1 = half2_of(w1 & 0xffffu), a3 = half2_of(w1 >> 16);
+                    const uint32_t a0 = half2_lo(w0), a2 = half2_hi(w0);
+                    const uint32_t a1 = half2_lo(w1), a3 = half2_hi(w1);
                     mma_f16(z[p], a0, a1, a2, a3, qh[ks][0], qh[ks][1]);
                     if constexpr (SPLIT) mma_f16(z[p], a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
                 }
@@ -916,8 +923,8 @@ __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
                     const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
                     const uint32_t x = __byte_perm(vr[p][0][j >> 1], vr[p][1][j >> 1], sel);
                     const uint32_t y = __byte_perm(vr[p][2][j >> 1], vr[p][3][j >> 1], sel);
-                    const uint32_t a0 = half2_of(x & 0xffffu), a1 = half2_of(x >> 16);
-                    const uint32_t a2 = half2_of(y & 0xffffu), a3 = half2_of(y >> 16);
+                    const uint32_t a0 = half2_lo(x), a1 = half2_hi(x);
+                    const uint32_t a2 = half2_lo(y), a3 = half2_hi(y);
                     mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
                     mma_f16(acc[j], a0, a1, a2, a3, r0, r1);
                 }

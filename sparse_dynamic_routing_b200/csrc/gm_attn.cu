@@ -250,9 +250,8 @@ template <typename T, int D, int NT> gm_status launch_kv8_attention(const gm::Kv
     if (!raise_smem(kern, sizeof(Smem))) return GM_ERR_CUDA;
     kern<<<(unsigned)(items * a.splits), gm::KV8_W * 32, sizeof(Smem), st>>>(a);
     if (a.splits > 1) {
-        const int64_t rows = (int64_t)B * a.t * a.hq;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+        cfg.gridDim = dim3((unsigned)((int64_t)B * a.t * a.hq));
         cfg.blockDim = dim3(128);
         cfg.stream = st;
         cudaLaunchAttribute attr[1];
@@ -260,7 +259,7 @@ template <typename T, int D, int NT> gm_status launch_kv8_attention(const gm::Kv
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        (void)cudaLaunchKernelEx(&cfg, gm::kv8_join_kernel<T, D, NT>, a, rows);
+        (void)cudaLaunchKernelEx(&cfg, gm::kv8_join_kernel<T, D, NT>, a);
     }
     return launched();
 }
@@ -270,15 +269,21 @@ template <typename T, int D> gm_status kv8_attention(const gm::Kv8AttnArgs &a, i
     return p.nt == 1 ? launch_kv8_attention<T, D, 1>(a, B, p.items, st) : launch_kv8_attention<T, D, 2>(a, B, p.items, st);
 }
 
+template <typename T, int D, int NP> gm_status launch_kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
+{
+    constexpr int smem = 4 * (int)sizeof(gm::Kv8SeaSmem<T, D, NP>);
+    auto kern = gm::kv8_sea_kernel<T, D, NP>;
+    if (!raise_smem(kern, smem)) return GM_ERR_CUDA;
+    // as many warps as the GPU holds at once, each taking step after step
+    const int per_sm = std::max(1, std::min(4, (227 * 1024) / (smem + 1024)));
+    const int64_t steps = a.tiles * ((a.G + 7) / 8);
+    kern<<<(unsigned)std::min<int64_t>((steps + 3) / 4, 148 * per_sm), 128, smem, st>>>(a, GM_CHECKED);
+    return launched();
+}
+
 template <typename T, int D> gm_status kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
 {
-    // up to 16 warps per SM, each taking tile after tile
-    const unsigned grid = (unsigned)std::min<int64_t>((a.tiles + 3) / 4, 148 * 4);
-    if (a.s <= 16)
-        gm::kv8_sea_kernel<T, D, 1><<<grid, 128, 0, st>>>(a, GM_CHECKED);
-    else
-        gm::kv8_sea_kernel<T, D, 2><<<grid, 128, 0, st>>>(a, GM_CHECKED);
-    return launched();
+    return a.s <= 16 ? launch_kv8_sea<T, D, 1>(a, st) : launch_kv8_sea<T, D, 2>(a, st);
 }
 
 }  // namespace

@@ -634,28 +634,33 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
     }
 }
 
-// Joins the splits of every row tile: one warp per row, its lanes across D.
-template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_join_kernel(Kv8AttnArgs a, int64_t rows)
+// Joins the splits of every row tile: one block per row, its warps taking splits in turn, lanes
+// across D.
+template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_join_kernel(Kv8AttnArgs a)
 {
     constexpr int ROWS = 8 * NT;
-    pdl_wait();
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);  // (b, x, hq)
-    const int lane = threadIdx.x & 31, d = lane * 4;
-    if (row >= rows) return;
+    __shared__ float4 so[4][D / 4];
+    __shared__ float sm[4], sl[4];
+    const int64_t row = blockIdx.x;  // (b, x, hq)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = lane * 4;
     const int64_t bx = row / a.hq;
     const int hq = (int)(row - bx * a.hq), h = hq / a.G;
     const int64_t b = bx / a.t;
     const int f = (int)(bx - b * a.t) * a.G + hq - h * a.G;  // row of the (sequence, KV head)
     const size_t at = (((size_t)(b * a.hkv + h) * a.tiles + f / ROWS) * a.splits) * ROWS + f % ROWS;
+    pdl_wait();
     float mx = -INFINITY;
-    for (int s = lane; s < a.splits; s += 32) mx = fmaxf(mx, a.ml[at + (size_t)s * ROWS].x);
+    for (int s = warp * 32 + lane; s < a.splits; s += 128) mx = fmaxf(mx, a.ml[at + (size_t)s * ROWS].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+    if (lane == 0) sm[warp] = mx;
+    __syncthreads();
+    mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
     const float mb = mx == -INFINITY ? 0.0f : mx;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
+    for (int s = warp; s < a.splits; s += 4) {
         const float2 ml = a.ml[at + (size_t)s * ROWS];
         const float w = ex2(ml.x - mb);
         sum += ml.y * w;
@@ -664,7 +669,17 @@ template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_
             o.x += v.x * w, o.y += v.y * w, o.z += v.z * w, o.w += v.w * w;
         }
     }
-    if (d < D) kv8_store_row<T>(a, (size_t)row, D, d, o, mx, sum, sum == 0.0f);
+    if (d < D) so[warp][lane] = o;
+    if (lane == 0) sl[warp] = sum;
+    __syncthreads();
+    if (warp > 0 || d >= D) return;
+    sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+        const float4 v = so[w][lane];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    kv8_store_row<T>(a, (size_t)row, D, d, o, mx, sum, sum == 0.0f);
 }
 
 // ---- sparse edge attention over the cache -----------------------------------------------------------
@@ -678,9 +693,12 @@ template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_
 // the rows' own diagonal blocks are masked away; the tensor cores have the time. Against fp32
 // multiplications on the gathered bytes this takes a fifth of the instructions, which had been
 // the bound. Weights enter as two fp16 terms (22 bits; the second costs a tile 8 of its 24 mma),
-// so the output's rounding is the only one that shows. Each lane resolves one slot of the next tile (edge -> page -> row of the pool,
-// scales: a chain of dependent loads) while the current tile is computed. Weights get a power of
-// two per query row that puts the largest product of weight and value scale at 2^14.
+// so the output's rounding is the only one that shows. Weights get a power of two per query row
+// that puts the largest product of weight and value scale at 2^14.
+//
+// A slot's chain of dependent loads (edge -> page -> scales) is walked one step per tile, three
+// tiles ahead, one lane per slot; the rows themselves and the queries are copied into the warp's
+// two-stage buffer in shared memory while the tile before them is computed.
 
 struct Kv8SeaArgs {
     Kv8 c;
@@ -698,257 +716,339 @@ struct Kv8SeaArgs {
     float sl2;             // scale * log2(e)
 };
 
-// What one slot of a row adds: its row of the pool (NONE: inactive), score factor, ln w, value scale.
+// A slot on its way: (1) its edge and its sequence's length, (2) its page, (3) its scales.
+struct Kv8Edge {
+    float w;
+    int t, len, x, ql, b;  // target; the sequence's length, the query row, the sequence's query rows
+    uint32_t h;
+};
+struct Kv8Paged {
+    float w;
+    int t, id;
+    uint32_t h;
+};
+// What a slot adds: its row of the pool (NONE: inactive), score factor, weight, value scale.
 struct Kv8Slot {
     static constexpr uint32_t NONE = 0xffffffffu;
     uint32_t row;
-    float zs, lw, vs;
+    float ks, w, vs;
 };
 
-__device__ __forceinline__ Kv8Slot kv8_slot(const Kv8SeaArgs &a, int64_t at, int j, bool report, int checked)
+__device__ __forceinline__ Kv8Edge kv8_edge(const Kv8SeaArgs &a, bool in, int64_t at, int j)
 {
-    Kv8Slot s{Kv8Slot::NONE, 0.0f, 0.0f, 0.0f};
-    if (at >= a.rows || j >= a.s) return s;
+    Kv8Edge s{0.0f, 0, 0, 0, 0, 0, 0};  // no slot: as a row of an empty sequence
+    if (!in || at >= a.rows || j >= a.s) return s;
     const uint32_t row = (uint32_t)at;  // rows < 2^31
-    const uint32_t bx = a.div_h.div(row), h = row - bx * a.div_h.d;
-    const uint32_t b = a.div_t.div(bx), x = bx - b * a.div_t.d;
-    const float w = __ldg(a.w + (size_t)row * a.s + j);
-    const int t = __ldg(a.idx + (size_t)row * a.s + j);
-    int len = __ldg(a.c.lens + b);
-    const int ql = a.q_lens ? min(max(__ldg(a.q_lens + b), 0), a.t) : a.t;
+    const uint32_t bx = a.div_h.div(row);
+    s.h = row - bx * a.div_h.d;
+    s.b = (int)a.div_t.div(bx);
+    s.x = (int)(bx - (uint32_t)s.b * a.div_t.d);
+    s.w = __ldg(a.w + (size_t)row * a.s + j);
+    s.t = __ldg(a.idx + (size_t)row * a.s + j);
+    s.len = __ldg(a.c.lens + s.b);
+    s.ql = a.q_lens ? __ldg(a.q_lens + s.b) : a.t;
+    return s;
+}
+
+__device__ __forceinline__ Kv8Paged kv8_paged(const Kv8SeaArgs &a, const Kv8Edge &e, bool report, int checked)
+{
+    Kv8Paged s{0.0f, e.t, 0, e.h};
     const int64_t room = (int64_t)a.c.max_pages << a.c.shift;
+    int len = e.len;
     if (len < 0 || len > room) {
         if (report) raise_index_error();
         len = len < 0 ? 0 : (int)room;
     }
-    const int pos = (int)x < ql ? len - ql + (int)x : -1;
+    const int ql = min(max(e.ql, 0), a.t), pos = e.x < ql ? len - ql + e.x : -1;
     if (checked && report && pos >= 0) {
-        const bool bad_w = !(w >= 0.0f) || isinf(w);
-        if (bad_w || (w > 0.0f && t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
+        const bool bad_w = !(e.w >= 0.0f) || isinf(e.w);
+        if (bad_w || (e.w > 0.0f && e.t > pos)) atomicOr(&g_error_flag, ERR_EDGE_INVALID);
     }
-    if (pos < 0 || !(w > 0.0f)) return s;
-    int id = -1;
-    if (t >= 0 && t < len) id = __ldg(a.c.table + (size_t)b * a.c.max_pages + (t >> a.c.shift));
-    if (id < 0 || id >= a.c.num_pages) {
+    if (pos < 0 || !(e.w > 0.0f)) return s;
+    if (e.t < 0 || e.t >= len) {
         if (report) raise_index_error();
         return s;
     }
-    const uint32_t blk = (uint32_t)id * (uint32_t)a.hkv + h;  // pool rows < 2^32
-    s.row = (blk << a.c.shift) + (uint32_t)(t & ((1 << a.c.shift) - 1));
-    s.zs = __ldg(a.c.kscale + blk) * a.sl2;
-    s.vs = __ldg(a.c.vscale + blk);
-    s.lw = lg2(w);
+    s.w = e.w;
+    s.id = __ldg(a.c.table + (size_t)e.b * a.c.max_pages + (e.t >> a.c.shift));
     return s;
 }
+
+__device__ __forceinline__ Kv8Slot kv8_slot(const Kv8SeaArgs &a, const Kv8Paged &p, bool report)
+{
+    Kv8Slot s{Kv8Slot::NONE, 0.0f, 1.0f, 0.0f};
+    if (p.w == 0.0f) return s;
+    if (p.id < 0 || p.id >= a.c.num_pages) {
+        if (report) raise_index_error();
+        return s;
+    }
+    const uint32_t blk = (uint32_t)p.id * (uint32_t)a.hkv + p.h;  // pool rows < 2^32
+    s.row = (blk << a.c.shift) + (uint32_t)(p.t & ((1 << a.c.shift) - 1));
+    s.ks = __ldg(a.c.kscale + blk);
+    s.vs = __ldg(a.c.vscale + blk);
+    s.w = p.w;
+    return s;
+}
+
+template <typename T, int D, int NP> struct Kv8SeaSmem {  // of one warp
+    uint8_t k[2][NP][16 * D], v[2][NP][16 * D];  // 16-byte chunks swizzled as in the attention's ring
+    T q[2][8 * D];                               // chunk x of row r at x ^ (r & 1)
+};
 
 // NP: pieces of 16 slots per row (2 for more than 16 slots).
 template <typename T, int D, int NP>
 __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
 {
     constexpr bool SPLIT = sizeof(T) == 4;
-    constexpr int VEC = Vec<T>::N, KS = D / 16, NK = D / 64, VW = D / 32;
-    constexpr int QV = 16 / VEC;  // 16-byte vectors of 16 query elements
+    constexpr int VEC = Vec<T>::N, KS = D / 16, NK = D / 64, VW = D / 32, CH = D / 16;
+    constexpr int QC = D / VEC;   // 16-byte chunks of a query row
+    constexpr int QV = 16 / VEC;  // of 16 query elements
+    extern __shared__ __align__(16) unsigned char kv8_smem[];
+    auto &sm = reinterpret_cast<Kv8SeaSmem<T, D, NP> *>(kv8_smem)[threadIdx.x >> 5];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int64_t step = (int64_t)gridDim.x * 4;
-    int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (tile >= a.tiles) return;
-    // slot `lane & 15` of a tile: row (lane & 15) >> s_shift (at most 16 slots per piece)
+    // steps: tiles, and within a tile the groups of eight heads
+    const int hg = (a.G + 7) / 8;
+    const int64_t nstep = a.tiles * hg, stride = (int64_t)gridDim.x * 4;
+    int64_t it = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (it >= nstep) return;
+    // slot `lane & 15` of a tile: row (lane & 15) >> ssh (at most 16 slots per piece)
     const int ssh = min(a.s_shift, 4), sr = (lane & 15) >> ssh, sj = (lane & 15) & ((1 << ssh) - 1);
-    const auto resolve = [&](int64_t ti, Kv8Slot (&s)[NP]) {
+    const auto tile_of = [&](int64_t i) { return hg == 1 ? i : i / hg; };
+    const auto first = [&](int64_t i) { return hg == 1 || i % hg == 0; };  // errors are raised once per tile
+
+    Kv8Edge edge[NP];
+    Kv8Paged paged[NP];
+    Kv8Slot slot[NP], cur[NP];
+    const auto step1 = [&](int64_t i) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) edge[p] = kv8_edge(a, i < nstep && sr < a.rt, tile_of(i) * a.rt + sr, p * 16 + sj);
+    };
+    const auto step2 = [&](int64_t i) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) paged[p] = kv8_paged(a, edge[p], lane < 16 && first(i), checked);
+    };
+    const auto step3 = [&](int64_t i) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) slot[p] = kv8_slot(a, paged[p], lane < 16 && first(i));
+    };
+    // column n of step i: row n >> g_shift of the tile, head g0 + (n & (2^g_shift - 1))
+    const auto column = [&](int64_t i, int n, int64_t &row, int &head) {
+        const int64_t ti = tile_of(i);
+        row = ti * a.rt + (n >> a.g_shift);
+        head = (int)(i - ti * hg) * 8 + (n & ((1 << a.g_shift) - 1));
+        return (n >> a.g_shift) < a.rt && row < a.rows && head < a.G;
+    };
+    const auto issue = [&](int64_t i, int st) {  // `slot` is step i's
+        if (i < nstep) {
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int y = 0; y < CH / 2; ++y) {
+                    const int x = lane + 32 * y, r = x / CH, col = x - r * CH;
+                    const uint32_t row = __shfl_sync(FULL, slot[p].row, r);
+                    const bool on = row != Kv8Slot::NONE;  // an inactive slot's rows are zeros
+                    const size_t at = on ? (size_t)row * D + col * 16 : 0;
+                    const int fk = D == 128 ? (r & 1) * 4 : 0, fv = D == 128 ? ((r >> 1) & 3) * 2 : (r >> 1) & 3;
+                    cp_async16_zfill(&sm.k[st][p][r * D + (col ^ fk) * 16], a.c.kq + at, on);
+                    cp_async16_zfill(&sm.v[st][p][r * D + (col ^ fv) * 16], a.c.vq + at, on);
+                }
+#pragma unroll
+            for (int y = 0; y < QC / 4; ++y) {
+                const int x = lane + 32 * y, n = x / QC, col = x - n * QC;
+                int64_t row;
+                int head;
+                const bool in = column(i, n, row, head);
+                cp_async16_zfill(&sm.q[st][n * D + (col ^ (n & 1)) * VEC],
+                                 (const T *)a.q + (in ? ((size_t)row * a.G + head) * D + col * VEC : 0), in);
+            }
+        }
+        cp_async_commit();
+    };
+
+    step1(it);
+    step2(it);
+    step3(it);
+    issue(it, 0);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) cur[p] = slot[p];
+    step1(it + stride);
+    step2(it + stride);
+    step3(it + stride);
+    step1(it + 2 * stride);
+    step2(it + 2 * stride);
+    step1(it + 3 * stride);
+    for (int st = 0; it < nstep; it += stride, st ^= 1) {
+        __syncwarp();  // every lane is done with the other stage
+        issue(it + stride, st ^ 1);
+        Kv8Slot after[NP];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) after[p] = slot[p];
+        step3(it + 2 * stride);
+        step2(it + 3 * stride);
+        step1(it + 4 * stride);
+        cp_async_wait<1>();
+        __syncwarp();  // the step's rows are complete
+
+        // ---- queries: column g, scaled into fp16 --------------------------------------------------
+        uint32_t qh[KS][2], ql[SPLIT ? KS : 1][2];
+        float qdown;
+        {
+            uint4 x[NK][QV];
+            float big = 0.0f;
+#pragma unroll
+            for (int e = 0; e < NK; ++e)
+#pragma unroll
+                for (int y = 0; y < QV; ++y) {
+                    x[e][y] = *reinterpret_cast<const uint4 *>(
+                        &sm.q[st][g * D + (((e * 64 + c * 16) / VEC + y) ^ (g & 1)) * VEC]);
+                    float f[VEC];
+                    unpack<T>(x[e][y], f);
+#pragma unroll
+                    for (int z = 0; z < VEC; ++z) big = fmaxf(big, fabsf(f[z]));
+                }
+            big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
+            const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+            qdown = __uint_as_float((uint32_t)(127 - 14 + e2) << 23) * a.sl2;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                float f[VEC];
+                unpack<T>(x[ks >> 2][(ks & 3) * 4 / VEC], f);
+                const int o = (ks & 3) * 4 % VEC;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float lo = f[o + 2 * y] * up, hi = f[o + 2 * y + 1] * up;
+                    qh[ks][y] = pack_half2(lo, hi);
+                    if constexpr (SPLIT) ql[ks][y] = pack_rest(lo, hi, qh[ks][y]);
+                }
+            }
+        }
+        // ---- scores of slots g, g + 8 for columns 2c, 2c + 1 ------------------------------------
+        float z[NP][4];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            s[p] = Kv8Slot{Kv8Slot::NONE, 0.0f, 0.0f, 0.0f};
-            if (ti < a.tiles && sr < a.rt) s[p] = kv8_slot(a, ti * a.rt + sr, p * 16 + sj, lane < 16, checked);
-        }
-    };
-    Kv8Slot next[NP];
-    resolve(tile, next);
-    for (; tile < a.tiles; tile += step) {
-        Kv8Slot cur[NP];
+            uint4 kr[2][NK];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) cur[p] = next[p];
-        const int64_t row0 = tile * a.rt;
-        for (int g0 = 0; g0 < a.G; g0 += 8) {
-            // ---- loads: K rows of slots g, g + 8; V rows of slots 2c, 2c+1, 2c+8, 2c+9; q of column g
-            uint4 kr[NP][2][NK];
-            uint32_t vr[NP][4][VW];
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const uint32_t r = __shfl_sync(FULL, cur[p].row, g + 8 * s);
-#pragma unroll
-                    for (int e = 0; e < NK; ++e) {
-                        kr[p][s][e] = make_uint4(0, 0, 0, 0);
-                        if (r != Kv8Slot::NONE) kr[p][s][e] = ld16(a.c.kq + (size_t)r * D + c * 16 + e * 64);
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t r = __shfl_sync(FULL, cur[p].row, 2 * c + (s & 1) + 8 * (s >> 1));
-#pragma unroll
-                    for (int e = 0; e < VW; ++e) vr[p][s][e] = 0;
-                    if (r != Kv8Slot::NONE) {
-                        const uint8_t *src = a.c.vq + (size_t)r * D + g * (D / 8);
-                        if constexpr (VW == 4) {
-                            const uint4 u = ld16(src);
-                            vr[p][s][0] = u.x, vr[p][s][1] = u.y, vr[p][s][2] = u.z, vr[p][s][3] = u.w;
-                        } else {
-                            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src));
-                            vr[p][s][0] = u.x, vr[p][s][1] = u.y;
-                        }
-                    }
-                }
-            }
-            // column n of the tile: row n >> g_shift, head g0 + (n & (2^g_shift - 1))
-            const auto column = [&](int n, int64_t &row, int &head) {
-                row = row0 + (n >> a.g_shift);
-                head = g0 + (n & ((1 << a.g_shift) - 1));
-                return (n >> a.g_shift) < a.rt && row < a.rows && head < a.G;
-            };
-            uint32_t qh[KS][2], ql[SPLIT ? KS : 1][2];
-            float qdown;
-            {
-                int64_t row;
-                int head;
-                const bool in = column(g, row, head);
-                const T *src = (const T *)a.q + ((size_t)row * a.G + head) * D + c * 16;
-                uint4 u[NK][QV];
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int e = 0; e < NK; ++e)
+                    kr[y][e] = *reinterpret_cast<const uint4 *>(
+                        &sm.k[st][p][(g + 8 * y) * D + ((c + 4 * e) ^ (D == 128 ? (g & 1) * 4 : 0)) * 16]);
 #pragma unroll
-                    for (int y = 0; y < QV; ++y) u[e][y] = in ? ld16(src + e * 64 + y * VEC) : make_uint4(0, 0, 0, 0);
-                float big = 0.0f;
+            for (int e = 0; e < 4; ++e) z[p][e] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < NK; ++e)
-#pragma unroll
-                    for (int y = 0; y < QV; ++y) {
-                        float f[VEC];
-                        unpack<T>(u[e][y], f);
-#pragma unroll
-                        for (int z = 0; z < VEC; ++z) big = fmaxf(big, fabsf(f[z]));
-                    }
-                big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
-                const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 127);
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
-                qdown = __uint_as_float((uint32_t)(127 - 14 + e2) << 23);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    float f[VEC];
-                    unpack<T>(u[ks >> 2][(ks & 3) * 4 / VEC], f);
-                    const int o = (ks & 3) * 4 % VEC;
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float lo = f[o + 2 * y] * up, hi = f[o + 2 * y + 1] * up;
-                        qh[ks][y] = pack_half2(lo, hi);
-                        if constexpr (SPLIT) ql[ks][y] = pack_rest(lo, hi, qh[ks][y]);
-                    }
-                }
-            }
-            if (g0 == 0) resolve(tile + step, next);
-            // ---- scores of slots g, g + 8 for columns 2c, 2c + 1 --------------------------------
-            float z[NP][4];
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[p][e] = 0.0f;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const uint32_t w0 = (&kr[p][0][ks >> 2].x)[ks & 3], w1 = (&kr[p][1][ks >> 2].x)[ks & 3];
-                    const uint32_t a0 = half2_lo(w0), a2 = half2_hi(w0);
-                    const uint32_t a1 = half2_lo(w1), a3 = half2_hi(w1);
-                    mma_f16(z[p], a0, a1, a2, a3, qh[ks][0], qh[ks][1]);
-                    if constexpr (SPLIT) mma_f16(z[p], a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
-                }
-            }
-            const float qd[2] = {__shfl_sync(FULL, qdown, 8 * c), __shfl_sync(FULL, qdown, 8 * c + 4)};
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, mu[2] = {0.0f, 0.0f}, vs[NP][2];
-            bool see[NP][4];
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int k = g + 8 * s;
-                    const bool on = __shfl_sync(FULL, cur[p].row, k) != Kv8Slot::NONE;
-                    const float zs = __shfl_sync(FULL, cur[p].zs, k), lw = __shfl_sync(FULL, cur[p].lw, k);
-                    vs[p][s] = __shfl_sync(FULL, cur[p].vs, k);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        see[p][2 * s + e] = on && (k >> ssh) == ((2 * c + e) >> a.g_shift);
-                        z[p][2 * s + e] = see[p][2 * s + e] ? fmaf(z[p][2 * s + e], qd[e] * zs, lw) : -INFINITY;
-                        m[e] = fmaxf(m[e], z[p][2 * s + e]);
-                    }
-                }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
-#pragma unroll
-            for (int p = 0; p < NP; ++p)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = ex2(z[p][e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
-                    l[e & 1] += x;
-                    z[p][e] = see[p][e] ? x * vs[p][e >> 1] : 0.0f;
-                    mu[e & 1] = fmaxf(mu[e & 1], z[p][e]);
-                }
-            float up[2], inv[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    l[e] += __shfl_xor_sync(FULL, l[e], o);
-                    mu[e] = fmaxf(mu[e], __shfl_xor_sync(FULL, mu[e], o));
-                }
-                const int e2 = min(max((int)(__float_as_uint(mu[e]) >> 23) - 127, -100), 127);
-                up[e] = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
-                // an empty row is 0, a NaN stays
-                inv[e] = l[e] == 0.0f ? 0.0f : __uint_as_float((uint32_t)(127 - 14 + e2) << 23) / l[e];
-            }
-            // ---- output ---------------------------------------------------------------------------
-            float acc[D / 16][4];
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const float p0 = z[p][0] * up[0], p1 = z[p][1] * up[1], p2 = z[p][2] * up[0], p3 = z[p][3] * up[1];
-                const uint32_t h0 = pack_half2(p0, p1), h1 = pack_half2(p2, p3);
-                const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
-                const uint32_t r0 = transpose8x8(pack_rest(p0, p1, h0)), r1 = transpose8x8(pack_rest(p2, p3, h1));
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-                    const uint32_t x = __byte_perm(vr[p][0][j >> 1], vr[p][1][j >> 1], sel);
-                    const uint32_t y = __byte_perm(vr[p][2][j >> 1], vr[p][3][j >> 1], sel);
-                    const uint32_t a0 = half2_lo(x), a1 = half2_hi(x);
-                    const uint32_t a2 = half2_lo(y), a3 = half2_hi(y);
-                    mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
-                    mma_f16(acc[j], a0, a1, a2, a3, r0, r1);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                int64_t row;
-                int head;
-                if (!column(2 * c + e, row, head)) continue;
-                const size_t ro = (size_t)row * a.G + head;  // row of o: (b, x, query head)
-                T *dst = (T *)a.o + ro * D + g * (D / 8);
-#pragma unroll
-                for (int y = 0; y < D / 8 / VEC; ++y) {
-                    float f[VEC];
-#pragma unroll
-                    for (int x = 0; x < VEC; ++x) {
-                        const int d = y * VEC + x;  // column g * (D/8) + d of the output
-                        f[x] = acc[d >> 1][(d & 1) * 2 + e] * inv[e];
-                    }
-                    *reinterpret_cast<uint4 *>(dst + y * VEC) = pack<T>(f);
-                }
-                if (a.lse && g == 0) a.lse[ro] = l[e] == 0.0f ? -INFINITY : (m[e] + lg2(l[e])) * LN2;
+            for (int ks = 0; ks < KS; ++ks) {
+                const uint32_t w0 = (&kr[0][ks >> 2].x)[ks & 3], w1 = (&kr[1][ks >> 2].x)[ks & 3];
+                const uint32_t a0 = half2_lo(w0), a2 = half2_hi(w0);
+                const uint32_t a1 = half2_lo(w1), a3 = half2_hi(w1);
+                mma_f16(z[p], a0, a1, a2, a3, qh[ks][0], qh[ks][1]);
+                if constexpr (SPLIT) mma_f16(z[p], a0, a1, a2, a3, ql[ks][0], ql[ks][1]);
             }
         }
+        const float qd[2] = {__shfl_sync(FULL, qdown, 8 * c), __shfl_sync(FULL, qdown, 8 * c + 4)};
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, mu[2] = {0.0f, 0.0f}, vs[NP][2];
+        bool see[NP][4];
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float mylw = lg2(cur[p].w);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = g + 8 * s;
+                const bool on = __shfl_sync(FULL, cur[p].row, k) != Kv8Slot::NONE;
+                const float ks = __shfl_sync(FULL, cur[p].ks, k), lw = __shfl_sync(FULL, mylw, k);
+                vs[p][s] = __shfl_sync(FULL, cur[p].vs, k);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    see[p][2 * s + e] = on && (k >> ssh) == ((2 * c + e) >> a.g_shift);
+                    z[p][2 * s + e] = see[p][2 * s + e] ? fmaf(z[p][2 * s + e], qd[e] * ks, lw) : -INFINITY;
+                    m[e] = fmaxf(m[e], z[p][2 * s + e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(FULL, m[e], o));
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = ex2(z[p][e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
+                l[e & 1] += x;
+                z[p][e] = see[p][e] ? x * vs[p][e >> 1] : 0.0f;
+                mu[e & 1] = fmaxf(mu[e & 1], z[p][e]);
+            }
+        float up[2], inv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                l[e] += __shfl_xor_sync(FULL, l[e], o);
+                mu[e] = fmaxf(mu[e], __shfl_xor_sync(FULL, mu[e], o));
+            }
+            const int e2 = min(max((int)(__float_as_uint(mu[e]) >> 23) - 127, -100), 127);
+            up[e] = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+            // an empty row is 0, a NaN stays
+            inv[e] = l[e] == 0.0f ? 0.0f : __uint_as_float((uint32_t)(127 - 14 + e2) << 23) / l[e];
+        }
+        // ---- output ---------------------------------------------------------------------------------
+        float acc[D / 16][4];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            uint32_t vr[4][VW];  // slots 2c, 2c+1, 2c+8, 2c+9: columns g * (D/8) ..
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = 2 * c + (y & 1) + 8 * (y >> 1);
+                if constexpr (VW == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(&sm.v[st][p][r * D + (g ^ (((r >> 1) & 3) * 2)) * 16]);
+                    vr[y][0] = x.x, vr[y][1] = x.y, vr[y][2] = x.z, vr[y][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(
+                        &sm.v[st][p][r * D + ((g >> 1) ^ ((r >> 1) & 3)) * 16 + (g & 1) * 8]);
+                    vr[y][0] = x.x, vr[y][1] = x.y;
+                }
+            }
+            const float p0 = z[p][0] * up[0], p1 = z[p][1] * up[1], p2 = z[p][2] * up[0], p3 = z[p][3] * up[1];
+            const uint32_t h0 = pack_half2(p0, p1), h1 = pack_half2(p2, p3);
+            const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+            const uint32_t r0 = transpose8x8(pack_rest(p0, p1, h0)), r1 = transpose8x8(pack_rest(p2, p3, h1));
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+                const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
+                const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
+                const uint32_t a0 = half2_lo(x), a1 = half2_hi(x);
+                const uint32_t a2 = half2_lo(y), a3 = half2_hi(y);
+                mma_f16(acc[j], a0, a1, a2, a3, b0, b1);
+                mma_f16(acc[j], a0, a1, a2, a3, r0, r1);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            int64_t row;
+            int head;
+            if (!column(it, 2 * c + e, row, head)) continue;
+            const size_t ro = (size_t)row * a.G + head;  // row of o: (b, x, query head)
+            T *dst = (T *)a.o + ro * D + g * (D / 8);
+#pragma unroll
+            for (int y = 0; y < D / 8 / VEC; ++y) {
+                float f[VEC];
+#pragma unroll
+                for (int x = 0; x < VEC; ++x) {
+                    const int d = y * VEC + x;  // column g * (D/8) + d of the output
+                    f[x] = acc[d >> 1][(d & 1) * 2 + e] * inv[e];
+                }
+                *reinterpret_cast<uint4 *>(dst + y * VEC) = pack<T>(f);
+            }
+            if (a.lse && g == 0) a.lse[ro] = l[e] == 0.0f ? -INFINITY : (m[e] + lg2(l[e])) * LN2;
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) cur[p] = after[p];
     }
 }
 

@@ -151,10 +151,10 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
     a.w.nblk = (w.n + gm::UW - 1) / gm::UW;
     a.npad = a.w.nblk * gm::UW;
     const int64_t rows = (int64_t)w.B * a.npad * w.hq;
-    float *nl = w.delta, *delta = w.delta + rows;
+    float *nl = w.delta, *ndelta = w.delta + rows;
     a.nl = nl;
-    a.delta = delta;
-    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(a, nl, delta);
+    a.ndelta = ndelta;
+    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(a, nl, ndelta);
     kq<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hq), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdq, a);
     kkv<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hkv), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdk, tdv, a);
     return launched();

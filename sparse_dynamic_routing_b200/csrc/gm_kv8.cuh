@@ -508,12 +508,12 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
                 const float mn = fmaxf(m[n][e], fmaxf(m0, m1)), vn = fmaxf(mv[n][e], fmaxf(m0 + lv[0], m1 + lv[1]));
                 const float vb = vn == -INFINITY ? 0.0f : vn;
                 mb[e] = mn == -INFINITY ? 0.0f : mn;
-                l[n][e] *= ex2(m[n][e] - mb[e]);
-                f[e] = ex2(mv[n][e] - vb);
+                l[n][e] *= ex2_ftz(m[n][e] - mb[e]);
+                f[e] = ex2_ftz(mv[n][e] - vb);
                 moved |= vn != mv[n][e];
                 m[n][e] = mn;
                 mv[n][e] = vn;
-                const float x = ex2(mb[e] - vb) * 0x1p14f;
+                const float x = ex2_ftz(mb[e] - vb) * 0x1p14f;
                 up[0][e] = vf[0] * x;
                 up[1][e] = vf[1] * x;
             }
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = see[p][e] ? ex2(s[p][n][e] - mb[e & 1]) : 0.0f;
+                    const float x = see[p][e] ? ex2_ftz(s[p][n][e] - mb[e & 1]) : 0.0f;
                     l[n][e & 1] += x;
                     s[p][n][e] = see[p][e] ? x * up[p][e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
                 }
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
             for (int sft = 4; sft < 32; sft <<= 1) l[n][e] += __shfl_xor_sync(FULL, l[n][e], sft);
             if (r < nrows) {
                 // back from the values' own maximum and the weights' 2^14
-                const float x = m[n][e] == -INFINITY ? 0.0f : ex2(mv[n][e] - m[n][e]) * 0x1p-14f;
+                const float x = m[n][e] == -INFINITY ? 0.0f : ex2_ftz(mv[n][e] - m[n][e]) * 0x1p-14f;
                 if (g == 0) {
                     sm.m[warp][r] = m[n][e];
                     sm.l[warp][r] = l[n][e];
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float f = ex2(sm.m[w][r] - mb);
+            const float f = ex2_ftz(sm.m[w][r] - mb);
             const float4 v = *reinterpret_cast<const float4 *>(&sm.part[w][r][d]);
             o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
             sum += sm.l[w][r] * f;
@@ -662,7 +662,7 @@ template <typename T, int D, int NT> __global__ void __launch_bounds__(128) kv8_
 #pragma unroll 4
     for (int s = warp; s < a.splits; s += 4) {
         const float2 ml = a.ml[at + (size_t)s * ROWS];
-        const float w = ex2(ml.x - mb);
+        const float w = ex2_ftz(ml.x - mb);
         sum += ml.y * w;
         if (d < D) {
             const float4 v = *reinterpret_cast<const float4 *>(a.part + (at + (size_t)s * ROWS) * D + d);
@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(128) kv8_sea_kernel(Kv8SeaArgs a, int checked)
         for (int p = 0; p < NP; ++p)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = ex2(z[p][e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
+                const float x = ex2_ftz(z[p][e] - (m[e & 1] == -INFINITY ? 0.0f : m[e & 1]));
                 l[e & 1] += x;
                 z[p][e] = see[p][e] ? x * vs[p][e >> 1] : 0.0f;
                 mu[e & 1] = fmaxf(mu[e & 1], z[p][e]);

@@ -32,7 +32,7 @@ struct WinBwdArgs {
     WinArgs w;          // w.scale: scale * log2(e) (never 0)
     float scale;
     const float *nl;    // [B, hq, npad]
-    const float *delta;
+    const float *ndelta;  // -delta
     int npad;
 };
 
@@ -53,8 +53,8 @@ template <int D> struct WinBwdGeom {
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
-// nl and delta of every row; D/8 lanes per row.
-template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdArgs a, float *nl, float *delta)
+// nl and -delta of every row; D/8 lanes per row.
+template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdArgs a, float *nl, float *ndelta)
 {
     constexpr int C = D / 8, RPB = 256 / C;
     const WinArgs &w = a.w;
@@ -78,7 +78,7 @@ template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdA
     if (in && c == 0) {
         const size_t to = ((size_t)b * w.hq + hq) * a.npad + i;
         nl[to] = valid ? -LOG2E * __ldg(w.lse_in + ((size_t)b * w.n + i) * w.hq + hq) : -INFINITY;
-        delta[to] = x;
+        ndelta[to] = -x;
     }
 }
 
@@ -277,7 +277,7 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
         const bool valid = i < len;
         const size_t st = ((size_t)b * a.hq + hq) * ba.npad + i;  // i < npad
-        const float nl = valid ? __ldg(ba.nl + st) : 0.0f, dl = valid ? __ldg(ba.delta + st) : 0.0f;
+        const float nl = valid ? __ldg(ba.nl + st) : 0.0f, dl = valid ? __ldg(ba.ndelta + st) : 0.0f;
         const float sl2 = a.scale;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
@@ -302,9 +302,11 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 if (c < nch) {
                     const uint32_t mask = whole ? 0xffffffffu : column_mask(c0 + c * 32, lo, hi, a.sinks - t0);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float p = ex2(fmaf(__uint_as_float(s[c][e]), sl2, nl));
-                        s[c][e] = __float_as_uint(p);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                                    make_float2(sl2, sl2), make_float2(nl, nl));
+                        s[c][e] = __float_as_uint(ex2_ftz(x.x));
+                        s[c][e + 1] = __float_as_uint(ex2_ftz(x.y));
                     }
                     if (!whole) {
 #pragma unroll
@@ -328,14 +330,14 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         // hidden keys: P is 0, and their dP (a row that holds anything) is dropped
-                        const float p0 = __uint_as_float(s[c][2 * e]), p1 = __uint_as_float(s[c][2 * e + 1]);
-                        float y0 = p0 * (__uint_as_float(d[c][2 * e]) - dl);
-                        float y1 = p1 * (__uint_as_float(d[c][2 * e + 1]) - dl);
+                        const float2 p = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                        float2 y = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
+                                                            make_float2(dl, dl)));
                         if (!whole) {
-                            y0 = p0 == 0.0f ? 0.0f : y0;
-                            y1 = p1 == 0.0f ? 0.0f : y1;
+                            y.x = p.x == 0.0f ? 0.0f : y.x;
+                            y.y = p.y == 0.0f ? 0.0f : y.y;
                         }
-                        x[e] = bf16_pair(y0, y1);
+                        x[e] = bf16_pair(y.x, y.y);
                     }
                     umma::tmem_st16(tp + c * 16, x);
                 }
@@ -442,7 +444,7 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
         for (int j = 0; ok && j < nt; ++j) {
             const int s3 = j % NQ, s2 = j % ND, g = j / nq, i0 = t0 + (j - g * nq) * UW, hq = h * a.G + g;
             const float *nl = ba.nl + ((size_t)b * a.hq + hq) * ba.npad + i0;
-            const float *dl = ba.delta + ((size_t)b * a.hq + hq) * ba.npad + i0;
+            const float *dl = ba.ndelta + ((size_t)b * a.hq + hq) * ba.npad + i0;
             const bool fix = i0 + UW > len && len < a.n;  // dK and dV sum over these rows
             if (lane == 0 && j >= NQ) ok = mbar_wait(q_empty + 8 * s3, ((j / NQ) - 1) & 1);
             if (lane == 0 && ok && j >= ND) ok = mbar_wait(do_empty + 8 * s2, ((j / ND) - 1) & 1);
@@ -540,10 +542,14 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float4 y = nl[c * 8 + e];
-                    s[c][4 * e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][4 * e]), sl2, y.x)));
-                    s[c][4 * e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][4 * e + 1]), sl2, y.y)));
-                    s[c][4 * e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][4 * e + 2]), sl2, y.z)));
-                    s[c][4 * e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][4 * e + 3]), sl2, y.w)));
+                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                 make_float2(sl2, sl2), make_float2(y.x, y.y));
+                    const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                 make_float2(sl2, sl2), make_float2(y.z, y.w));
+                    s[c][4 * e] = __float_as_uint(ex2_ftz(x0.x));
+                    s[c][4 * e + 1] = __float_as_uint(ex2_ftz(x0.y));
+                    s[c][4 * e + 2] = __float_as_uint(ex2_ftz(x1.x));
+                    s[c][4 * e + 3] = __float_as_uint(ex2_ftz(x1.y));
                 }
                 if (!whole) {
 #pragma unroll
@@ -571,11 +577,15 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                 uint32_t x[16];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float4 y = dl[c * 8 + e];
-                    x[2 * e] = bf16_pair(__uint_as_float(s[c][4 * e]) * (__uint_as_float(d[c][4 * e]) - y.x),
-                                         __uint_as_float(s[c][4 * e + 1]) * (__uint_as_float(d[c][4 * e + 1]) - y.y));
-                    x[2 * e + 1] = bf16_pair(__uint_as_float(s[c][4 * e + 2]) * (__uint_as_float(d[c][4 * e + 2]) - y.z),
-                                             __uint_as_float(s[c][4 * e + 3]) * (__uint_as_float(d[c][4 * e + 3]) - y.w));
+                    const float4 y = dl[c * 8 + e];  // -delta
+                    const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                 __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e]), __uint_as_float(d[c][4 * e + 1])),
+                                                            make_float2(y.x, y.y)));
+                    const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                 __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e + 2]), __uint_as_float(d[c][4 * e + 3])),
+                                                            make_float2(y.z, y.w)));
+                    x[2 * e] = bf16_pair(x0.x, x0.y);
+                    x[2 * e + 1] = bf16_pair(x1.x, x1.y);
                 }
                 umma::tmem_st16(tP + lane_off + c0 + c * 16, x);
             }

@@ -8,6 +8,10 @@
 //   warps 0-3, 4-7  softmax of tile 0, 1 (and their output)
 //   warp 8          TMA loads: Q once, then K and V through separate stages
 //   warp 9          MMA issue
+// A thread reads its scores twice, 32 columns at a time, once for the maximum and once for the
+// exponentials: 128 of them kept in registers spill, and TMEM has the bandwidth.
+// P is handed over in two halves, so that the first half's products run under the second half's
+// exponentials.
 // TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).
 //
 // The running maximum is allowed to lag: O is rescaled only when a row's maximum has grown by
@@ -23,6 +27,8 @@
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "gm_common.cuh"
 #include "gm_umma.cuh"
@@ -40,7 +46,7 @@ template <int D> struct WinFwdGeom {
     static constexpr int OFF_K = 2 * TILE;
     static constexpr int OFF_V = OFF_K + NST * TILE;
     static constexpr int OFF_BAR = OFF_V + NST * TILE;
-    static constexpr int NBAR = 2 + 4 * NST + 2 + 2 + 2 + 1;
+    static constexpr int NBAR = 2 + 4 * NST + 2 + 4 + 2 + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr int THREADS = 320;
 };
@@ -87,7 +93,7 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     const uint32_t sq = base, sk = base + Geo::OFF_K, sv = base + Geo::OFF_V, sb = base + Geo::OFF_BAR;
     const uint32_t q_full = sb, tail = sb + 8, k_full = sb + 16, k_empty = k_full + 8 * NST;
     const uint32_t v_full = k_empty + 8 * NST, v_empty = v_full + 8 * NST, s_full = v_empty + 8 * NST;
-    const uint32_t p_full = s_full + 16, o_full = p_full + 16, mma_done = o_full + 16, tslot = mma_done + 8;
+    const uint32_t p_full = s_full + 16, o_full = p_full + 32, mma_done = o_full + 16, tslot = mma_done + 8;
     const uint32_t *tslot_p = reinterpret_cast<const uint32_t *>(sm + Geo::OFF_BAR + Geo::NBAR * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -139,7 +145,8 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full + 8 * t, 1);
-            mbar_init(p_full + 8 * t, UW);
+            mbar_init(p_full + 16 * t, UW);
+            mbar_init(p_full + 16 * t + 8, UW);
             mbar_init(o_full + 8 * t, 1);
         }
         mbar_init(mma_done, 1);
@@ -232,13 +239,17 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                 ok = mbar_wait(v_full + 8 * s, (j / NST) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (ok) ok = mbar_wait(p_full + 8 * t, j & 1);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (ok) ok = mbar_wait(p_full + 16 * t + 8 * half, j & 1);
+                        if (!ok) break;
+                        umma::fence_after_sync();
+                        for (int ks = half * 4; ks < min(w / 16, half * 4 + 4); ++ks)  // O_t += P_t V_j
+                            umma::mma_bf16_ta(tmem + 2 * UW + t * D, tmem + t * UW + ks * 8,
+                                              umma::sdesc_sw128_mnmajor(sv + s * TILE + ks * 2048, UATOM), idesc_pv,
+                                              j > 0 || ks > 0);
+                    }
                     if (!ok) break;
-                    umma::fence_after_sync();
-                    for (int ks = 0; ks < w / 16; ++ks)  // O_t += P_t V_j
-                        umma::mma_bf16_ta(tmem + 2 * UW + t * D, tmem + t * UW + ks * 8,
-                                          umma::sdesc_sw128_mnmajor(sv + s * TILE + ks * 2048, UATOM), idesc_pv,
-                                          j > 0 || ks > 0);
                     if (t == 1) umma::commit(v_empty + 8 * s);
                     if (n > 0) {
                         if (t == 0) {
@@ -274,83 +285,98 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             if (!ok) break;
             umma::fence_after_sync();
             const int t0 = kb.start(j, UW), t1 = kb.end(j, UW), nch = (t1 - t0 + 31) / 32;
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < nch) umma::tmem_ld32(ts + c * 32, s[c]);
-            umma::tmem_wait_ld();
-            const bool whole = ((t1 - t0) & 31) == 0 && t1 - 1 <= it && it + UW <= len &&
+            const bool whole = t1 - t0 == UW && t1 - 1 <= it && it + UW <= len &&
                                (t0 > it + UW - 1 - a.window || t1 <= a.sinks);
-            if (!whole) {
-                // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
-                const int hi = valid ? min(i, t1 - 1) - t0 : -1;
-                const int lo = i - a.window + 1 - t0;
+            const auto block = [&](auto all) {
+                constexpr bool ALL = decltype(all)::value;  // every row sees all 128 keys
+                uint32_t s[2][32], mask[4];
+                if constexpr (!ALL) {
+                    // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
+                    const int hi = valid ? min(i, t1 - 1) - t0 : -1;
+                    const int lo = i - a.window + 1 - t0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < nch) {
-                        const uint32_t mask = column_mask(c * 32, lo, hi, a.sinks - t0);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((mask >> e) & 1)) s[c][e] = __float_as_uint(hide);
-                    }
-            }
-            float mx = hide;
-            if (sl2 > 0.0f) {
+                    for (int c = 0; c < 4; ++c) mask[c] = column_mask(c * 32, lo, hi, a.sinks - t0);
+                }
+                const auto hidden = [&](int c, int e) { return !ALL && !((mask[c] >> e) & 1); };
                 float m4[4] = {hide, hide, hide, hide};
+                umma::tmem_ld32(ts, s[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (c < nch) {
+                    if (ALL || c < nch) {
+                        uint32_t(&x)[32] = s[c & 1];
+                        umma::tmem_wait_ld32(x);
+                        if (ALL ? c < 3 : c + 1 < nch) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                        if constexpr (!ALL) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(s[c][e]));
+                            for (int e = 0; e < 32; ++e)
+                                if (hidden(c, e)) x[e] = __float_as_uint(hide);
+                        }
+                        if (sl2 > 0.0f) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                m4[(e >> 1) & 3] = fmaxf(fmaxf(m4[(e >> 1) & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) m4[e & 3] = fminf(m4[e & 3], __uint_as_float(x[e]));
+                        }
                     }
-                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            } else {
+                float mx = sl2 > 0.0f ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))
+                                      : fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
+                mx *= sl2;
+                const bool grow = mx > m + 8.0f;
+                if (__any_sync(FULL, grow)) {
+                    const float f = grow ? ex2_ftz(m - mx) : 1.0f;  // the first visible block: 2^-inf = 0
+                    if (grow) m = mx;
+                    l *= f;
+                    if (j > 0) {
+                        // S_t(j) was issued after P_t(j-1) V, so O_t is at rest until this block's P
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            umma::tmem_ld32(to + c * 32, o);
+                            umma::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c < nch) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fminf(mx, __uint_as_float(s[c][e]));
-                    }
-            }
-            mx *= sl2;
-            const bool grow = mx > m + 8.0f;
-            if (__any_sync(FULL, grow)) {
-                const float f = grow ? ex2(m - mx) : 1.0f;  // the first visible block: ex2(-inf) = 0
-                if (grow) m = mx;
-                l *= f;
-                if (j > 0) {
-                    // S_t(j) was issued after P_t(j-1) V, so O_t is at rest until this block's P
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        umma::tmem_ld32(to + c * 32, o);
-                        umma::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        umma::tmem_st32(to + c * 32, o);
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            umma::tmem_st32(to + c * 32, o);
+                        }
                     }
                 }
-            }
-            const float nm = m == -INFINITY ? 0.0f : -m;
-            float sum[2] = {0.0f, 0.0f};
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                umma::tmem_ld32(ts, s[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < nch) {
-                    uint32_t p[16];
+                for (int c = 0; c < 4; ++c) {
+                    if (ALL || c < nch) {
+                        uint32_t p[16];
+                        uint32_t(&y)[32] = s[c & 1];
+                        umma::tmem_wait_ld32(y);
+                        // P of piece c lies over scores of pieces already read
+                        if (ALL ? c < 3 : c + 1 < nch) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(s[c][2 * e]), sl2, nm));
-                        const float p1 = ex2(fmaf(__uint_as_float(s[c][2 * e + 1]), sl2, nm));
-                        sum[0] += p0;
-                        sum[1] += p1;
-                        p[e] = bf16_pair(p0, p1);
+                        for (int e = 0; e < 16; ++e) {
+                            float2 x = make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                            x = __ffma2_rn(x, sl22, nm2);
+                            x.x = hidden(c, 2 * e) ? 0.0f : ex2_ftz(x.x);
+                            x.y = hidden(c, 2 * e + 1) ? 0.0f : ex2_ftz(x.y);
+                            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                            p[e] = bf16_pair(x.x, x.y);
+                        }
+                        umma::tmem_st16(ts + c * 16, p);
                     }
-                    umma::tmem_st16(ts + c * 16, p);
+                    if (c & 1) {  // half of the block is ready for the tensor cores
+                        umma::tmem_wait_st();
+                        umma::fence_before_sync();
+                        mbar_arrive(p_full + 16 * t + 8 * (c >> 1));
+                    }
                 }
-            l += sum[0] + sum[1];
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            mbar_arrive(p_full + 8 * t);
+                sum[0] = __fadd2_rn(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
+            };
+            if (whole)
+                block(std::true_type{});
+            else
+                block(std::false_type{});
         }
         // ---- output -----------------------------------------------------------------------
         if (ok) ok = __all_sync(FULL, mbar_wait(o_full + 8 * t, 0));

@@ -82,6 +82,15 @@ template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdA
     }
 }
 
+// Whether queries [i, i + 32) see all, some or none of keys [k0, k0 + 32). Queries past the end
+// need no mask: their P is 0 by nl.
+__device__ __forceinline__ Piece query_piece(int k0, int i, int len, int window, int sinks)
+{
+    if (i + 31 < k0 || i >= len || k0 >= len || (i > k0 + 31 + window - 1 && k0 >= sinks)) return Piece::none;
+    if (i >= k0 + 31 && (i + 31 <= k0 + window - 1 || k0 + 32 <= sinks)) return Piece::all;
+    return Piece::some;
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
@@ -296,24 +305,24 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             umma::tmem_wait_ld();
             umma::fence_before_sync();
             mbar_arrive(s_empty);
-            const int hi = valid ? min(i, t1 - 1) - t0 : -1, lo = i - a.window + 1 - t0;
+            Piece piece[2];
+            uint32_t mask[2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (c < nch) {
-                    const uint32_t mask = whole ? 0xffffffffu : column_mask(c0 + c * 32, lo, hi, a.sinks - t0);
+            for (int c = 0; c < 2; ++c) {
+                const int col = c0 + c * 32;
+                piece[c] = whole ? Piece::all : key_piece(i0 + (warp & 3) * 32, t0 + col, t1, len, a.window, a.sinks);
+                mask[c] = piece[c] == Piece::some ? column_mask(col, i - a.window + 1 - t0, valid ? min(i, t1 - 1) - t0 : -1,
+                                                                a.sinks - t0)
+                                                  : 0u;
+                if (piece[c] == Piece::none) continue;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                                                    make_float2(sl2, sl2), make_float2(nl, nl));
-                        s[c][e] = __float_as_uint(ex2_ftz(x.x));
-                        s[c][e + 1] = __float_as_uint(ex2_ftz(x.y));
-                    }
-                    if (!whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((mask >> e) & 1)) s[c][e] = 0u;
-                    }
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                                make_float2(sl2, sl2), make_float2(nl, nl));
+                    s[c][e] = __float_as_uint(ex2_ftz(x.x));
+                    s[c][e + 1] = __float_as_uint(ex2_ftz(x.y));
                 }
+            }
             ok = __all_sync(FULL, mbar_wait(dp_full + 8 * (j & 1), (j >> 1) & 1));
             if (!ok) break;
             umma::fence_after_sync();
@@ -321,26 +330,34 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             uint32_t d[2][32];
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                if (c < nch) umma::tmem_ld32(tp + c * 32, d[c]);
+                if (piece[c] != Piece::none) umma::tmem_ld32(tp + c * 32, d[c]);
             umma::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (c < nch) {
-                    uint32_t x[16];
+            for (int c = 0; c < 2; ++c) {
+                uint32_t x[16];
+                if (piece[c] == Piece::none) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e] = 0u;
+                } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        // hidden keys: P is 0, and their dP (a row that holds anything) is dropped
                         const float2 p = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
-                        float2 y = __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
-                                                            make_float2(dl, dl)));
-                        if (!whole) {
-                            y.x = p.x == 0.0f ? 0.0f : y.x;
-                            y.y = p.y == 0.0f ? 0.0f : y.y;
-                        }
+                        const float2 y =
+                            __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
+                                                     make_float2(dl, dl)));
                         x[e] = bf16_pair(y.x, y.y);
                     }
-                    umma::tmem_st16(tp + c * 16, x);
+                    if (piece[c] == Piece::some) {  // hidden keys' dS is dropped, whatever their rows held
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t lo = (mask[c] >> (2 * e)) & 1 ? 0x0000ffffu : 0u;
+                            const uint32_t hi = (mask[c] >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u;
+                            x[e] &= lo | hi;
+                        }
+                    }
                 }
+                if (c < nch) umma::tmem_st16(tp + c * 16, x);
+            }
             umma::tmem_wait_st();
             umma::fence_before_sync();
             mbar_arrive(ds_full + 8 * (j & 1));
@@ -532,33 +549,44 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             if (!ok) break;
             umma::fence_after_sync();
             const float4 *nl = reinterpret_cast<const float4 *>(sm + Geo::OFF_NL + (j % NQ) * 512) + wg * 16;
-            uint32_t s[2][32];
+            // pieces of 32 queries: which keys of the warp's 32 rows do they see?
+            Piece piece[2];
+            uint32_t mask[2], s[2][32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
+            for (int c = 0; c < 2; ++c) {
+                piece[c] = whole ? Piece::all : query_piece(t0 + (warp & 3) * 32, i0 + c0 + c * 32, len, a.window, a.sinks);
+                mask[c] = piece[c] == Piece::some ? column_mask(c0 + c * 32, t - i0, last - i0, 0) : 0u;
+                if (piece[c] != Piece::none) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
+            }
             umma::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const uint32_t mask = whole ? 0xffffffffu : column_mask(c0 + c * 32, t - i0, last - i0, 0);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 y = nl[c * 8 + e];
-                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
-                                                 make_float2(sl2, sl2), make_float2(y.x, y.y));
-                    const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
-                                                 make_float2(sl2, sl2), make_float2(y.z, y.w));
-                    s[c][4 * e] = __float_as_uint(ex2_ftz(x0.x));
-                    s[c][4 * e + 1] = __float_as_uint(ex2_ftz(x0.y));
-                    s[c][4 * e + 2] = __float_as_uint(ex2_ftz(x1.x));
-                    s[c][4 * e + 3] = __float_as_uint(ex2_ftz(x1.y));
-                }
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((mask >> e) & 1)) s[c][e] = 0u;
-                }
                 uint32_t x[16];
+                if (piece[c] == Piece::none) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = bf16_pair(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                    for (int e = 0; e < 16; ++e) x[e] = 0u;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 y = nl[c * 8 + e];
+                        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                     make_float2(sl2, sl2), make_float2(y.x, y.y));
+                        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                     make_float2(sl2, sl2), make_float2(y.z, y.w));
+                        s[c][4 * e] = __float_as_uint(ex2_ftz(x0.x));
+                        s[c][4 * e + 1] = __float_as_uint(ex2_ftz(x0.y));
+                        s[c][4 * e + 2] = __float_as_uint(ex2_ftz(x1.x));
+                        s[c][4 * e + 3] = __float_as_uint(ex2_ftz(x1.y));
+                    }
+                    if (piece[c] == Piece::some) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((mask[c] >> e) & 1)) s[c][e] = 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = bf16_pair(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                }
                 umma::tmem_st16(tS + lane_off + c0 + c * 16, x);
             }
             umma::tmem_wait_st();
@@ -567,25 +595,31 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             ok = __all_sync(FULL, mbar_wait(do_full + 8 * (j % ND), (j / ND) & 1) && mbar_wait(dp_full, j & 1));
             if (!ok) break;
             umma::fence_after_sync();
-            const float4 *dl = reinterpret_cast<const float4 *>(sm + Geo::OFF_DELTA + (j % ND) * 512) + wg * 16;
+            const float4 *dl = reinterpret_cast<const float4 *>(sm + Geo::OFF_DELTA + (j % ND) * 512) + wg * 16;  // -delta
             uint32_t d[2][32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) umma::tmem_ld32(tP + lane_off + c0 + c * 32, d[c]);
+            for (int c = 0; c < 2; ++c)
+                if (piece[c] != Piece::none) umma::tmem_ld32(tP + lane_off + c0 + c * 32, d[c]);
             umma::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t x[16];
+                if (piece[c] == Piece::none) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 y = dl[c * 8 + e];  // -delta
-                    const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
-                                                 __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e]), __uint_as_float(d[c][4 * e + 1])),
-                                                            make_float2(y.x, y.y)));
-                    const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
-                                                 __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e + 2]), __uint_as_float(d[c][4 * e + 3])),
-                                                            make_float2(y.z, y.w)));
-                    x[2 * e] = bf16_pair(x0.x, x0.y);
-                    x[2 * e + 1] = bf16_pair(x1.x, x1.y);
+                    for (int e = 0; e < 16; ++e) x[e] = 0u;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 y = dl[c * 8 + e];
+                        const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                     __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e]), __uint_as_float(d[c][4 * e + 1])),
+                                                                make_float2(y.x, y.y)));
+                        const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                     __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e + 2]), __uint_as_float(d[c][4 * e + 3])),
+                                                                make_float2(y.z, y.w)));
+                        x[2 * e] = bf16_pair(x0.x, x0.y);
+                        x[2 * e + 1] = bf16_pair(x1.x, x1.y);
+                    }
                 }
                 umma::tmem_st16(tP + lane_off + c0 + c * 16, x);
             }

@@ -28,8 +28,6 @@
 
 #include <cuda.h>
 
-#include <type_traits>
-
 #include "gm_common.cuh"
 #include "gm_umma.cuh"
 #include "gm_window.cuh"
@@ -71,6 +69,16 @@ __device__ __forceinline__ uint32_t column_mask(int base, int lo, int hi, int si
         return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u);
     };
     return below(hi + 1) & (~below(lo) | below(sink));
+}
+
+// Whether rows [r0, r0 + 32) see all, some or none of the 32 keys from t on (keys end at t1).
+enum class Piece { none, some, all };
+__device__ __forceinline__ Piece key_piece(int r0, int t, int t1, int len, int window, int sinks)
+{
+    const int last = min(r0 + 31, len - 1);  // the last row that is one
+    if (t >= t1 || t > last || (t + 31 <= r0 - window && t >= sinks)) return Piece::none;
+    if (t + 31 < t1 && t + 31 <= r0 && r0 + 31 < len && (t > r0 + 31 - window || t + 31 < sinks)) return Piece::all;
+    return Piece::some;
 }
 
 __device__ __forceinline__ void named_sync(int id, int count)
@@ -272,7 +280,7 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     } else {
         // ---- softmax: thread = query row = TMEM lane ----------------------------------------
         const int t = warp >> 2, r = (warp & 3) * 32 + lane;
-        const int it = t ? i1 : i0, i = it + r, hq = t ? hq1 : hq0;
+        const int it = t ? i1 : i0, i = it + r, hq = t ? hq1 : hq0, r0 = it + (warp & 3) * 32;
         const bool valid = i < len;
         const float sl2 = a.scale;  // log2(e) folded in by the host, never 0
         const float hide = sl2 > 0.0f ? -INFINITY : INFINITY;
@@ -287,96 +295,122 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             const int t0 = kb.start(j, UW), t1 = kb.end(j, UW), nch = (t1 - t0 + 31) / 32;
             const bool whole = t1 - t0 == UW && t1 - 1 <= it && it + UW <= len &&
                                (t0 > it + UW - 1 - a.window || t1 <= a.sinks);
-            const auto block = [&](auto all) {
-                constexpr bool ALL = decltype(all)::value;  // every row sees all 128 keys
-                uint32_t s[2][32], mask[4];
-                if constexpr (!ALL) {
-                    // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
-                    const int hi = valid ? min(i, t1 - 1) - t0 : -1;
-                    const int lo = i - a.window + 1 - t0;
+            // ---- maximum over the visible columns ------------------------------------------------
+            float m4[4] = {hide, hide, hide, hide};
+            const auto maximum = [&](const uint32_t(&x)[32]) {
+                if (sl2 > 0.0f) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) mask[c] = column_mask(c * 32, lo, hi, a.sinks - t0);
+                    for (int e = 0; e < 32; e += 2)
+                        m4[(e >> 1) & 3] = fmaxf(fmaxf(m4[(e >> 1) & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) m4[e & 3] = fminf(m4[e & 3], __uint_as_float(x[e]));
                 }
-                const auto hidden = [&](int c, int e) { return !ALL && !((mask[c] >> e) & 1); };
-                float m4[4] = {hide, hide, hide, hide};
-                umma::tmem_ld32(ts, s[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (ALL || c < nch) {
-                        uint32_t(&x)[32] = s[c & 1];
-                        umma::tmem_wait_ld32(x);
-                        if (ALL ? c < 3 : c + 1 < nch) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
-                        if constexpr (!ALL) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (hidden(c, e)) x[e] = __float_as_uint(hide);
-                        }
-                        if (sl2 > 0.0f) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                m4[(e >> 1) & 3] = fmaxf(fmaxf(m4[(e >> 1) & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) m4[e & 3] = fminf(m4[e & 3], __uint_as_float(x[e]));
-                        }
-                    }
-                float mx = sl2 > 0.0f ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))
-                                      : fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
-                mx *= sl2;
-                const bool grow = mx > m + 8.0f;
-                if (__any_sync(FULL, grow)) {
-                    const float f = grow ? ex2_ftz(m - mx) : 1.0f;  // the first visible block: 2^-inf = 0
-                    if (grow) m = mx;
-                    l *= f;
-                    if (j > 0) {
-                        // S_t(j) was issued after P_t(j-1) V, so O_t is at rest until this block's P
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            umma::tmem_ld32(to + c * 32, o);
-                            umma::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            umma::tmem_st32(to + c * 32, o);
-                        }
-                    }
-                }
-                const float nm = m == -INFINITY ? 0.0f : -m;
-                const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(nm, nm);
-                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            };
+            // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
+            const int hi = valid ? min(i, t1 - 1) - t0 : -1, lo = i - a.window + 1 - t0;
+            uint32_t s[2][32];
+            if (whole) {
                 umma::tmem_ld32(ts, s[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (ALL || c < nch) {
-                        uint32_t p[16];
-                        uint32_t(&y)[32] = s[c & 1];
-                        umma::tmem_wait_ld32(y);
-                        // P of piece c lies over scores of pieces already read
-                        if (ALL ? c < 3 : c + 1 < nch) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                    umma::tmem_wait_ld32(s[c & 1]);
+                    if (c < 3) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                    maximum(s[c & 1]);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < nch; ++c) {
+                    const Piece piece = key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks);
+                    if (piece == Piece::none) continue;
+                    umma::tmem_ld32(ts + c * 32, s[0]);
+                    umma::tmem_wait_ld32(s[0]);
+                    if (piece == Piece::some) {
+                        const uint32_t mask = column_mask(c * 32, lo, hi, a.sinks - t0);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 x = make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-                            x = __ffma2_rn(x, sl22, nm2);
-                            x.x = hidden(c, 2 * e) ? 0.0f : ex2_ftz(x.x);
-                            x.y = hidden(c, 2 * e + 1) ? 0.0f : ex2_ftz(x.y);
-                            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-                            p[e] = bf16_pair(x.x, x.y);
-                        }
-                        umma::tmem_st16(ts + c * 16, p);
+                        for (int e = 0; e < 32; ++e)
+                            if (!((mask >> e) & 1)) s[0][e] = __float_as_uint(hide);
                     }
-                    if (c & 1) {  // half of the block is ready for the tensor cores
-                        umma::tmem_wait_st();
-                        umma::fence_before_sync();
-                        mbar_arrive(p_full + 16 * t + 8 * (c >> 1));
+                    maximum(s[0]);
+                }
+            }
+            float mx = sl2 > 0.0f ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))
+                                  : fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
+            mx *= sl2;
+            const bool grow = mx > m + 8.0f;
+            if (__any_sync(FULL, grow)) {
+                const float f = grow ? ex2_ftz(m - mx) : 1.0f;  // the first visible block: 2^-inf = 0
+                if (grow) m = mx;
+                l *= f;
+                if (j > 0) {
+                    // S_t(j) was issued after P_t(j-1) V, so O_t is at rest until this block's P
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        umma::tmem_ld32(to + c * 32, o);
+                        umma::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        umma::tmem_st32(to + c * 32, o);
                     }
                 }
-                sum[0] = __fadd2_rn(sum[0], sum[1]);
-                l += sum[0].x + sum[0].y;
+            }
+            // ---- P = 2^(sl2 S - m), piece c over scores of pieces already read --------------------
+            const float nm = m == -INFINITY ? 0.0f : -m;
+            const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(nm, nm);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            const auto exponentials = [&](const uint32_t(&y)[32], uint32_t(&p)[16], uint32_t mask, bool masked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 x = make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                    x = __ffma2_rn(x, sl22, nm2);
+                    x.x = ex2_ftz(x.x);
+                    x.y = ex2_ftz(x.y);
+                    if (masked) {
+                        x.x = (mask >> (2 * e)) & 1 ? x.x : 0.0f;
+                        x.y = (mask >> (2 * e + 1)) & 1 ? x.y : 0.0f;
+                    }
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    p[e] = bf16_pair(x.x, x.y);
+                }
             };
-            if (whole)
-                block(std::true_type{});
-            else
-                block(std::false_type{});
+            const auto hand_over = [&](int half) {  // half of the block is ready for the tensor cores
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                mbar_arrive(p_full + 16 * t + 8 * half);
+            };
+            uint32_t p[16];
+            if (whole) {
+                umma::tmem_ld32(ts, s[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    umma::tmem_wait_ld32(s[c & 1]);
+                    if (c < 3) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                    exponentials(s[c & 1], p, 0, false);
+                    umma::tmem_st16(ts + c * 16, p);
+                    if (c & 1) hand_over(c >> 1);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const Piece piece = key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks);
+                    if (piece != Piece::none) {
+                        umma::tmem_ld32(ts + c * 32, s[0]);
+                        umma::tmem_wait_ld32(s[0]);
+                        if (piece == Piece::all)
+                            exponentials(s[0], p, 0, false);
+                        else
+                            exponentials(s[0], p, column_mask(c * 32, lo, hi, a.sinks - t0), true);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = 0;
+                    }
+                    if (c < nch) umma::tmem_st16(ts + c * 16, p);
+                    if (c & 1) hand_over(c >> 1);
+                }
+            }
+            sum[0] = __fadd2_rn(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
         }
         // ---- output -----------------------------------------------------------------------
         if (ok) ok = __all_sync(FULL, mbar_wait(o_full + 8 * t, 0));

@@ -82,16 +82,16 @@ template <int D> gm_status window_backward(gm::WinArgs a, cudaStream_t st)
 }
 
 // A bf16 feature tensor [B, n, heads, d] as a 4-d TMA map whose boxes are 64 elements of d (128
-// bytes, the swizzle width) x 1 head x 128 rows of one sequence; rows past n read as zeros and are
+// bytes, the swizzle width) x 1 head x box_rows rows of one sequence; rows past n read as zeros and are
 // not written.
-bool sequence_tmap(CUtensorMap &m, const void *ptr, int B, int n, int heads, int d)
+bool sequence_tmap(CUtensorMap &m, const void *ptr, int B, int n, int heads, int d, int box_rows = gm::UW)
 {
     const EncodeTiledFn f = encode_tiled();
     if (f == nullptr) return false;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n, (cuuint64_t)B};
     const cuuint64_t row = (cuuint64_t)heads * d * 2;
     const cuuint64_t strides[3] = {(cuuint64_t)d * 2, row, row * n};
-    const cuuint32_t box[4] = {64, 1, gm::UW, 1};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return f(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -120,15 +120,15 @@ template <int D> gm_status window_forward_bf16(gm::WinArgs a, cudaStream_t st)
 {
     using Geo = gm::WinFwdGeom<D>;
     CUtensorMap tq, tk, tv, to;
-    if (!sequence_tmap(tq, a.q, a.B, a.n, a.hq, D) || !sequence_tmap(tk, a.k, a.B, a.n, a.hkv, D) ||
-        !sequence_tmap(tv, a.v, a.B, a.n, a.hkv, D) || !sequence_tmap(to, a.o, a.B, a.n, a.hq, D))
+    if (!sequence_tmap(tq, a.q, a.B, a.n, a.hq, D) || !sequence_tmap(tk, a.k, a.B, a.n, a.hkv, D, gm::FK) ||
+        !sequence_tmap(tv, a.v, a.B, a.n, a.hkv, D, gm::FK) || !sequence_tmap(to, a.o, a.B, a.n, a.hq, D))
         return GM_ERR_CUDA;
     auto kern = gm::win_fwd_umma_kernel<D>;
     if (!raise_smem(kern, Geo::SMEM)) return GM_ERR_CUDA;
     gm::WinPairs wp;
-    const int64_t grid = window_pairs(a, wp);
+    wp.items = window_pairs(a, wp);
     a.scale = base2_scale(a.scale);
-    kern<<<(unsigned)grid, Geo::THREADS, Geo::SMEM, st>>>(tq, tk, tv, to, a, wp);
+    kern<<<(unsigned)std::min<int64_t>(wp.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tk, tv, to, a, wp);
     return launched();
 }
 

@@ -261,6 +261,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     return true;
 }
 
+// The same wait by a whole warp: true in every lane, or false in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity)
+{
+    return __all_sync(FULL, mbar_wait(bar, parity)) != 0;
+}
+
 // Dot product of a 16-byte chunk of q (as fp32 pairs) with a chunk of k: even and odd
 // elements accumulate separately with packed fp32x2 FMAs, then the two halves are added.
 // Every SEA kernel uses this same order, so all paths give identical bits.

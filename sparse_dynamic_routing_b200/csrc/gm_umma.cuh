@@ -49,14 +49,56 @@ __host__ __device__ constexpr uint64_t sdesc_sw128_mnmajor(uint32_t smem_addr, u
 
 #if defined(__CUDACC__)
 
-// A in TMEM: lane = row of A, 32-bit column c = the bf16 pair (2c, 2c + 1) along K.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate)
+// ---- MMA issue by a whole warp -----------------------------------------------------------------
+//
+// The functions below are executed by all lanes of a warp and act in the lane whose `lead` is not
+// 0. Nothing branches on the lane, so operands that are the same in every lane stay in uniform
+// registers, where the MMA instruction wants them: issued under `if (lane == 0)` each one first
+// moves its descriptors there, 100 to 140 cycles per instruction instead of the 64 that a
+// 128 x 128 x 16 product takes. Descriptors are given as their low word (sdesc_lo plus an offset in
+// 16-byte units) and their high word, the same for every operand here.
+
+__device__ __forceinline__ uint32_t elect_lead()
+{
+    uint32_t lead;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
+    return lead;
+}
+
+constexpr uint32_t SDESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // as in sdesc_sw128_*
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t smem_addr, uint32_t block_bytes)
+{
+    return (smem_addr >> 4) | ((block_bytes >> 4) << 16);
+}
+constexpr uint32_t KMAJOR = 16;  // block_bytes of a K-major operand: the field reads 1
+
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%2, %6};\n mov.b64 db, {%3, %6};\n"
+        " setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %0, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%1], da, db, %4, p;\n}\n" ::"r"(lead),
+        "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        : "memory");
+}
+// A in TMEM: lane = row of A, 32-bit column c = the bf16 pair (2c, 2c + 1) along K.
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 db;\n mov.b64 db, {%3, %6};\n"
+        " setp.ne.b32 p, %5, 0;\n setp.ne.b32 q, %0, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], db, %4, p;\n}\n" ::"r"(lead),
+        "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(SDESC_HI)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %0, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(lead),
+        "r"(bar)
         : "memory");
 }
 
@@ -110,6 +152,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr)
         : "memory");
 }
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+        "%13, %14, %15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // 32 consecutive 32-bit columns of this thread's TMEM lane written; completes at tmem_wait_st.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {

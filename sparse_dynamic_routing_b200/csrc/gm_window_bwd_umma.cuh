@@ -98,57 +98,28 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Whole warp: zeroes rows [first, 128) of a 128 x D tile and makes that visible to the tensor cores.
-template <int NA> __device__ __forceinline__ void zero_rows(uint8_t *tile, int first, int lane)
-{
-    const int per = (UW - first) * 8;
-    for (int y = lane; y < NA * per; y += 32) {
-        const int at = y / per, z = y - at * per;
-        *reinterpret_cast<uint4 *>(tile + at * UATOM + first * 128 + z * 16) = make_uint4(0, 0, 0, 0);
-    }
-}
-
-// A x B^T of two K-major 128 x D / n x D tiles into TMEM at `d`.
-template <int D> __device__ __forceinline__ void mma_tiles(uint32_t d, uint32_t sa, uint32_t sbt, int n)
+// Whole warp: A x B^T of two K-major tiles (128 x D and n x D) into TMEM at `d`; the descriptors'
+// low words.
+template <int D> __device__ __forceinline__ void mma_tiles(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo, int n)
 {
     const uint32_t idesc = umma::idesc_bf16_f32(UW, n);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = (ks / 4) * UATOM + (ks % 4) * 32;
-        umma::mma_bf16(d, umma::sdesc_sw128_kmajor(sa + off), umma::sdesc_sw128_kmajor(sbt + off), idesc, ks > 0);
+        const uint32_t off = ((ks / 4) * UATOM + (ks % 4) * 32) >> 4;
+        umma::mma_ss(lead, d, a_lo + off, b_lo + off, idesc, ks > 0);
     }
 }
 
-// TMEM operand (bf16 pairs: columns 0-63 at +0, columns 64-127 at +64) x rows [0, k) of a tile
-// taken MN-major, added to the D columns at `d`.
-template <int D> __device__ __forceinline__ void mma_accumulate(uint32_t d, uint32_t ta, uint32_t sbt, int k, bool add)
+// Whole warp: TMEM operand (bf16 pairs: columns 0-63 at +0, columns 64-127 at +64) x rows [0, k) of
+// a tile taken MN-major, added to the D columns at `d`. k: a multiple of 32.
+template <int D>
+__device__ __forceinline__ void mma_accumulate(uint32_t lead, uint32_t d, uint32_t ta, uint32_t b_lo, int k, bool add)
 {
     constexpr uint32_t idesc = umma::idesc_bf16_f32_bmn(UW, D);
-    for (int ks = 0; ks < k / 16; ++ks)
-        umma::mma_bf16_ta(d, ta + (ks < 4 ? ks * 8 : 64 + (ks - 4) * 8), umma::sdesc_sw128_mnmajor(sbt + ks * 2048, UATOM),
-                          idesc, add || ks > 0);
-}
-
-// This thread's row of a TMEM accumulator (columns [c0, c1) of 32s), times f, as bf16 into a
-// swizzled tile; zeros where `keep` is false.
-__device__ __forceinline__ void stage_row(uint8_t *tile, uint32_t taddr, int r, int c0, int c1, float f, bool keep)
-{
-#pragma unroll 1
-    for (int c = c0; c < c1; ++c) {
-        uint32_t o[32];
-        umma::tmem_ld32(taddr + c * 32, o);
-        umma::tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t x[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                x[y] = keep ? bf16_pair(__uint_as_float(o[e * 8 + 2 * y]) * f, __uint_as_float(o[e * 8 + 2 * y + 1]) * f)
-                            : 0u;
-            *reinterpret_cast<uint4 *>(tile + (c / 2) * UATOM + r * 128 + ((((c & 1) * 4 + e) ^ (r & 7)) * 16)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
-        }
-    }
+    for (int ks = 0; ks < 8; ++ks)
+        if (ks < 2 || ks * 16 < k)
+            umma::mma_ts(lead, d, ta + (ks < 4 ? ks * 8 : 64 + (ks - 4) * 8), b_lo + (ks * 2048 >> 4), idesc, add || ks > 0);
 }
 
 template <int D>
@@ -233,7 +204,7 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
             if (fix) {
                 ok = __all_sync(FULL, mbar_wait(tail, 0));
-                if (ok) zero_rows<NA>(sm + Geo::OFF_3 + s3 * TILE, max(len - t0, 0), lane);
+                if (ok) zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(len - t0, 0), lane);
                 umma::fence_proxy_async();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(k_full + 8 * s3);
@@ -251,37 +222,39 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             for (int s = 0; s < NV; ++s) mbar_wait(v_full + 8 * s, 0);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            const auto width = [&](int j) { return (kb.end(j, UW) - kb.start(j, UW) + 31) & ~31; };
-            const auto first = [&](int j) {  // S(j), then dP(j)
-                const int n = width(j);
-                bool ok = mbar_wait(k_full + 8 * (j % NK), (j / NK) & 1);
-                if (ok && j > 0) ok = mbar_wait(s_empty, (j - 1) & 1);
-                if (!ok) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(tS, sq, sk + (j % NK) * TILE, n);
-                umma::commit(s_full);
-                ok = mbar_wait(v_full + 8 * (j % NV), (j / NV) & 1);
-                if (!ok) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(tP + (j & 1) * 128, sdo, sv + (j % NV) * TILE, n);
-                umma::commit(dp_full + 8 * (j & 1));
-                umma::commit(v_empty + 8 * (j % NV));
-                return true;
-            };
-            bool ok = mbar_wait(q_full, 0) && first(0);
-            for (int j = 0; ok && j < nt; ++j) {
-                if (j + 1 < nt) ok = first(j + 1);
-                if (ok) ok = mbar_wait(ds_full + 8 * (j & 1), (j >> 1) & 1);
-                if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(tQ, tP + (j & 1) * 128, sk + (j % NK) * TILE, width(j), j > 0);
-                umma::commit(k_empty + 8 * (j % NK));
-            }
-            if (ok) umma::commit(dq_full);
-            umma::commit(mma_done);
-            mbar_wait(mma_done, 0);
+        // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
+        const uint32_t lead = umma::elect_lead();
+        const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), do_lo = umma::sdesc_lo(sdo, umma::KMAJOR);
+        const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), kt_lo = umma::sdesc_lo(sk, UATOM);
+        const uint32_t v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
+        const auto width = [&](int j) { return (kb.end(j, UW) - kb.start(j, UW) + 31) & ~31; };
+        const auto first = [&](int j) {  // S(j), then dP(j)
+            const int n = width(j), s3 = j % NK, s2 = j % NV;
+            bool ok = mbar_wait_warp(k_full + 8 * s3, (j / NK) & 1);
+            if (ok && j > 0) ok = mbar_wait_warp(s_empty, (j - 1) & 1);
+            if (!ok) return false;
+            umma::fence_after_sync();
+            mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
+            umma::commit_if(lead, s_full);
+            if (!mbar_wait_warp(v_full + 8 * s2, (j / NV) & 1)) return false;
+            umma::fence_after_sync();
+            mma_tiles<D>(lead, tP + (j & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
+            umma::commit_if(lead, dp_full + 8 * (j & 1));
+            umma::commit_if(lead, v_empty + 8 * s2);
+            return true;
+        };
+        bool ok = mbar_wait_warp(q_full, 0) && first(0);
+        for (int j = 0; ok && j < nt; ++j) {
+            if (j + 1 < nt) ok = first(j + 1);
+            if (ok) ok = mbar_wait_warp(ds_full + 8 * (j & 1), (j >> 1) & 1);
+            if (!ok) break;
+            umma::fence_after_sync();
+            mma_accumulate<D>(lead, tQ, tP + (j & 1) * 128, kt_lo + (j % NK) * (TILE >> 4), width(j), j > 0);
+            umma::commit_if(lead, k_empty + 8 * (j % NK));
         }
+        if (ok) umma::commit_if(lead, dq_full);
+        umma::commit_if(lead, mma_done);
+        mbar_wait_warp(mma_done, 0);
     } else {
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
         const bool valid = i < len;
@@ -483,8 +456,8 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             if (fix) {
                 ok = __all_sync(FULL, mbar_wait(tail, fixes++ & 1));
                 if (ok) {
-                    zero_rows<NA>(sm + Geo::OFF_3 + s3 * TILE, max(len - i0, 0), lane);
-                    zero_rows<NA>(sm + Geo::OFF_2 + s2 * TILE, max(len - i0, 0), lane);
+                    zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(len - i0, 0), lane);
+                    zero_rows<NA, UW>(sm + Geo::OFF_2 + s2 * TILE, max(len - i0, 0), lane);
                 }
                 umma::fence_proxy_async();
                 __syncwarp();
@@ -500,40 +473,43 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             for (int s = 0; s < ND; ++s) mbar_wait(do_full + 8 * s, 0);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            const auto scores = [&](int j) {
-                if (!mbar_wait(q_full + 8 * (j % NQ), (j / NQ) & 1)) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(tS, sk, sq + (j % NQ) * TILE, UW);
-                umma::commit(s_full);
-                return true;
-            };
-            const auto dps = [&](int j) {
-                if (!mbar_wait(do_full + 8 * (j % ND), (j / ND) & 1)) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(tP, sv, sdo + (j % ND) * TILE, UW);
-                umma::commit(dp_full);
-                return true;
-            };
-            bool ok = mbar_wait(kv_full, 0) && scores(0) && dps(0);
-            for (int j = 0; ok && j < nt; ++j) {
-                ok = mbar_wait(p_full, j & 1);
-                if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(tV, tS, sdo + (j % ND) * TILE, UW, j > 0);
-                if (j + 1 < nt) ok = scores(j + 1);
-                if (ok) ok = mbar_wait(ds_full, j & 1);
-                if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(tK, tP, sq + (j % NQ) * TILE, UW, j > 0);
-                umma::commit(q_empty + 8 * (j % NQ));
-                umma::commit(do_empty + 8 * (j % ND));
-                if (j + 1 < nt) ok = dps(j + 1);
-            }
-            if (ok) umma::commit(acc_full);
-            umma::commit(mma_done);
-            mbar_wait(mma_done, 0);
+        // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
+        const uint32_t lead = umma::elect_lead();
+        const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
+        const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), qt_lo = umma::sdesc_lo(sq, UATOM);
+        const uint32_t do_lo = umma::sdesc_lo(sdo, umma::KMAJOR), dot_lo = umma::sdesc_lo(sdo, UATOM);
+        const auto scores = [&](int j) {
+            if (!mbar_wait_warp(q_full + 8 * (j % NQ), (j / NQ) & 1)) return false;
+            umma::fence_after_sync();
+            mma_tiles<D>(lead, tS, k_lo, q_lo + (j % NQ) * (TILE >> 4), UW);
+            umma::commit_if(lead, s_full);
+            return true;
+        };
+        const auto dps = [&](int j) {
+            if (!mbar_wait_warp(do_full + 8 * (j % ND), (j / ND) & 1)) return false;
+            umma::fence_after_sync();
+            mma_tiles<D>(lead, tP, v_lo, do_lo + (j % ND) * (TILE >> 4), UW);
+            umma::commit_if(lead, dp_full);
+            return true;
+        };
+        bool ok = mbar_wait_warp(kv_full, 0) && scores(0) && dps(0);
+        for (int j = 0; ok && j < nt; ++j) {
+            ok = mbar_wait_warp(p_full, j & 1);
+            if (!ok) break;
+            umma::fence_after_sync();
+            mma_accumulate<D>(lead, tV, tS, dot_lo + (j % ND) * (TILE >> 4), UW, j > 0);
+            if (j + 1 < nt) ok = scores(j + 1);
+            if (ok) ok = mbar_wait_warp(ds_full, j & 1);
+            if (!ok) break;
+            umma::fence_after_sync();
+            mma_accumulate<D>(lead, tK, tP, qt_lo + (j % NQ) * (TILE >> 4), UW, j > 0);
+            umma::commit_if(lead, q_empty + 8 * (j % NQ));
+            umma::commit_if(lead, do_empty + 8 * (j % ND));
+            if (j + 1 < nt) ok = dps(j + 1);
         }
+        if (ok) umma::commit_if(lead, acc_full);
+        umma::commit_if(lead, mma_done);
+        mbar_wait_warp(mma_done, 0);
     } else {
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane, t = t0 + r;
         const bool valid = t < len;

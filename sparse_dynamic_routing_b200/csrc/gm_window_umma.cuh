@@ -41,19 +41,19 @@ namespace gm {
 
 constexpr int UW = 128;                 // rows of a tile (keys of a block in the backward)
 constexpr int UATOM = UW * 128;         // bytes of one 64-column block of a tile
-constexpr int FK = 64;                  // keys of a block in the forward
+constexpr int FK = 128;                 // keys of a block in the forward
 constexpr int FATOM = FK * 128;
 
 template <int D> struct WinFwdGeom {
     static constexpr int NA = D / 64;
     static constexpr int TILE = NA * UATOM;           // bytes of one 128 x D tile
-    static constexpr int KTILE = NA * FATOM;          // of 64 keys
-    static constexpr int NST = 4;                     // stages of K and of V
+    static constexpr int KTILE = NA * FATOM;          // of a key block
+    static constexpr int NST = D == 128 ? 2 : 4;      // stages of K and of V
     static constexpr int OFF_K = 2 * TILE;
     static constexpr int OFF_V = OFF_K + NST * KTILE;
     static constexpr int OFF_OUT = OFF_V + NST * KTILE;  // per tile: 64 columns of output on their way
     static constexpr int OFF_BAR = OFF_OUT + 2 * UATOM;
-    static constexpr int NBAR = 3 + 4 * NST + 4 + 4 + 4 + 2 + 2 + 1;
+    static constexpr int NBAR = 3 + 4 * NST + 2 + 4 + 2 + 2 + 2 + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr int THREADS = 320;
     static_assert(SMEM > 114 * 1024, "one CTA per SM: a second would wait for TMEM columns");
@@ -181,11 +181,9 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     const uint32_t sq = base, sk = base + Geo::OFF_K, sv = base + Geo::OFF_V, sb = base + Geo::OFF_BAR;
     const uint32_t q_full = sb, q_empty = sb + 8, tail = sb + 16, k_full = sb + 24, k_empty = k_full + 8 * NST;
     const uint32_t v_full = k_empty + 8 * NST, v_empty = v_full + 8 * NST;
-    const uint32_t s_full = v_empty + 8 * NST;                    // [tile][buffer]
-    // [tile][buffer]: the softmax may hand over a second P before the first has been taken, so a
-    // barrier per tile could be two phases ahead of who waits for it
-    const uint32_t p_full = s_full + 32, pv_done = p_full + 32;
-    const uint32_t o_empty = pv_done + 32, out_sync = o_empty + 16;  // [tile]
+    const uint32_t s_full = v_empty + 8 * NST;                            // [tile]
+    const uint32_t p_full = s_full + 16;                                  // [tile][half]
+    const uint32_t pv_done = p_full + 32, o_empty = pv_done + 16, out_sync = o_empty + 16;  // [tile]
     const uint32_t mma_done = out_sync + 16, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
     const uint32_t *tslot_p = reinterpret_cast<const uint32_t *>(sm + Geo::OFF_BAR + Geo::NBAR * 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -203,13 +201,11 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full + 16 * t, 1);
-            mbar_init(s_full + 16 * t + 8, 1);
+            mbar_init(s_full + 8 * t, 1);
             mbar_init(p_full + 16 * t, UW);
             mbar_init(p_full + 16 * t + 8, UW);
             mbar_init(out_sync + 8 * t, UW);
-            mbar_init(pv_done + 16 * t, 1);
-            mbar_init(pv_done + 16 * t + 8, 1);
+            mbar_init(pv_done + 8 * t, 1);
             mbar_init(o_empty + 8 * t, UW);
         }
         mbar_init(mma_done, 1);
@@ -298,45 +294,46 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             const auto scores = [&](int t, int j) {  // S_t(j) = Q_t K_j^T
                 const uint32_t y = kc + j, s = y % NST;
                 const uint32_t idesc = umma::idesc_bf16_f32(UW, width(j));
-                const uint32_t d = tmem + t * 128 + (y & 1) * 64;
+                const uint32_t d = tmem + t * 128;
                 const uint32_t al = q_lo + t * (TILE >> 4), bl = k_lo + s * (KTILE >> 4);
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     umma::mma_ss(lead, d, al + (((ks / 4) * UATOM + (ks % 4) * 32) >> 4),
                                  bl + (((ks / 4) * FATOM + (ks % 4) * 32) >> 4), idesc, ks > 0);
-                umma::commit_if(lead, s_full + 16 * t + 8 * (y & 1));
+                umma::commit_if(lead, s_full + 8 * t);
                 if (t == 1) {
                     umma::commit_if(lead, k_empty + 8 * s);
                     if (j == w.nt - 1) umma::commit_if(lead, q_empty);
                 }
             };
-            ok = mbar_wait_warp(q_full, qc & 1);
-            for (int j = 0; ok && j < min(w.nt, 2); ++j) {
-                ok = mbar_wait_warp(k_full + 8 * ((kc + j) % NST), ((kc + j) / NST) & 1);
-                if (!ok) break;
-                umma::fence_after_sync();
-                scores(0, j);
-                scores(1, j);
-            }
+            ok = mbar_wait_warp(q_full, qc & 1) && mbar_wait_warp(k_full + 8 * (kc % NST), (kc / NST) & 1);
+            if (!ok) break;
+            umma::fence_after_sync();
+            scores(0, 0);
+            scores(1, 0);
             for (int j = 0; ok && j < w.nt; ++j) {
                 const uint32_t y = kc + j, s = y % NST;
-                const bool four = width(j) == FK;
+                const int wd = width(j);
                 ok = mbar_wait_warp(v_full + 8 * s, (y / NST) & 1);
-                if (ok && j + 2 < w.nt) ok = mbar_wait_warp(k_full + 8 * ((y + 2) % NST), ((y + 2) / NST) & 1);
+                if (ok && j + 1 < w.nt) ok = mbar_wait_warp(k_full + 8 * ((y + 1) % NST), ((y + 1) / NST) & 1);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (ok) ok = mbar_wait_warp(p_full + 16 * t + 8 * (y & 1), (y >> 1) & 1);
                     if (ok && j == 0 && qc > 0) ok = mbar_wait_warp(o_empty + 8 * t, (qc - 1) & 1);
-                    if (!ok) break;
-                    umma::fence_after_sync();
-                    const uint32_t d = tmem + 256 + t * D, p = tmem + t * 128 + (y & 1) * 64;
-                    const uint32_t bl = v_lo + s * (KTILE >> 4);
+                    const uint32_t d = tmem + 256 + t * D, bl = v_lo + s * (KTILE >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)  // O_t += P_t V_j
-                        if (ks < 2 || four) umma::mma_ts(lead, d, p + ks * 8, bl + (ks * 2048 >> 4), idesc_pv, j > 0 || ks > 0);
-                    umma::commit_if(lead, pv_done + 16 * t + 8 * (y & 1));
+                    for (int half = 0; half < 2; ++half) {
+                        if (ok) ok = mbar_wait_warp(p_full + 16 * t + 8 * half, y & 1);
+                        if (!ok) break;
+                        umma::fence_after_sync();
+#pragma unroll
+                        for (int ks = half * 4; ks < half * 4 + 4; ++ks)  // O_t += P_t V_j
+                            if (ks < 2 || ks * 16 < wd)
+                                umma::mma_ts(lead, d, tmem + t * 128 + ks * 8, bl + (ks * 2048 >> 4), idesc_pv, j > 0 || ks > 0);
+                    }
+                    if (!ok) break;
+                    umma::commit_if(lead, pv_done + 8 * t);
                     if (t == 1) umma::commit_if(lead, v_empty + 8 * s);
-                    if (j + 2 < w.nt) scores(t, j + 2);
+                    if (j + 1 < w.nt) scores(t, j + 1);
                 }
             }
             kc += w.nt;
@@ -369,42 +366,53 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
             float m = -INFINITY, l = 0.0f;
             for (int j = 0; j < w.nt; ++j) {
                 const uint32_t y = kc + j;
-                ok = __all_sync(FULL, mbar_wait(s_full + 16 * t + 8 * (y & 1), (y >> 1) & 1));
+                ok = mbar_wait_warp(s_full + 8 * t, y & 1);
                 if (!ok) break;
                 umma::fence_after_sync();
-                const uint32_t ts = trow + t * 128 + (y & 1) * 64;
-                const int t0 = w.kb.start(j, FK), t1 = w.kb.end(j, FK);
+                const uint32_t ts = trow + t * 128;
+                const int t0 = w.kb.start(j, FK), t1 = w.kb.end(j, FK), nch = (t1 - t0 + 31) / 32;
                 const bool whole = t1 - t0 == FK && t1 - 1 <= r0 && r0 + 32 <= len &&
                                    (t0 > r0 + 31 - a.window || t1 <= a.sinks);
-                uint32_t s[2][32];
-                Piece piece[2] = {Piece::all, Piece::all};
-                uint32_t mask[2] = {0, 0};
-                umma::tmem_ld32(ts, s[0]);
-                umma::tmem_ld32(ts + 32, s[1]);
-                umma::tmem_wait_ld();
+                // ---- maximum over the visible columns ------------------------------------------
                 float m4[4] = {hide, hide, hide, hide};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!whole) {
-                        piece[c] = key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks);
-                        if (piece[c] == Piece::none) continue;
-                        if (piece[c] == Piece::some) {
-                            // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
-                            mask[c] = column_mask(c * 32, i - a.window + 1 - t0, valid ? min(i, t1 - 1) - t0 : -1, a.sinks - t0);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((mask[c] >> e) & 1)) s[c][e] = __float_as_uint(hide);
-                        }
-                    }
+                const auto maximum = [&](const uint32_t(&x)[32]) {
                     if (sl2 > 0.0f) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 2)
-                            m4[(e >> 1) & 3] =
-                                fmaxf(fmaxf(m4[(e >> 1) & 3], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
+                            m4[(e >> 1) & 3] = fmaxf(fmaxf(m4[(e >> 1) & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) m4[e & 3] = fminf(m4[e & 3], __uint_as_float(s[c][e]));
+                        for (int e = 0; e < 32; ++e) m4[e & 3] = fminf(m4[e & 3], __uint_as_float(x[e]));
                     }
+                };
+                // columns the row sees: c <= hi and (c >= lo or c < sinks - t0)
+                const int hi = valid ? min(i, t1 - 1) - t0 : -1, lo = i - a.window + 1 - t0;
+                uint32_t s[2][32];
+                if (whole) {
+                    umma::tmem_ld32(ts, s[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        umma::tmem_wait_ld32(s[c & 1]);
+                        if (c < 3) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                        maximum(s[c & 1]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < nch; ++c) {
+                        const Piece piece = key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks);
+                        if (piece == Piece::none) continue;
+                        umma::tmem_ld32(ts + c * 32, s[0]);
+                        umma::tmem_wait_ld32(s[0]);
+                        if (piece == Piece::some) {
+                            const uint32_t mask = column_mask(c * 32, lo, hi, a.sinks - t0);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((mask >> e) & 1)) s[0][e] = __float_as_uint(hide);
+                            umma::tmem_st32(ts + c * 32, s[0]);  // for the second reading
+                        }
+                        maximum(s[0]);
+                    }
+                    umma::tmem_wait_st();
                 }
                 float mx = sl2 > 0.0f ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]))
                                       : fminf(fminf(m4[0], m4[1]), fminf(m4[2], m4[3]));
@@ -415,10 +423,7 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                     if (grow) m = mx;
                     l *= f;
                     if (j > 0) {
-                        // P_t(j-1) V may still be adding to O_t
-                        ok = __all_sync(FULL, mbar_wait(pv_done + 16 * t + 8 * ((y - 1) & 1), ((y - 1) >> 1) & 1));
-                        if (!ok) break;
-                        umma::fence_after_sync();
+                        // S_t(j) was issued after P_t(j-1) V, so O_t is at rest until this block's P
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t o[16];
@@ -430,41 +435,61 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                         }
                     }
                 }
-                // ---- P = 2^(sl2 S - m) --------------------------------------------------------
+                // ---- P = 2^(sl2 S - m), piece c over scores of pieces already read --------------
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(nm, nm);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                // a hidden score is an infinity of the sign that gives 2^-inf = 0
+                const auto exponentials = [&](const uint32_t(&v)[32], uint32_t(&p)[16]) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t p[16];
-                    if (piece[c] == Piece::none) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) p[e] = 0;
-                    } else {
-                        // a hidden score is an infinity of the sign that gives 2^-inf = 0
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 x = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
-                            x = __ffma2_rn(x, sl22, nm2);
-                            x.x = ex2_ftz(x.x);
-                            x.y = ex2_ftz(x.y);
-                            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-                            p[e] = bf16_pair(x.x, x.y);
-                        }
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                        x = __ffma2_rn(x, sl22, nm2);
+                        x.x = ex2_ftz(x.x);
+                        x.y = ex2_ftz(x.y);
+                        sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                        p[e] = bf16_pair(x.x, x.y);
                     }
-                    umma::tmem_st16(ts + c * 16, p);
+                };
+                const auto hand_over = [&](int half) {  // half of the block is ready for the tensor cores
+                    umma::tmem_wait_st();
+                    umma::fence_before_sync();
+                    mbar_arrive(p_full + 16 * t + 8 * half);
+                };
+                uint32_t p[16];
+                if (whole) {
+                    umma::tmem_ld32(ts, s[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        umma::tmem_wait_ld32(s[c & 1]);
+                        if (c < 3) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
+                        exponentials(s[c & 1], p);
+                        umma::tmem_st16(ts + c * 16, p);
+                        if (c & 1) hand_over(c >> 1);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        if (key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks) != Piece::none) {
+                            umma::tmem_ld32(ts + c * 32, s[0]);
+                            umma::tmem_wait_ld32(s[0]);
+                            exponentials(s[0], p);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) p[e] = 0;
+                        }
+                        if (c < nch) umma::tmem_st16(ts + c * 16, p);
+                        if (c & 1) hand_over(c >> 1);
+                    }
                 }
                 sum[0] = __fadd2_rn(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
-                umma::tmem_wait_st();
-                umma::fence_before_sync();
-                mbar_arrive(p_full + 16 * t + 8 * (y & 1));
             }
             kc += w.nt;
             if (!ok) break;
             // ---- output: 64 columns at a time through the tile's buffer, out by TMA ----------------
             if (w.nt > 0) {
-                ok = __all_sync(FULL, mbar_wait(pv_done + 16 * t + 8 * ((kc - 1) & 1), ((kc - 1) >> 1) & 1));
+                ok = mbar_wait_warp(pv_done + 8 * t, (kc - 1) & 1);
                 if (!ok) break;
                 umma::fence_after_sync();
             }

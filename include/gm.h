@@ -557,8 +557,10 @@ gm_status gm_window_attention_backward(const void *q, const void *k, const void 
                                        void *dv, void *workspace, size_t workspace_bytes,
                                        cudaStream_t stream);
 
-/* Bytes of workspace gm_window_attention_backward needs. Pure host function; no CUDA call. */
-size_t gm_window_attention_backward_workspace_size(int B, int n, int hq);
+/* Bytes of workspace gm_window_attention_backward needs for this shape (0 for a shape it does not
+ * take). Pure host function; no CUDA call. */
+size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n, int hq, int hkv, int d,
+                                                   int window, int sinks);
 
 /*
  * gm_kv8_append - put new tokens' keys and values into a paged cache held in 8 bits.

@@ -62,7 +62,7 @@ SIGNATURES = {
                                     _vp, _vp],
     "gm_window_attention_backward": [_vp, _vp, _vp, _vp, _vp, _vp, _ci, _vp, _ci, _ci, _ci, _ci, _ci, _ci,
                                      _ci, _cf, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp],
-    "gm_window_attention_backward_workspace_size": [_ci, _ci, _ci],
+    "gm_window_attention_backward_workspace_size": [_ci] * 8,
     "gm_kv8_append": [_vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci, _vp, _vp,
                       _vp],
     "gm_kv8_attention_forward": [_vp, _ci, _ci, _ci, _ci, _ci, _ci, _vp, _vp, _vp, _vp, _ci, _ci, _vp, _ci,
@@ -695,9 +695,12 @@ def gm_window_attention_forward(q, k, v, window=None, sinks: int = 0, lens=None,
     return o, lse
 
 
-def gm_window_attention_backward_workspace_size(B: int, n: int, hq: int) -> int:
-    """Workspace bytes of gm_window_attention_backward."""
-    return int(load_library().gm_window_attention_backward_workspace_size(B, n, hq))
+def gm_window_attention_backward_workspace_size(dtype, B: int, n: int, hq: int, hkv: int, d: int, window=None,
+                                                sinks: int = 0) -> int:
+    """Workspace bytes of gm_window_attention_backward (0: a shape it does not take)."""
+    window, sinks = _window(window, sinks)
+    dt = GM_BF16 if dtype == torch.bfloat16 else GM_F32 if dtype == torch.float32 else -1
+    return int(load_library().gm_window_attention_backward_workspace_size(dt, B, n, hq, hkv, d, window, sinks))
 
 
 def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int = 0, lens=None, scale=None,
@@ -716,8 +719,9 @@ def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int 
         dk, pdk = _out(dk, kv, dt, dev, "dk")
         dv, pdv = _out(dv, kv, dt, dev, "dv")
         if workspace is None:
-            workspace = torch.empty(lib.gm_window_attention_backward_workspace_size(B, n, hq), dtype=torch.uint8,
-                                    device=dev)
+            workspace = torch.empty(
+                lib.gm_window_attention_backward_workspace_size(_fdtype(q), B, n, hq, hkv, d, window, sinks),
+                dtype=torch.uint8, device=dev)
         st = lib.gm_window_attention_backward(
             _arg(q, q.shape, dt, dev, "q"), _arg(k, kv, dt, dev, "k"), _arg(v, kv, dt, dev, "v"),
             _arg(o, q.shape, dt, dev, "o"), _arg(dout, q.shape, dt, dev, "dout"),

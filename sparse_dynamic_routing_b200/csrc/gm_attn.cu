@@ -132,31 +132,84 @@ template <int D> gm_status window_forward_bf16(gm::WinArgs a, cudaStream_t st)
     return launched();
 }
 
+// How the key blocks of a backward are cut (gm_window_bwd_umma.cuh, WinBwdArgs), and the workspace.
+struct WinBwdPlan {
+    int nblk, sink_blocks, sink_chunks, chunks, sink_steps, steps;
+    int64_t sink_items, items;
+    size_t stats_bytes, bytes;  // nl and -delta and two counters, then the pieces' partial sums
+};
+
+WinBwdPlan window_backward_plan(int B, int n, int hq, int hkv, int d, int window, int sinks)
+{
+    WinBwdPlan p{};
+    const int G = hq / hkv;
+    window = std::min(window, n);
+    sinks = std::min(sinks, n);
+    p.nblk = (n + gm::UW - 1) / gm::UW;
+    const int64_t per = (int64_t)B * hkv;
+    // steps (128 queries of one head) of the block that is seen longest, with and without sinks
+    const int64_t near = std::min<int64_t>(p.nblk, (127 + (int64_t)window + 127) / 128);
+    p.sink_blocks = near < p.nblk ? std::min(p.nblk, (sinks + 127) / 128) : 0;
+    const int64_t sink_most = (int64_t)p.nblk * G, most = near * G;
+    int64_t total = 0;
+    for (int64_t b = 0; b < p.nblk; ++b) total += (b < p.sink_blocks ? p.nblk - b : std::min(near, p.nblk - b)) * G;
+    total *= per;
+    // Blocks are cut where the longest would take half as long again as an SM's share of it all
+    // (B=1 n=32768 window 512 with sinks: 1520 -> 900 us); otherwise the writes and reads of 2 x 128 x
+    // d fp32 sums per piece cost more than the balance gives (B=1 n=4096 full: 275 -> 356 us).
+    const int64_t share = (total + 147) / 148, piece = std::max<int64_t>(8, share / 2);
+    const auto pieces = [&](int64_t steps) { return (int)(2 * steps > 3 * share && steps >= 16 ? (steps + piece - 1) / piece : 1); };
+    p.sink_chunks = p.sink_blocks ? pieces(sink_most) : 1;
+    p.chunks = pieces(most);
+    p.sink_steps = p.sink_chunks > 1 ? (int)((sink_most + p.sink_chunks - 1) / p.sink_chunks) : INT32_MAX;
+    p.steps = p.chunks > 1 ? (int)((most + p.chunks - 1) / p.chunks) : INT32_MAX;
+    p.sink_items = per * p.sink_blocks * p.sink_chunks;
+    p.items = p.sink_items + per * (p.nblk - p.sink_blocks) * p.chunks;
+    const int64_t cut = (p.sink_chunks > 1 ? p.sink_items : 0) + (p.chunks > 1 ? p.items - p.sink_items : 0);
+    p.stats_bytes = (size_t)B * p.nblk * gm::UW * hq * 8 + 16;
+    p.bytes = p.stats_bytes + (size_t)cut * 2 * gm::UW * d * 4;
+    return p;
+}
+
 template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream_t st)
 {
     using Geo = gm::WinBwdGeom<D>;
-    CUtensorMap tq, tdo, tk, tv, tdq, tdk, tdv;
+    CUtensorMap tq, tdo, tk, tv;
     if (!sequence_tmap(tq, w.q, w.B, w.n, w.hq, D) || !sequence_tmap(tdo, w.dout, w.B, w.n, w.hq, D) ||
-        !sequence_tmap(tk, w.k, w.B, w.n, w.hkv, D) || !sequence_tmap(tv, w.v, w.B, w.n, w.hkv, D) ||
-        !sequence_tmap(tdq, w.dq, w.B, w.n, w.hq, D) || !sequence_tmap(tdk, w.dk, w.B, w.n, w.hkv, D) ||
-        !sequence_tmap(tdv, w.dv, w.B, w.n, w.hkv, D))
+        !sequence_tmap(tk, w.k, w.B, w.n, w.hkv, D) || !sequence_tmap(tv, w.v, w.B, w.n, w.hkv, D))
         return GM_ERR_CUDA;
     auto kq = gm::win_dq_umma_kernel<D>;
     auto kkv = gm::win_dkv_umma_kernel<D>;
     if (!raise_smem(kq, Geo::SMEM) || !raise_smem(kkv, Geo::SMEM)) return GM_ERR_CUDA;
+    const WinBwdPlan p = window_backward_plan(w.B, w.n, w.hq, w.hkv, D, w.window, w.sinks);
     gm::WinBwdArgs a{};
     a.w = w;
     a.scale = w.scale;
     a.w.scale = base2_scale(w.scale);
-    a.w.nblk = (w.n + gm::UW - 1) / gm::UW;
-    a.npad = a.w.nblk * gm::UW;
+    a.w.nblk = p.nblk;
+    a.npad = p.nblk * gm::UW;
+    a.sink_blocks = p.sink_blocks;
+    a.sink_chunks = p.sink_chunks;
+    a.chunks = p.chunks;
+    a.sink_steps = p.sink_steps;
+    a.steps = p.steps;
     const int64_t rows = (int64_t)w.B * a.npad * w.hq;
     float *nl = w.delta, *ndelta = w.delta + rows;
     a.nl = nl;
     a.ndelta = ndelta;
+    a.next = (int *)(ndelta + rows);
+    a.part = (float *)((char *)w.delta + p.stats_bytes);
     gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(a, nl, ndelta);
-    kq<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hq), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdq, a);
-    kkv<<<(unsigned)((int64_t)a.w.nblk * w.B * w.hkv), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, tdk, tdv, a);
+    a.items = (int64_t)p.nblk * w.B * w.hq;
+    kq<<<(unsigned)std::min<int64_t>(a.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, a);
+    a.items = p.items;
+    a.next += 1;
+    kkv<<<(unsigned)std::min<int64_t>(a.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, a);
+    const int64_t per = (int64_t)w.B * w.hkv, threads = 2 * gm::UW * D / 4;  // per key block
+    if (p.sink_chunks > 1)
+        gm::win_dkv_join_kernel<D><<<(unsigned)(per * p.sink_blocks * threads / 256), 256, 0, st>>>(a, 0, p.sink_chunks);
+    if (p.chunks > 1)
+        gm::win_dkv_join_kernel<D><<<(unsigned)(per * (p.nblk - p.sink_blocks) * threads / 256), 256, 0, st>>>(a, p.sink_items, p.chunks);
     return launched();
 }
 
@@ -308,11 +361,11 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
     return d == 64 ? window_forward_bf16<64>(a, stream) : window_forward_bf16<128>(a, stream);
 }
 
-size_t gm_window_attention_backward_workspace_size(int B, int n, int hq)
+size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n, int hq, int hkv, int d, int window, int sinks)
 {
-    if (B < 1 || n < 1 || hq < 1) return 0;
-    // two fp32 values per row of sequences padded to whole 128-row blocks
-    return (size_t)B * (((size_t)n + 127) / 128 * 128) * hq * 8;
+    if (check_window(dtype, B, n, hq, hkv, d, window, sinks, 1.0f) != GM_OK || (int64_t)B * n == 0) return 0;
+    if (dtype == GM_F32) return ((size_t)B * n * hq * 4 + 15) / 16 * 16;
+    return window_backward_plan(B, n, hq, hkv, d, window, sinks).bytes;
 }
 
 gm_status gm_window_attention_backward(const void *q, const void *k, const void *v, const void *o, const void *dout,
@@ -325,7 +378,8 @@ gm_status gm_window_attention_backward(const void *q, const void *k, const void 
     if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace) return GM_ERR_INVALID_ARG;
     for (const void *p : {q, k, v, o, dout, (const void *)dq, (const void *)dk, (const void *)dv, (const void *)workspace})
         if (!aligned16(p)) return GM_ERR_INVALID_ARG;
-    if (workspace_bytes < gm_window_attention_backward_workspace_size(B, n, hq)) return GM_ERR_INVALID_ARG;
+    if (workspace_bytes < gm_window_attention_backward_workspace_size(dtype, B, n, hq, hkv, d, window, sinks))
+        return GM_ERR_INVALID_ARG;
     gm::WinArgs a = window_args(B, n, hq, hkv, window, sinks, scale, lens);
     a.q = q;
     a.k = k;

@@ -21,6 +21,15 @@
 // multiple of 128; rows at or past the sequence's end have nl = -inf (P = 0) and delta = 0.
 // Such rows of the tiles are zeroed in shared memory where a product sums over them.
 //
+// Both kernels run one CTA per SM, which takes item after item from a counter in the workspace
+// (items differ in length, by the mask and by the sequences): the loads, S and dP of the next item
+// start under the last elements and the output of the one before. Output rows go from registers to global memory, 16 bytes at a time: all of shared
+// memory holds operands.
+//
+// dkv with few keys that many queries see (sinks; few sequences): the steps of one key block are
+// cut into chunks, each an item of its own that writes fp32 partial sums to the workspace, and
+// win_dkv_join_kernel adds those in chunk order.
+//
 // Every wait is bounded (gm_common.cuh, mbar_wait).
 #pragma once
 
@@ -34,6 +43,54 @@ struct WinBwdArgs {
     const float *nl;    // [B, hq, npad]
     const float *ndelta;  // -delta
     int npad;
+    int64_t items;        // work items of the kernel that is launched
+    int *next;            // its counter, 0 at the launch
+    // dkv: the first `sink_blocks` key blocks are cut into sink_chunks, the others into chunks pieces of
+    // at most sink_steps / steps steps; pieces of cut blocks go to `part` [piece][dk, dv][128][D]
+    int sink_blocks, sink_chunks, chunks, sink_steps, steps;
+    float *part;
+};
+
+// One piece of one key block's work in dkv.
+struct DkvItem {
+    int b, h, t0, len, nq, j0, j1;  // query blocks per head; steps [j0, j1) of nq * G
+    bool cut;
+    int64_t slot;                   // of the piece in `part`
+    __device__ __forceinline__ DkvItem(const WinBwdArgs &ba, int64_t item)
+    {
+        const WinArgs &a = ba.w;
+        const int64_t per = (int64_t)a.B * a.hkv, sink_items = per * ba.sink_blocks * ba.sink_chunks;
+        int blk, chunk, most;
+        int64_t x;
+        if (item < sink_items) {  // a block's pieces are neighbours
+            chunk = (int)(item % ba.sink_chunks);
+            x = item / ba.sink_chunks;
+            blk = (int)(x / per);
+            most = ba.sink_steps;
+            cut = ba.sink_chunks > 1;
+            slot = item;
+        } else {
+            const int64_t y = item - sink_items;
+            chunk = (int)(y % ba.chunks);
+            x = y / ba.chunks;
+            blk = ba.sink_blocks + (int)(x / per);
+            most = ba.steps;
+            cut = ba.chunks > 1;
+            slot = (ba.sink_chunks > 1 ? sink_items : 0) + y;
+        }
+        const int bh = (int)(x % per);
+        b = bh / a.hkv;
+        h = bh - b * a.hkv;
+        t0 = blk * UW;
+        len = win_len(a, b);
+        const int t1 = min(t0 + UW, len);
+        const int qend = t1 > t0 ? query_end(t0, t1, len, a.window, a.sinks) : t0;
+        nq = (qend - t0 + UW - 1) / UW;
+        const int64_t first = (int64_t)chunk * most;  // 64 bits: steps of an uncut block are unlimited
+        const int all = nq * a.G;
+        j0 = (int)(first < all ? first : all);
+        j1 = (int)(first + most < all ? first + most : all);
+    }
 };
 
 template <int D> struct WinBwdGeom {
@@ -45,8 +102,9 @@ template <int D> struct WinBwdGeom {
     static constexpr int OFF_NL = OFF_2 + N2 * TILE;   // dkv: nl with the first operand's stages
     static constexpr int OFF_DELTA = OFF_NL + N3 * 512;
     static constexpr int OFF_BAR = OFF_DELTA + N2 * 512;
-    static constexpr int NBAR = 24;
-    static constexpr int NEED = OFF_BAR + NBAR * 8 + 16;
+    static constexpr int NBAR = 32;                    // the last eight: the item queue's
+    static constexpr int OFF_QUEUE = OFF_BAR + NBAR * 8 + 16;
+    static constexpr int NEED = OFF_QUEUE + 16;
     // more than half of the SM's shared memory: a second CTA would wait there for TMEM columns
     static constexpr int SMEM = NEED < 120 * 1024 ? 120 * 1024 : NEED;
     static constexpr int THREADS = 320;
@@ -54,8 +112,10 @@ template <int D> struct WinBwdGeom {
 };
 
 // nl and -delta of every row; D/8 lanes per row.
+// Also sets both counters to 0.
 template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdArgs a, float *nl, float *ndelta)
 {
+    if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
     constexpr int C = D / 8, RPB = 256 / C;
     const WinArgs &w = a.w;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / C;  // (b, i < npad, hq)
@@ -91,6 +151,50 @@ __device__ __forceinline__ Piece query_piece(int k0, int i, int len, int window,
     return Piece::some;
 }
 
+// The CTA's queue of work items: the load warp takes them from the counter and passes them on, up
+// to four ahead of the slowest reader. Item `items` or more ends the work.
+struct ItemQueue {
+    uint32_t full, empty;    // barriers of the four slots
+    volatile int *slots;
+    uint32_t n = 0;
+    __device__ __forceinline__ ItemQueue(uint32_t bars, void *mem) : full(bars), empty(bars + 32), slots((volatile int *)mem) {}
+    // By one thread, before the others read.
+    __device__ __forceinline__ void init() const
+    {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 9);  // eight element warps and the MMA warp
+        }
+    }
+    // By the load warp: passes `item` on; false after a wait that gave up.
+    __device__ __forceinline__ bool push(int item, int lane)
+    {
+        const uint32_t s = n % 4;
+        bool ok = true;
+        if (lane == 0) {
+            if (n >= 4) ok = mbar_wait(empty + 8 * s, ((n / 4) - 1) & 1);
+            if (ok) {
+                slots[s] = item;
+                mbar_arrive(full + 8 * s);
+            }
+        }
+        ++n;
+        return __shfl_sync(FULL, ok, 0);
+    }
+    // By a reading warp: the next item, or -1 after a wait that gave up.
+    __device__ __forceinline__ int pop(int lane)
+    {
+        const uint32_t s = n % 4;
+        if (!mbar_wait_warp(full + 8 * s, (n / 4) & 1)) return -1;
+        const int item = slots[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * s);
+        ++n;
+        return item;
+    }
+};
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
@@ -122,11 +226,34 @@ __device__ __forceinline__ void mma_accumulate(uint32_t lead, uint32_t d, uint32
             umma::mma_ts(lead, d, ta + (ks < 4 ? ks * 8 : 64 + (ks - 4) * 8), b_lo + (ks * 2048 >> 4), idesc, add || ks > 0);
 }
 
+// This thread's row of a TMEM accumulator, columns [32 c0, 32 c1), times f, as bf16 (or fp32) to
+// global memory; nothing where `keep` is 0, zeros where it is 1, the values where it is 2.
+template <typename T>
+__device__ __forceinline__ void store_row(T *dst, uint32_t taddr, int c0, int c1, float f, int keep)
+{
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+        uint32_t o[32];
+        umma::tmem_ld32(taddr + c * 32, o);
+        umma::tmem_wait_ld();
+        if (keep) {
+            constexpr int V = 16 / sizeof(T);
+#pragma unroll
+            for (int e = 0; e < 32 / V; ++e) {
+                float x[V];
+#pragma unroll
+                for (int y = 0; y < V; ++y) x[y] = keep == 2 ? __uint_as_float(o[e * V + y]) * f : 0.0f;
+                *reinterpret_cast<uint4 *>(dst + c * 32 + e * V) = pack<T>(x);
+            }
+        }
+        __syncwarp();
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(WinBwdGeom<D>::THREADS, 1)
 win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmdo,
-                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                   const __grid_constant__ CUtensorMap tmdq, WinBwdArgs ba)
+                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, WinBwdArgs ba)
 {
     using Geo = WinBwdGeom<D>;
     constexpr int NA = Geo::NA, TILE = Geo::TILE, NK = Geo::N3, NV = Geo::N2;
@@ -136,30 +263,17 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const uint32_t base = smem_u32(sm);
     const uint32_t sq = base, sdo = base + TILE, sk = base + Geo::OFF_3, sv = base + Geo::OFF_2;
     const uint32_t sb = base + Geo::OFF_BAR;
-    const uint32_t q_full = sb, tail = sb + 8, k_full = sb + 16, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK;
-    const uint32_t v_empty = v_full + 8 * NV, s_full = v_empty + 8 * NV, s_empty = s_full + 8, dp_full = s_empty + 8;
-    const uint32_t ds_full = dp_full + 16, dq_full = ds_full + 16, mma_done = dq_full + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
+    const uint32_t q_full = sb, q_empty = sb + 8, tail = sb + 16, k_full = sb + 24, k_empty = k_full + 8 * NK;
+    const uint32_t v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV, s_full = v_empty + 8 * NV, s_empty = s_full + 8;
+    const uint32_t dp_full = s_empty + 8, ds_full = dp_full + 16, dq_full = ds_full + 16, dq_empty = dq_full + 8;
+    const uint32_t mma_done = dq_empty + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
     const uint32_t *tslot_p = reinterpret_cast<const uint32_t *>(sm + Geo::OFF_BAR + Geo::NBAR * 8);
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = a.B * a.hq;
-    const int blk = a.nblk - 1 - (int)(blockIdx.x / (unsigned)per);
-    const int bh = (int)(blockIdx.x % (unsigned)per);
-    const int b = bh / a.hq, hq = bh - b * a.hq, h = hq / a.G, i0 = blk * UW;
-    const int len = win_len(a, b);
-    const KeyBlocks kb(i0, UW, len, a.window, a.sinks, UW);
-    const int nt = kb.na + kb.nb;
-    if (nt == 0) {
-        for (int y = threadIdx.x; y < UW * (D / 8); y += Geo::THREADS) {
-            const int r = y / (D / 8), c = y - r * (D / 8);
-            if (i0 + r < a.n)
-                *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dq + (((size_t)b * a.n + i0 + r) * a.hq + hq) * D + c * 8) =
-                    make_uint4(0, 0, 0, 0);
-        }
-        return;
-    }
+    ItemQueue queue(base + Geo::OFF_BAR + (Geo::NBAR - 8) * 8, sm + Geo::OFF_QUEUE);
+
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         mbar_init(tail, 1);
 #pragma unroll
         for (int s = 0; s < NK; ++s) mbar_init(k_full + 8 * s, 1), mbar_init(k_empty + 8 * s, 1);
@@ -170,7 +284,9 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 #pragma unroll
         for (int s = 0; s < 2; ++s) mbar_init(dp_full + 8 * s, 1), mbar_init(ds_full + 8 * s, 256);
         mbar_init(dq_full, 1);
+        mbar_init(dq_empty, 256);
         mbar_init(mma_done, 1);
+        queue.init();
         mbar_init_fence();
     }
     if (warp == 9) umma::tmem_alloc(tslot, 512);
@@ -180,46 +296,82 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const uint32_t tmem = *tslot_p;
     const uint32_t tS = tmem, tP = tmem + 128, tQ = tmem + 384;  // S, two dP / dS buffers, dQ
 
-    if (warp == 8) {
-        const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
-#pragma unroll
-            for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, b, bar);
-        };
-        if (lane == 0) {
-            mbar_arrive_expect(q_full, 2 * TILE);
-            load(sq, &tmq, hq, i0, q_full);
-            load(sdo, &tmdo, hq, i0, q_full);
+    // item: (query block, longest prefixes first; sequence; head)
+    const int per = a.B * a.hq;
+    struct Item {
+        int b, hq, h, i0, len, nt;
+        KeyBlocks kb;
+        __device__ __forceinline__ Item(const WinArgs &a, int64_t item, int per) : kb(0, 0, 0, 1, 0, 1)
+        {
+            const int x = (int)(item % per);
+            b = x / a.hq;
+            hq = x - b * a.hq;
+            h = hq / a.G;
+            i0 = (a.nblk - 1 - (int)(item / per)) * UW;
+            len = win_len(a, b);
+            kb = KeyBlocks(i0, UW, len, a.window, a.sinks, UW);
+            nt = kb.na + kb.nb;
         }
+    };
+
+    if (warp == 8) {
+        uint32_t kc = 0, fixes = 0;
+        int qc = 0;
         bool ok = true;
-        for (int j = 0; ok && j < nt; ++j) {
-            const int s3 = j % NK, s2 = j % NV, t0 = kb.start(j, UW);
-            if (lane == 0 && j >= NK) ok = mbar_wait(k_empty + 8 * s3, ((j / NK) - 1) & 1);
+        // the first item by position, the others from the counter, asked for one item ahead
+        int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
+        for (;;) {
+            ok = queue.push(item, lane);
+            if (!ok || item >= ba.items) break;
+            const Item w(a, item, per);
+            item = __shfl_sync(FULL, ahead, 0);
+            if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
+            if (w.nt == 0) continue;
+            const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
+#pragma unroll
+                for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
+            };
+            if (lane == 0 && qc > 0) ok = mbar_wait(q_empty, (qc - 1) & 1);
             ok = __shfl_sync(FULL, ok, 0);
             if (!ok) break;
-            const bool fix = t0 + UW > len && len < a.n;  // the last block alone: dQ sums over K's rows
-            const uint32_t bar = fix ? tail : k_full + 8 * s3;
             if (lane == 0) {
-                mbar_arrive_expect(bar, TILE);
-                load(sk + s3 * TILE, &tmk, h, t0, bar);
+                mbar_arrive_expect(q_full, 2 * TILE);
+                load(sq, &tmq, w.hq, w.i0, q_full);
+                load(sdo, &tmdo, w.hq, w.i0, q_full);
             }
-            if (fix) {
-                ok = __all_sync(FULL, mbar_wait(tail, 0));
-                if (ok) zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(len - t0, 0), lane);
-                umma::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(k_full + 8 * s3);
+            ++qc;
+            for (int j = 0; ok && j < w.nt; ++j, ++kc) {
+                const uint32_t s3 = kc % NK, s2 = kc % NV;
+                const int t0 = w.kb.start(j, UW);
+                if (lane == 0 && kc >= NK) ok = mbar_wait(k_empty + 8 * s3, ((kc / NK) - 1) & 1);
+                ok = __shfl_sync(FULL, ok, 0);
+                if (!ok) break;
+                const bool fix = t0 + UW > w.len && w.len < a.n;  // the last block alone: dQ sums over K's rows
+                const uint32_t bar = fix ? tail : k_full + 8 * s3;
+                if (lane == 0) {
+                    mbar_arrive_expect(bar, TILE);
+                    load(sk + s3 * TILE, &tmk, w.h, t0, bar);
+                }
+                if (fix) {
+                    ok = mbar_wait_warp(tail, fixes++ & 1);
+                    if (ok) zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - t0, 0), lane);
+                    umma::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(k_full + 8 * s3);
+                }
+                if (lane == 0 && ok && kc >= NV) ok = mbar_wait(v_empty + 8 * s2, ((kc / NV) - 1) & 1);
+                if (lane == 0 && ok) {
+                    mbar_arrive_expect(v_full + 8 * s2, TILE);
+                    load(sv + s2 * TILE, &tmv, w.h, t0, v_full + 8 * s2);
+                }
+                ok = __shfl_sync(FULL, ok, 0);
             }
-            if (lane == 0 && ok && j >= NV) ok = mbar_wait(v_empty + 8 * s2, ((j / NV) - 1) & 1);
-            if (lane == 0 && ok) {
-                mbar_arrive_expect(v_full + 8 * s2, TILE);
-                load(sv + s2 * TILE, &tmv, h, t0, v_full + 8 * s2);
-            }
-            ok = __shfl_sync(FULL, ok, 0);
+            if (!ok) break;
         }
-        if (lane == 0 && !ok) {  // gave up: copies in flight land before the CTA ends (bounded)
-            mbar_wait(q_full, 0);
-            for (int s = 0; s < NK; ++s) mbar_wait(k_full + 8 * s, 0);
-            for (int s = 0; s < NV; ++s) mbar_wait(v_full + 8 * s, 0);
+        if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
+            mbar_wait(q_full, (qc - 1) & 1);
+            for (uint32_t y = kc > NK ? kc - NK : 0; y < kc; ++y) mbar_wait(k_full + 8 * (y % NK), (y / NK) & 1);
+            for (uint32_t y = kc > NV ? kc - NV : 0; y < kc; ++y) mbar_wait(v_full + 8 * (y % NV), (y / NV) & 1);
         }
     } else if (warp == 9) {
         // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
@@ -227,127 +379,153 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), do_lo = umma::sdesc_lo(sdo, umma::KMAJOR);
         const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), kt_lo = umma::sdesc_lo(sk, UATOM);
         const uint32_t v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
-        const auto width = [&](int j) { return (kb.end(j, UW) - kb.start(j, UW) + 31) & ~31; };
-        const auto first = [&](int j) {  // S(j), then dP(j)
-            const int n = width(j), s3 = j % NK, s2 = j % NV;
-            bool ok = mbar_wait_warp(k_full + 8 * s3, (j / NK) & 1);
-            if (ok && j > 0) ok = mbar_wait_warp(s_empty, (j - 1) & 1);
-            if (!ok) return false;
-            umma::fence_after_sync();
-            mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
-            umma::commit_if(lead, s_full);
-            if (!mbar_wait_warp(v_full + 8 * s2, (j / NV) & 1)) return false;
-            umma::fence_after_sync();
-            mma_tiles<D>(lead, tP + (j & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
-            umma::commit_if(lead, dp_full + 8 * (j & 1));
-            umma::commit_if(lead, v_empty + 8 * s2);
-            return true;
-        };
-        bool ok = mbar_wait_warp(q_full, 0) && first(0);
-        for (int j = 0; ok && j < nt; ++j) {
-            if (j + 1 < nt) ok = first(j + 1);
-            if (ok) ok = mbar_wait_warp(ds_full + 8 * (j & 1), (j >> 1) & 1);
-            if (!ok) break;
-            umma::fence_after_sync();
-            mma_accumulate<D>(lead, tQ, tP + (j & 1) * 128, kt_lo + (j % NK) * (TILE >> 4), width(j), j > 0);
-            umma::commit_if(lead, k_empty + 8 * (j % NK));
+        uint32_t kc = 0;
+        int qc = 0;
+        bool ok = true;
+        while (ok) {
+            const int item = queue.pop(lane);
+            if (item < 0 || item >= ba.items) break;
+            const Item w(a, item, per);
+            if (w.nt == 0) continue;
+            const auto width = [&](int j) { return (w.kb.end(j, UW) - w.kb.start(j, UW) + 31) & ~31; };
+            const auto first = [&](int j) {  // S(j), then dP(j)
+                const uint32_t y = kc + j, s3 = y % NK, s2 = y % NV;
+                const int n = width(j);
+                bool ok = mbar_wait_warp(k_full + 8 * s3, (y / NK) & 1);
+                if (ok && y > 0) ok = mbar_wait_warp(s_empty, (y - 1) & 1);
+                if (!ok) return false;
+                umma::fence_after_sync();
+                mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
+                umma::commit_if(lead, s_full);
+                if (!mbar_wait_warp(v_full + 8 * s2, (y / NV) & 1)) return false;
+                umma::fence_after_sync();
+                mma_tiles<D>(lead, tP + (y & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
+                umma::commit_if(lead, dp_full + 8 * (y & 1));
+                umma::commit_if(lead, v_empty + 8 * s2);
+                if (j == w.nt - 1) umma::commit_if(lead, q_empty);
+                return true;
+            };
+            ok = mbar_wait_warp(q_full, qc & 1) && first(0);
+            for (int j = 0; ok && j < w.nt; ++j) {
+                const uint32_t y = kc + j;
+                if (j + 1 < w.nt) ok = first(j + 1);
+                if (ok && j == 0 && qc > 0) ok = mbar_wait_warp(dq_empty, (qc - 1) & 1);
+                if (ok) ok = mbar_wait_warp(ds_full + 8 * (y & 1), (y >> 1) & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                mma_accumulate<D>(lead, tQ, tP + (y & 1) * 128, kt_lo + (y % NK) * (TILE >> 4), width(j), j > 0);
+                umma::commit_if(lead, k_empty + 8 * (y % NK));
+            }
+            if (ok) umma::commit_if(lead, dq_full);
+            kc += w.nt;
+            ++qc;
         }
-        if (ok) umma::commit_if(lead, dq_full);
+        // every MMA issued has completed before the CTA releases its tensor memory
         umma::commit_if(lead, mma_done);
         mbar_wait_warp(mma_done, 0);
     } else {
-        const int wg = warp >> 2, r = (warp & 3) * 32 + lane, i = i0 + r;
-        const bool valid = i < len;
-        const size_t st = ((size_t)b * a.hq + hq) * ba.npad + i;  // i < npad
-        const float nl = valid ? __ldg(ba.nl + st) : 0.0f, dl = valid ? __ldg(ba.ndelta + st) : 0.0f;
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
         const float sl2 = a.scale;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        uint32_t kc = 0;
+        int qc = 0;
         bool ok = true;
-        for (int j = 0; j < nt; ++j) {
-            const int t0 = kb.start(j, UW), t1 = kb.end(j, UW);
-            const int c0 = wg * 64, nch = min(max((t1 - t0 - c0 + 31) / 32, 0), 2);  // this group's pieces
-            const bool whole = ((t1 - t0) & 31) == 0 && t1 - 1 <= i0 && i0 + UW <= len &&
-                               (t0 > i0 + UW - 1 - a.window || t1 <= a.sinks);
-            ok = __all_sync(FULL, mbar_wait(s_full, j & 1));
-            if (!ok) break;
-            umma::fence_after_sync();
-            uint32_t s[2][32];
+        while (ok) {
+            const int item = queue.pop(lane);
+            if (item < 0 || item >= ba.items) break;
+            const Item w(a, item, per);
+            const int len = w.len, i0 = w.i0, i = i0 + r;
+            const bool valid = i < len;
+            const size_t st = ((size_t)w.b * a.hq + w.hq) * ba.npad + i;  // i < npad
+            const float nl = valid ? __ldg(ba.nl + st) : 0.0f, dl = valid ? __ldg(ba.ndelta + st) : 0.0f;
+            for (int j = 0; j < w.nt; ++j) {
+                const uint32_t y = kc + j;
+                const int t0 = w.kb.start(j, UW), t1 = w.kb.end(j, UW);
+                const int c0 = wg * 64, nch = min(max((t1 - t0 - c0 + 31) / 32, 0), 2);  // this group's pieces
+                const bool whole = ((t1 - t0) & 31) == 0 && t1 - 1 <= i0 && i0 + UW <= len &&
+                                   (t0 > i0 + UW - 1 - a.window || t1 <= a.sinks);
+                ok = mbar_wait_warp(s_full, y & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                uint32_t s[2][32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (c < nch) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
-            umma::tmem_wait_ld();
-            umma::fence_before_sync();
-            mbar_arrive(s_empty);
-            Piece piece[2];
-            uint32_t mask[2];
+                for (int c = 0; c < 2; ++c)
+                    if (c < nch) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
+                umma::tmem_wait_ld();
+                umma::fence_before_sync();
+                mbar_arrive(s_empty);
+                Piece piece[2];
+                uint32_t mask[2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int col = c0 + c * 32;
-                piece[c] = whole ? Piece::all : key_piece(i0 + (warp & 3) * 32, t0 + col, t1, len, a.window, a.sinks);
-                mask[c] = piece[c] == Piece::some ? column_mask(col, i - a.window + 1 - t0, valid ? min(i, t1 - 1) - t0 : -1,
-                                                                a.sinks - t0)
-                                                  : 0u;
-                if (piece[c] == Piece::none) continue;
+                for (int c = 0; c < 2; ++c) {
+                    const int col = c0 + c * 32;
+                    piece[c] = key_piece(i0 + (warp & 3) * 32, t0 + col, t1, len, a.window, a.sinks);
+                    if (whole) piece[c] = c < nch ? Piece::all : Piece::none;
+                    mask[c] = piece[c] == Piece::some ? column_mask(col, i - a.window + 1 - t0, valid ? min(i, t1 - 1) - t0 : -1,
+                                                                    a.sinks - t0)
+                                                      : 0u;
+                    if (piece[c] == Piece::none) continue;
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                                                make_float2(sl2, sl2), make_float2(nl, nl));
-                    s[c][e] = __float_as_uint(ex2_ftz(x.x));
-                    s[c][e + 1] = __float_as_uint(ex2_ftz(x.y));
-                }
-            }
-            ok = __all_sync(FULL, mbar_wait(dp_full + 8 * (j & 1), (j >> 1) & 1));
-            if (!ok) break;
-            umma::fence_after_sync();
-            const uint32_t tp = tP + (j & 1) * 128 + lane_off + c0;
-            uint32_t d[2][32];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (piece[c] != Piece::none) umma::tmem_ld32(tp + c * 32, d[c]);
-            umma::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t x[16];
-                if (piece[c] == Piece::none) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0u;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 p = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
-                        const float2 y =
-                            __fmul2_rn(p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
-                                                     make_float2(dl, dl)));
-                        x[e] = bf16_pair(y.x, y.y);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                                    make_float2(sl2, sl2), make_float2(nl, nl));
+                        s[c][e] = __float_as_uint(ex2_ftz(x.x));
+                        s[c][e + 1] = __float_as_uint(ex2_ftz(x.y));
                     }
-                    if (piece[c] == Piece::some) {  // hidden keys' dS is dropped, whatever their rows held
+                }
+                ok = mbar_wait_warp(dp_full + 8 * (y & 1), (y >> 1) & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                const uint32_t tp = tP + (y & 1) * 128 + lane_off + c0;
+                uint32_t d[2][32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (piece[c] != Piece::none) umma::tmem_ld32(tp + c * 32, d[c]);
+                umma::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[16];
+                    if (piece[c] == Piece::none) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = 0u;
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const uint32_t lo = (mask[c] >> (2 * e)) & 1 ? 0x0000ffffu : 0u;
-                            const uint32_t hi = (mask[c] >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u;
-                            x[e] &= lo | hi;
+                            const float2 p = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                            const float2 z = __fmul2_rn(
+                                p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
+                                              make_float2(dl, dl)));
+                            x[e] = bf16_pair(z.x, z.y);
+                        }
+                        if (piece[c] == Piece::some) {  // hidden keys' dS is dropped, whatever their rows held
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t lo = (mask[c] >> (2 * e)) & 1 ? 0x0000ffffu : 0u;
+                                const uint32_t hi = (mask[c] >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u;
+                                x[e] &= lo | hi;
+                            }
                         }
                     }
+                    if (c < nch) umma::tmem_st16(tp + c * 16, x);
                 }
-                if (c < nch) umma::tmem_st16(tp + c * 16, x);
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                mbar_arrive(ds_full + 8 * (y & 1));
             }
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            mbar_arrive(ds_full + 8 * (j & 1));
-        }
-        if (ok) ok = __all_sync(FULL, mbar_wait(dq_full, 0));
-        if (ok) {
-            umma::fence_after_sync();
-            // the tile's Q rows are free now
-            stage_row(sm, tQ + lane_off, r, wg * (D / 64), (wg + 1) * (D / 64), ba.scale, valid);
-            umma::fence_proxy_async();
-        }
-        named_sync(1, 256);
-        if (threadIdx.x == 0 && ok) {
-#pragma unroll
-            for (int at = 0; at < NA; ++at) umma::tma_store_4d(&tmdq, sq + at * UATOM, at * 64, hq, i0, b);
-            umma::tma_store_commit();
-            umma::tma_store_wait_read();
+            kc += w.nt;
+            if (!ok) break;
+            if (w.nt > 0) {
+                ok = mbar_wait_warp(dq_full, qc & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+            }
+            __nv_bfloat16 *row = (__nv_bfloat16 *)a.dq + (((size_t)w.b * a.n + i) * a.hq + w.hq) * D;
+            store_row(row, tQ + lane_off, wg * (D / 64), (wg + 1) * (D / 64), ba.scale, i >= a.n ? 0 : valid ? 2 : 1);
+            if (w.nt > 0) {
+                umma::fence_before_sync();
+                mbar_arrive(dq_empty);
+                ++qc;
+            }
         }
     }
     umma::fence_before_sync();
@@ -361,8 +539,7 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
 template <int D>
 __global__ void __launch_bounds__(WinBwdGeom<D>::THREADS, 1)
 win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmdo,
-                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                    const __grid_constant__ CUtensorMap tmdk, const __grid_constant__ CUtensorMap tmdv, WinBwdArgs ba)
+                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, WinBwdArgs ba)
 {
     using Geo = WinBwdGeom<D>;
     constexpr int NA = Geo::NA, TILE = Geo::TILE, NQ = Geo::N3, ND = Geo::N2;
@@ -372,33 +549,17 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     const uint32_t base = smem_u32(sm);
     const uint32_t sk = base, sv = base + TILE, sq = base + Geo::OFF_3, sdo = base + Geo::OFF_2;
     const uint32_t sb = base + Geo::OFF_BAR;
-    const uint32_t kv_full = sb, tail = sb + 8, q_full = sb + 16, q_empty = q_full + 8 * NQ, do_full = q_empty + 8 * NQ;
-    const uint32_t do_empty = do_full + 8 * ND, s_full = do_empty + 8 * ND, dp_full = s_full + 8, p_full = dp_full + 8;
-    const uint32_t ds_full = p_full + 8, acc_full = ds_full + 8, mma_done = acc_full + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
+    const uint32_t kv_full = sb, kv_empty = sb + 8, tail = sb + 16, q_full = sb + 24, q_empty = q_full + 8 * NQ;
+    const uint32_t do_full = q_empty + 8 * NQ, do_empty = do_full + 8 * ND, s_full = do_empty + 8 * ND, dp_full = s_full + 8;
+    const uint32_t p_full = dp_full + 8, ds_full = p_full + 8, acc_full = ds_full + 8, acc_empty = acc_full + 8;
+    const uint32_t mma_done = acc_empty + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
     const uint32_t *tslot_p = reinterpret_cast<const uint32_t *>(sm + Geo::OFF_BAR + Geo::NBAR * 8);
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = a.B * a.hkv;
-    const int blk = (int)(blockIdx.x / (unsigned)per);  // the keys that most queries see first
-    const int bh = (int)(blockIdx.x % (unsigned)per);
-    const int b = bh / a.hkv, h = bh - b * a.hkv, t0 = blk * UW;
-    const int len = win_len(a, b);
-    const int t1 = min(t0 + UW, len);
-    const int qend = t1 > t0 ? query_end(t0, t1, len, a.window, a.sinks) : t0;
-    const int nq = (qend - t0 + UW - 1) / UW, nt = nq * a.G;  // query blocks per head, steps
-    if (nt == 0) {
-        for (int y = threadIdx.x; y < UW * (D / 8); y += Geo::THREADS) {
-            const int r = y / (D / 8), c = y - r * (D / 8);
-            if (t0 + r < a.n) {
-                const size_t at = (((size_t)b * a.n + t0 + r) * a.hkv + h) * D + c * 8;
-                *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dk + at) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.dv + at) = make_uint4(0, 0, 0, 0);
-            }
-        }
-        return;
-    }
+    ItemQueue queue(base + Geo::OFF_BAR + (Geo::NBAR - 8) * 8, sm + Geo::OFF_QUEUE);
+
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
+        mbar_init(kv_empty, 1);
         mbar_init(tail, 1);
 #pragma unroll
         for (int s = 0; s < NQ; ++s) mbar_init(q_full + 8 * s, 1), mbar_init(q_empty + 8 * s, 1);
@@ -409,7 +570,9 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
         mbar_init(p_full, 256);
         mbar_init(ds_full, 256);
         mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 256);
         mbar_init(mma_done, 1);
+        queue.init();
         mbar_init_fence();
     }
     if (warp == 9) umma::tmem_alloc(tslot, 512);
@@ -420,57 +583,74 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 256 + D;
 
     if (warp == 8) {
-        const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
-#pragma unroll
-            for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, b, bar);
-        };
-        if (lane == 0) {
-            mbar_arrive_expect(kv_full, 2 * TILE);
-            load(sk, &tmk, h, t0, kv_full);
-            load(sv, &tmv, h, t0, kv_full);
-        }
+        uint32_t kc = 0, fixes = 0;  // steps so far
+        int qc = 0;                  // items with steps so far
         bool ok = true;
-        int fixes = 0;
-        for (int j = 0; ok && j < nt; ++j) {
-            const int s3 = j % NQ, s2 = j % ND, g = j / nq, i0 = t0 + (j - g * nq) * UW, hq = h * a.G + g;
-            const float *nl = ba.nl + ((size_t)b * a.hq + hq) * ba.npad + i0;
-            const float *dl = ba.ndelta + ((size_t)b * a.hq + hq) * ba.npad + i0;
-            const bool fix = i0 + UW > len && len < a.n;  // dK and dV sum over these rows
-            if (lane == 0 && j >= NQ) ok = mbar_wait(q_empty + 8 * s3, ((j / NQ) - 1) & 1);
-            if (lane == 0 && ok && j >= ND) ok = mbar_wait(do_empty + 8 * s2, ((j / ND) - 1) & 1);
+        // the first item by position, the others from the counter, asked for one item ahead
+        int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
+        for (;;) {
+            ok = queue.push(item, lane);
+            if (!ok || item >= ba.items) break;
+            const DkvItem w(ba, item);
+            item = __shfl_sync(FULL, ahead, 0);
+            if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
+            if (w.j1 <= w.j0) continue;
+            const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
+#pragma unroll
+                for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
+            };
+            if (lane == 0 && qc > 0) ok = mbar_wait(kv_empty, (qc - 1) & 1);
             ok = __shfl_sync(FULL, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                const uint32_t bq = fix ? tail : q_full + 8 * s3, bd = fix ? tail : do_full + 8 * s2;
+                mbar_arrive_expect(kv_full, 2 * TILE);
+                load(sk, &tmk, w.h, w.t0, kv_full);
+                load(sv, &tmv, w.h, w.t0, kv_full);
+            }
+            ++qc;
+            for (int j = w.j0; ok && j < w.j1; ++j, ++kc) {
+                const uint32_t s3 = kc % NQ, s2 = kc % ND;
+                const int g = j / w.nq, i0 = w.t0 + (j - g * w.nq) * UW, hq = w.h * a.G + g;
+                const float *nl = ba.nl + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
+                const float *dl = ba.ndelta + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
+                const bool fix = i0 + UW > w.len && w.len < a.n;  // dK and dV sum over these rows
+                if (lane == 0 && kc >= NQ) ok = mbar_wait(q_empty + 8 * s3, ((kc / NQ) - 1) & 1);
+                if (lane == 0 && ok && kc >= ND) ok = mbar_wait(do_empty + 8 * s2, ((kc / ND) - 1) & 1);
+                ok = __shfl_sync(FULL, ok, 0);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t bq = fix ? tail : q_full + 8 * s3, bd = fix ? tail : do_full + 8 * s2;
+                    if (fix) {
+                        mbar_arrive_expect(tail, 2 * (TILE + 512));
+                    } else {
+                        mbar_arrive_expect(bq, TILE + 512);
+                        mbar_arrive_expect(bd, TILE + 512);
+                    }
+                    load(sq + s3 * TILE, &tmq, hq, i0, bq);
+                    bulk_load(base + Geo::OFF_NL + s3 * 512, nl, 512, bq);
+                    load(sdo + s2 * TILE, &tmdo, hq, i0, bd);
+                    bulk_load(base + Geo::OFF_DELTA + s2 * 512, dl, 512, bd);
+                }
                 if (fix) {
-                    mbar_arrive_expect(tail, 2 * (TILE + 512));
-                } else {
-                    mbar_arrive_expect(bq, TILE + 512);
-                    mbar_arrive_expect(bd, TILE + 512);
-                }
-                load(sq + s3 * TILE, &tmq, hq, i0, bq);
-                bulk_load(base + Geo::OFF_NL + s3 * 512, nl, 512, bq);
-                load(sdo + s2 * TILE, &tmdo, hq, i0, bd);
-                bulk_load(base + Geo::OFF_DELTA + s2 * 512, dl, 512, bd);
-            }
-            if (fix) {
-                ok = __all_sync(FULL, mbar_wait(tail, fixes++ & 1));
-                if (ok) {
-                    zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(len - i0, 0), lane);
-                    zero_rows<NA, UW>(sm + Geo::OFF_2 + s2 * TILE, max(len - i0, 0), lane);
-                }
-                umma::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0 && ok) {
-                    mbar_arrive(q_full + 8 * s3);
-                    mbar_arrive(do_full + 8 * s2);
+                    ok = mbar_wait_warp(tail, fixes++ & 1);
+                    if (ok) {
+                        zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - i0, 0), lane);
+                        zero_rows<NA, UW>(sm + Geo::OFF_2 + s2 * TILE, max(w.len - i0, 0), lane);
+                    }
+                    umma::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0 && ok) {
+                        mbar_arrive(q_full + 8 * s3);
+                        mbar_arrive(do_full + 8 * s2);
+                    }
                 }
             }
+            if (!ok) break;
         }
-        if (lane == 0 && !ok) {
-            mbar_wait(kv_full, 0);
-            for (int s = 0; s < NQ; ++s) mbar_wait(q_full + 8 * s, 0);
-            for (int s = 0; s < ND; ++s) mbar_wait(do_full + 8 * s, 0);
+        if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
+            mbar_wait(kv_full, (qc - 1) & 1);
+            for (uint32_t y = kc > NQ ? kc - NQ : 0; y < kc; ++y) mbar_wait(q_full + 8 * (y % NQ), (y / NQ) & 1);
+            for (uint32_t y = kc > ND ? kc - ND : 0; y < kc; ++y) mbar_wait(do_full + 8 * (y % ND), (y / ND) & 1);
         }
     } else if (warp == 9) {
         // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
@@ -478,147 +658,174 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
         const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
         const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), qt_lo = umma::sdesc_lo(sq, UATOM);
         const uint32_t do_lo = umma::sdesc_lo(sdo, umma::KMAJOR), dot_lo = umma::sdesc_lo(sdo, UATOM);
-        const auto scores = [&](int j) {
-            if (!mbar_wait_warp(q_full + 8 * (j % NQ), (j / NQ) & 1)) return false;
+        const auto scores = [&](uint32_t y) {
+            if (!mbar_wait_warp(q_full + 8 * (y % NQ), (y / NQ) & 1)) return false;
             umma::fence_after_sync();
-            mma_tiles<D>(lead, tS, k_lo, q_lo + (j % NQ) * (TILE >> 4), UW);
+            mma_tiles<D>(lead, tS, k_lo, q_lo + (y % NQ) * (TILE >> 4), UW);
             umma::commit_if(lead, s_full);
             return true;
         };
-        const auto dps = [&](int j) {
-            if (!mbar_wait_warp(do_full + 8 * (j % ND), (j / ND) & 1)) return false;
+        const auto dps = [&](uint32_t y, bool last) {
+            if (!mbar_wait_warp(do_full + 8 * (y % ND), (y / ND) & 1)) return false;
             umma::fence_after_sync();
-            mma_tiles<D>(lead, tP, v_lo, do_lo + (j % ND) * (TILE >> 4), UW);
+            mma_tiles<D>(lead, tP, v_lo, do_lo + (y % ND) * (TILE >> 4), UW);
             umma::commit_if(lead, dp_full);
+            if (last) umma::commit_if(lead, kv_empty);
             return true;
         };
-        bool ok = mbar_wait_warp(kv_full, 0) && scores(0) && dps(0);
-        for (int j = 0; ok && j < nt; ++j) {
-            ok = mbar_wait_warp(p_full, j & 1);
-            if (!ok) break;
-            umma::fence_after_sync();
-            mma_accumulate<D>(lead, tV, tS, dot_lo + (j % ND) * (TILE >> 4), UW, j > 0);
-            if (j + 1 < nt) ok = scores(j + 1);
-            if (ok) ok = mbar_wait_warp(ds_full, j & 1);
-            if (!ok) break;
-            umma::fence_after_sync();
-            mma_accumulate<D>(lead, tK, tP, qt_lo + (j % NQ) * (TILE >> 4), UW, j > 0);
-            umma::commit_if(lead, q_empty + 8 * (j % NQ));
-            umma::commit_if(lead, do_empty + 8 * (j % ND));
-            if (j + 1 < nt) ok = dps(j + 1);
+        uint32_t kc = 0;
+        int qc = 0;
+        bool ok = true;
+        while (ok) {
+            const int item = queue.pop(lane);
+            if (item < 0 || item >= ba.items) break;
+            const DkvItem w(ba, item);
+            const int nt = w.j1 - w.j0;
+            if (nt <= 0) continue;
+            ok = mbar_wait_warp(kv_full, qc & 1) && scores(kc) && dps(kc, nt == 1);
+            for (int j = 0; ok && j < nt; ++j) {
+                const uint32_t y = kc + j;
+                if (j == 0 && qc > 0) ok = mbar_wait_warp(acc_empty, (qc - 1) & 1);
+                if (ok) ok = mbar_wait_warp(p_full, y & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                mma_accumulate<D>(lead, tV, tS, dot_lo + (y % ND) * (TILE >> 4), UW, j > 0);
+                if (j + 1 < nt) ok = scores(y + 1);
+                if (ok) ok = mbar_wait_warp(ds_full, y & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                mma_accumulate<D>(lead, tK, tP, qt_lo + (y % NQ) * (TILE >> 4), UW, j > 0);
+                umma::commit_if(lead, q_empty + 8 * (y % NQ));
+                umma::commit_if(lead, do_empty + 8 * (y % ND));
+                if (j + 1 < nt) ok = dps(y + 1, j + 2 == nt);
+            }
+            if (ok) umma::commit_if(lead, acc_full);
+            kc += nt;
+            ++qc;
         }
-        if (ok) umma::commit_if(lead, acc_full);
+        // every MMA issued has completed before the CTA releases its tensor memory
         umma::commit_if(lead, mma_done);
         mbar_wait_warp(mma_done, 0);
     } else {
-        const int wg = warp >> 2, r = (warp & 3) * 32 + lane, t = t0 + r;
-        const bool valid = t < len;
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
         const float sl2 = a.scale;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const int c0 = wg * 64;
-        const int last = t < a.sinks ? len - 1 : min(len - 1, t + a.window - 1);  // last query that sees the key
+        uint32_t kc = 0;
+        int qc = 0;
         bool ok = true;
-        for (int j = 0; j < nt; ++j) {
-            const int g = j / nq, i0 = t0 + (j - g * nq) * UW;
-            const bool whole = i0 >= t0 + UW - 1 && (i0 + UW - 1 <= t0 + a.window - 1 || t0 + UW <= a.sinks);
-            ok = __all_sync(FULL, mbar_wait(q_full + 8 * (j % NQ), (j / NQ) & 1) && mbar_wait(s_full, j & 1));
-            if (!ok) break;
-            umma::fence_after_sync();
-            const float4 *nl = reinterpret_cast<const float4 *>(sm + Geo::OFF_NL + (j % NQ) * 512) + wg * 16;
-            // pieces of 32 queries: which keys of the warp's 32 rows do they see?
-            Piece piece[2];
-            uint32_t mask[2], s[2][32];
+        while (ok) {
+            const int item = queue.pop(lane);
+            if (item < 0 || item >= ba.items) break;
+            const DkvItem w(ba, item);
+            const int len = w.len, t0 = w.t0, t = t0 + r;
+            const bool valid = t < len;
+            const int last = t < a.sinks ? len - 1 : min(len - 1, t + a.window - 1);  // last query that sees the key
+            for (int j = w.j0; j < w.j1; ++j) {
+                const uint32_t y = kc + j - w.j0;
+                const int g = j / w.nq, i0 = t0 + (j - g * w.nq) * UW;
+                const bool whole = i0 >= t0 + UW - 1 && (i0 + UW - 1 <= t0 + a.window - 1 || t0 + UW <= a.sinks);
+                ok = mbar_wait_warp(q_full + 8 * (y % NQ), (y / NQ) & 1) && mbar_wait_warp(s_full, y & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                const float4 *nl = reinterpret_cast<const float4 *>(sm + Geo::OFF_NL + (y % NQ) * 512) + wg * 16;
+                // pieces of 32 queries: which keys of the warp's 32 rows do they see?
+                Piece piece[2];
+                uint32_t mask[2], s[2][32];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                piece[c] = whole ? Piece::all : query_piece(t0 + (warp & 3) * 32, i0 + c0 + c * 32, len, a.window, a.sinks);
-                mask[c] = piece[c] == Piece::some ? column_mask(c0 + c * 32, t - i0, last - i0, 0) : 0u;
-                if (piece[c] != Piece::none) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
-            }
-            umma::tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t x[16];
-                if (piece[c] == Piece::none) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0u;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 y = nl[c * 8 + e];
-                        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
-                                                     make_float2(sl2, sl2), make_float2(y.x, y.y));
-                        const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
-                                                     make_float2(sl2, sl2), make_float2(y.z, y.w));
-                        s[c][4 * e] = __float_as_uint(ex2_ftz(x0.x));
-                        s[c][4 * e + 1] = __float_as_uint(ex2_ftz(x0.y));
-                        s[c][4 * e + 2] = __float_as_uint(ex2_ftz(x1.x));
-                        s[c][4 * e + 3] = __float_as_uint(ex2_ftz(x1.y));
-                    }
-                    if (piece[c] == Piece::some) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((mask[c] >> e) & 1)) s[c][e] = 0u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        x[e] = bf16_pair(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
+                for (int c = 0; c < 2; ++c) {
+                    piece[c] = whole ? Piece::all : query_piece(t0 + (warp & 3) * 32, i0 + c0 + c * 32, len, a.window, a.sinks);
+                    mask[c] = piece[c] == Piece::some ? column_mask(c0 + c * 32, t - i0, last - i0, 0) : 0u;
+                    if (piece[c] != Piece::none) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
                 }
-                umma::tmem_st16(tS + lane_off + c0 + c * 16, x);
-            }
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            mbar_arrive(p_full);
-            ok = __all_sync(FULL, mbar_wait(do_full + 8 * (j % ND), (j / ND) & 1) && mbar_wait(dp_full, j & 1));
-            if (!ok) break;
-            umma::fence_after_sync();
-            const float4 *dl = reinterpret_cast<const float4 *>(sm + Geo::OFF_DELTA + (j % ND) * 512) + wg * 16;  // -delta
-            uint32_t d[2][32];
+                umma::tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (piece[c] != Piece::none) umma::tmem_ld32(tP + lane_off + c0 + c * 32, d[c]);
-            umma::tmem_wait_ld();
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[16];
+                    if (piece[c] == Piece::none) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t x[16];
-                if (piece[c] == Piece::none) {
+                        for (int e = 0; e < 16; ++e) x[e] = 0u;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = 0u;
-                } else {
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 z = nl[c * 8 + e];
+                            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                         make_float2(sl2, sl2), make_float2(z.x, z.y));
+                            const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                         make_float2(sl2, sl2), make_float2(z.z, z.w));
+                            s[c][4 * e] = __float_as_uint(ex2_ftz(x0.x));
+                            s[c][4 * e + 1] = __float_as_uint(ex2_ftz(x0.y));
+                            s[c][4 * e + 2] = __float_as_uint(ex2_ftz(x1.x));
+                            s[c][4 * e + 3] = __float_as_uint(ex2_ftz(x1.y));
+                        }
+                        if (piece[c] == Piece::some) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 y = dl[c * 8 + e];
-                        const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
-                                                     __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e]), __uint_as_float(d[c][4 * e + 1])),
-                                                                make_float2(y.x, y.y)));
-                        const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
-                                                     __fadd2_rn(make_float2(__uint_as_float(d[c][4 * e + 2]), __uint_as_float(d[c][4 * e + 3])),
-                                                                make_float2(y.z, y.w)));
-                        x[2 * e] = bf16_pair(x0.x, x0.y);
-                        x[2 * e + 1] = bf16_pair(x1.x, x1.y);
+                            for (int e = 0; e < 32; ++e)
+                                if (!((mask[c] >> e) & 1)) s[c][e] = 0u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            x[e] = bf16_pair(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
                     }
+                    umma::tmem_st16(tS + lane_off + c0 + c * 16, x);
                 }
-                umma::tmem_st16(tP + lane_off + c0 + c * 16, x);
-            }
-            umma::tmem_wait_st();
-            umma::fence_before_sync();
-            mbar_arrive(ds_full);
-        }
-        if (ok) ok = __all_sync(FULL, mbar_wait(acc_full, 0));
-        if (ok) {
-            umma::fence_after_sync();
-            // the K and V tiles are free now: dk goes out through the first, dv through the second
-            stage_row(sm + wg * TILE, (wg ? tV : tK) + lane_off, r, 0, D / 32, wg ? 1.0f : ba.scale, valid);
-            umma::fence_proxy_async();
-        }
-        named_sync(1, 256);
-        if (threadIdx.x == 0 && ok) {
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                mbar_arrive(p_full);
+                ok = mbar_wait_warp(do_full + 8 * (y % ND), (y / ND) & 1) && mbar_wait_warp(dp_full, y & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+                const float4 *dl = reinterpret_cast<const float4 *>(sm + Geo::OFF_DELTA + (y % ND) * 512) + wg * 16;  // -delta
 #pragma unroll
-            for (int at = 0; at < NA; ++at) {
-                umma::tma_store_4d(&tmdk, sk + at * UATOM, at * 64, h, t0, b);
-                umma::tma_store_4d(&tmdv, sv + at * UATOM, at * 64, h, t0, b);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[16], d[32];
+                    if (piece[c] == Piece::none) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) x[e] = 0u;
+                    } else {
+                        umma::tmem_ld32(tP + lane_off + c0 + c * 32, d);
+                        umma::tmem_wait_ld32(d);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 z = dl[c * 8 + e];
+                            const float2 x0 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])),
+                                                         __fadd2_rn(make_float2(__uint_as_float(d[4 * e]), __uint_as_float(d[4 * e + 1])),
+                                                                    make_float2(z.x, z.y)));
+                            const float2 x1 = __fmul2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])),
+                                                         __fadd2_rn(make_float2(__uint_as_float(d[4 * e + 2]), __uint_as_float(d[4 * e + 3])),
+                                                                    make_float2(z.z, z.w)));
+                            x[2 * e] = bf16_pair(x0.x, x0.y);
+                            x[2 * e + 1] = bf16_pair(x1.x, x1.y);
+                        }
+                    }
+                    // dS of piece c lies over dP of this or an earlier piece of the group
+                    umma::tmem_st16(tP + lane_off + c0 + c * 16, x);
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                mbar_arrive(ds_full);
             }
-            umma::tma_store_commit();
-            umma::tma_store_wait_read();
+            const int nt = w.j1 - w.j0;
+            kc += nt;
+            if (!ok) break;
+            if (nt > 0) {
+                ok = mbar_wait_warp(acc_full, qc & 1);
+                if (!ok) break;
+                umma::fence_after_sync();
+            }
+            // one group writes dk, the other dv
+            if (w.cut) {
+                if (nt > 0) store_row(ba.part + ((size_t)w.slot * 2 + wg) * (UW * D) + (size_t)r * D, (wg ? tV : tK) + lane_off, 0,
+                                      D / 32, wg ? 1.0f : ba.scale, 2);
+            } else {
+                __nv_bfloat16 *row = (__nv_bfloat16 *)(wg ? a.dv : a.dk) + (((size_t)w.b * a.n + t) * a.hkv + w.h) * D;
+                store_row(row, (wg ? tV : tK) + lane_off, 0, D / 32, wg ? 1.0f : ba.scale, t >= a.n ? 0 : valid ? 2 : 1);
+            }
+            if (nt > 0) {
+                umma::fence_before_sync();
+                mbar_arrive(acc_empty);
+                ++qc;
+            }
         }
     }
     umma::fence_before_sync();
@@ -627,6 +834,33 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
         umma::fence_after_sync();
         umma::tmem_dealloc(tmem, 512);
     }
+}
+
+// dk and dv of key blocks that were cut: their pieces' partial sums, added in order. One thread per
+// four elements; first_item: the block's first piece.
+template <int D> __global__ void __launch_bounds__(256) win_dkv_join_kernel(WinBwdArgs ba, int64_t first_item, int chunks)
+{
+    const WinArgs &a = ba.w;
+    constexpr int PER = 2 * UW * D / 4;  // threads per key block
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t block = x / PER;
+    const int e = (int)(x - block * PER), kv = e / (UW * D / 4), at = (e - kv * (UW * D / 4)) * 4;
+    const int r = at / D, d = at - r * D;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const DkvItem w(ba, first_item + block * chunks);
+    const int t = w.t0 + r;
+    if (t >= a.n) return;
+    if (t < w.len) {
+        for (int c = 0; c < chunks; ++c) {
+            const DkvItem y(ba, first_item + block * chunks + c);
+            if (y.j1 <= y.j0) break;
+            const float4 v = *reinterpret_cast<const float4 *>(ba.part + ((size_t)y.slot * 2 + kv) * (UW * D) + at);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+    }
+    const __nv_bfloat162 p[2] = {__floats2bfloat162_rn(sum.x, sum.y), __floats2bfloat162_rn(sum.z, sum.w)};
+    __nv_bfloat16 *row = (__nv_bfloat16 *)(kv ? a.dv : a.dk) + (((size_t)w.b * a.n + t) * a.hkv + w.h) * D + d;
+    *reinterpret_cast<uint2 *>(row) = *reinterpret_cast<const uint2 *>(p);
 }
 
 }  // namespace gm

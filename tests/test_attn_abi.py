@@ -52,10 +52,14 @@ def test_window_pointers(lib):
     assert backward(lib) == bnd.GM_ERR_INVALID_ARG  # misaligned dq
     for x in ("q", "k", "v", "o", "dout", "lse", "dk", "dv", "ws"):
         assert backward(lib, **{x: NULL}) == bnd.GM_ERR_INVALID_ARG
-    need = lib.gm_window_attention_backward_workspace_size(1, 8, 4)
+    size = lib.gm_window_attention_backward_workspace_size
+    need = size(bnd.GM_BF16, 1, 8, 4, 2, 64, 3, 1)
     assert need >= 8 * 4 * 4
     assert backward(lib, dq=FAKE, size=need - 1) == bnd.GM_ERR_INVALID_ARG
-    assert lib.gm_window_attention_backward_workspace_size(0, 8, 4) == 0
+    assert size(bnd.GM_BF16, 0, 8, 4, 2, 64, 3, 1) == 0 and size(bnd.GM_BF16, 1, 8, 4, 3, 64, 3, 1) == 0
+    assert size(bnd.GM_F32, 1, 8, 4, 2, 64, 3, 1) >= 8 * 4 * 4
+    # a few keys that every query of a long sequence sees: their steps are shared out
+    assert size(bnd.GM_BF16, 1, 32768, 16, 8, 128, 512, 4) > size(bnd.GM_BF16, 1, 32768, 16, 8, 128, 512, 0)
 
 
 CACHE = dict(kq=FAKE, vq=FAKE, ks=FAKE, vs=FAKE, pages=4, page=16, table=FAKE, maxp=2, lens=FAKE)

@@ -76,6 +76,18 @@ def test_long_sequence_with_a_small_window(dtype):
     run_and_check(1, 2500, 2, 1, 64, dtype, 33, 70, seed=5)
 
 
+@pytest.mark.parametrize("window,sinks", [(64, 0), (64, 5), (64, 300), (None, 0), (700, 130)])
+@pytest.mark.parametrize("lens", [None, [3000, 1700, 2]])
+def test_many_blocks_cut_and_uncut(window, sinks, lens):
+    """Long sequences of few heads: key blocks whose steps are shared out among CTAs."""
+    run_and_check(3, 3000, 4, 1, 64, torch.bfloat16, window, sinks, lens=lens, seed=9)
+
+
+def test_more_items_than_SMs():
+    """Every CTA takes several items, some of them empty."""
+    run_and_check(20, 300, 8, 4, 64, torch.bfloat16, 100, 3, lens=[300, 0, 131, 17, 256] * 4, seed=10)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_peaked_and_flat_rows(dtype):
     run_and_check(1, 200, 2, 2, 128, dtype, 100, 2, seed=6, size=12.0)
@@ -118,7 +130,7 @@ def test_padding_may_hold_anything(fill, dtype):
 def test_two_calls_give_the_same_bits_into_given_outputs(dtype):
     (q, k, v, dout, _), first = run_and_check(2, 500, 4, 2, 128, dtype, 90, 10, seed=21)
     given = [torch.full_like(x, 7.0) for x in first]
-    ws = torch.full((gm.gm_window_attention_backward_workspace_size(2, 500, 4),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((gm.gm_window_attention_backward_workspace_size(dtype, 2, 500, 4, 2, 128, 90, 10),), 255, dtype=torch.uint8, device="cuda")
     gm.gm_window_attention_forward(q, k, v, 90, 10, o=given[0], lse=given[1])
     gm.gm_window_attention_backward(q, k, v, given[0], dout, given[1], 90, 10, dq=given[2], dk=given[3], dv=given[4],
                                     workspace=ws)
@@ -174,7 +186,7 @@ def test_captured_and_replayed_on_a_side_stream(dtype):
     (q, k, v, dout, _), want = run_and_check(1, 400, 4, 2, 64, dtype, 60, 4, seed=51)
     x = [torch.zeros_like(y) for y in (q, k, v, dout)]
     outs = [torch.empty_like(y) for y in want]
-    ws = torch.empty(gm.gm_window_attention_backward_workspace_size(1, 400, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gm.gm_window_attention_backward_workspace_size(dtype, 1, 400, 4, 2, 64, 60, 4), dtype=torch.uint8, device="cuda")
 
     def step():
         gm.gm_window_attention_forward(*x[:3], 60, 4, o=outs[0], lse=outs[1])

@@ -154,13 +154,16 @@ WinBwdPlan window_backward_plan(int B, int n, int hq, int hkv, int d, int window
     int64_t total = 0;
     for (int64_t b = 0; b < p.nblk; ++b) total += (b < p.sink_blocks ? p.nblk - b : std::min(near, p.nblk - b)) * G;
     total *= per;
-    // Blocks are cut where the longest would take half as long again as an SM's share of it all
-    // (B=1 n=32768 window 512 with sinks: 1520 -> 900 us); otherwise the writes and reads of 2 x 128 x
-    // d fp32 sums per piece cost more than the balance gives (B=1 n=4096 full: 275 -> 356 us).
-    const int64_t share = (total + 147) / 148, piece = std::max<int64_t>(8, share / 2);
-    const auto pieces = [&](int64_t steps) { return (int)(2 * steps > 3 * share && steps >= 16 ? (steps + piece - 1) / piece : 1); };
-    p.sink_chunks = p.sink_blocks ? pieces(sink_most) : 1;
-    p.chunks = pieces(most);
+    // Blocks are cut where the longest would take half as long again as an SM's share of it all, sink
+    // blocks, of which there are few, at half of that share (B=1 n=32768 window 512 with sinks: 1520 ->
+    // 900 us); elsewhere the writes and reads of 2 x 128 x d fp32 sums per piece cost more than the
+    // balance gives (B=1 n=4096 full: 275 -> 356 us).
+    const int64_t share = (total + 147) / 148;
+    const auto pieces = [&](int64_t steps, int64_t longest, int64_t piece) {
+        return (int)(steps >= 16 && steps > longest ? (steps + std::max<int64_t>(8, piece) - 1) / std::max<int64_t>(8, piece) : 1);
+    };
+    p.sink_chunks = p.sink_blocks ? pieces(sink_most, share / 2, share / 4) : 1;
+    p.chunks = pieces(most, 3 * share / 2, share / 2);
     p.sink_steps = p.sink_chunks > 1 ? (int)((sink_most + p.sink_chunks - 1) / p.sink_chunks) : INT32_MAX;
     p.steps = p.chunks > 1 ? (int)((most + p.chunks - 1) / p.chunks) : INT32_MAX;
     p.sink_items = per * p.sink_blocks * p.sink_chunks;
@@ -199,7 +202,7 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
     a.ndelta = ndelta;
     a.next = (int *)(ndelta + rows);
     a.part = (float *)((char *)w.delta + p.stats_bytes);
-    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 255) / 256), 256, 0, st>>>(a, nl, ndelta);
+    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 1023) / 1024), 256, 0, st>>>(a, nl, ndelta);
     a.items = (int64_t)p.nblk * w.B * w.hq;
     kq<<<(unsigned)std::min<int64_t>(a.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, a);
     a.items = p.items;

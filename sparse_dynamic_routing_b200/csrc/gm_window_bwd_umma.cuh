@@ -111,34 +111,48 @@ template <int D> struct WinBwdGeom {
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
-// nl and -delta of every row; D/8 lanes per row.
-// Also sets both counters to 0.
+// nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking four rows 256 / (D/8)
+// apart so that eight 16-byte loads are in flight. Also sets both counters to 0. Bound by HBM: o
+// and dout once.
 template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdArgs a, float *nl, float *ndelta)
 {
     if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
-    constexpr int C = D / 8, RPB = 256 / C;
+    constexpr int C = D / 8, RPB = 256 / C, N = 4;
     const WinArgs &w = a.w;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / C;  // (b, i < npad, hq)
     const int c = threadIdx.x % C;
-    const int64_t bi = row / w.hq;
-    const int hq = (int)(row - bi * w.hq);
-    const int b = (int)(bi / a.npad), i = (int)(bi - (int64_t)b * a.npad);
-    const bool in = b < w.B;
-    const bool valid = in && i < win_len(w, b);
-    float x = 0.0f;
-    if (valid) {
-        const size_t at = (((size_t)b * w.n + i) * w.hq + hq) * D + c * 8;
-        float fo[8], fg[8];
-        unpack<__nv_bfloat16>(ld16((const __nv_bfloat16 *)w.o_in + at), fo);
-        unpack<__nv_bfloat16>(ld16((const __nv_bfloat16 *)w.dout + at), fg);
+    const int64_t row0 = (int64_t)blockIdx.x * (RPB * N) + threadIdx.x / C;
+    uint4 uo[N], ug[N];
+    float lse[N];
+    bool in[N], valid[N];
+    int64_t to[N];
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        const int64_t row = row0 + r * RPB, bi = row / w.hq, b = bi / a.npad;
+        const int hq = (int)(row - bi * w.hq), i = (int)(bi - b * a.npad);
+        in[r] = b < w.B;
+        valid[r] = in[r] && i < win_len(w, (int)b);
+        to[r] = (b * w.hq + hq) * a.npad + i;
+        const int64_t src = (b * w.n + i) * w.hq + hq;
+        uo[r] = ug[r] = make_uint4(0, 0, 0, 0);
+        lse[r] = 0.0f;
+        if (valid[r]) {
+            uo[r] = ld16_stream((const __nv_bfloat16 *)w.o_in + src * D + c * 8);
+            ug[r] = ld16((const __nv_bfloat16 *)w.dout + src * D + c * 8);
+            if (c == 0) lse[r] = __ldg(w.lse_in + src);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        float fo[8], fg[8], x = 0.0f;
+        unpack<__nv_bfloat16>(uo[r], fo);
+        unpack<__nv_bfloat16>(ug[r], fg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += fo[e] * fg[e];
-    }
-    x = seg_sum<C>(x);
-    if (in && c == 0) {
-        const size_t to = ((size_t)b * w.hq + hq) * a.npad + i;
-        nl[to] = valid ? -LOG2E * __ldg(w.lse_in + ((size_t)b * w.n + i) * w.hq + hq) : -INFINITY;
-        ndelta[to] = -x;
+        x = seg_sum<C>(x);
+        if (in[r] && c == 0) {
+            nl[to[r]] = valid[r] ? -LOG2E * lse[r] : -INFINITY;
+            ndelta[to[r]] = -x;
+        }
     }
 }
 

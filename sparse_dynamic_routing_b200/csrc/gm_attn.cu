@@ -58,27 +58,59 @@ gm::WinArgs window_args(int B, int n, int hq, int hkv, int window, int sinks, fl
     return a;
 }
 
-template <int D> gm_status window_forward(gm::WinArgs a, cudaStream_t st)
+// Rows per thread of the fp32 kernels: 4 where blocks of 64 rows fill the SMs one and a half times,
+// else 2 or 1 (gm_window.cuh).
+int f32_rows(int n, int64_t heads)
 {
-    constexpr size_t smem = gm::WinF32<D>::fwd_smem;
-    auto kern = gm::win_fwd_f32_kernel<D>;
-    if (!raise_smem(kern, smem)) return GM_ERR_CUDA;
-    a.nblk = (a.n + gm::WT - 1) / gm::WT;
-    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
+    const int64_t blocks = (n + 63) / 64 * heads;
+    return blocks >= 222 ? 4 : blocks >= 74 ? 2 : 1;
+}
+
+template <int D, int R> gm_status window_forward_f32(gm::WinArgs a, cudaStream_t st)
+{
+    using S = gm::WinF32<D, R>;
+    auto kern = gm::win_fwd_f32_kernel<D, R>;
+    if (!raise_smem(kern, S::fwd_smem)) return GM_ERR_CUDA;
+    a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
+    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, S::fwd_smem, st>>>(a);
     return launched();
 }
 
-template <int D> gm_status window_backward(gm::WinArgs a, cudaStream_t st)
+template <int D> gm_status window_forward(const gm::WinArgs &a, cudaStream_t st)
 {
-    constexpr size_t smem = gm::WinF32<D>::bwd_smem;
-    auto kq = gm::win_dq_f32_kernel<D>;
-    auto kkv = gm::win_dkv_f32_kernel<D>;
-    if (!raise_smem(kq, smem) || !raise_smem(kkv, smem)) return GM_ERR_CUDA;
-    a.nblk = (a.n + gm::WT - 1) / gm::WT;
-    gm::win_delta_kernel<D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
-    kq<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, smem, st>>>(a);
-    kkv<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, smem, st>>>(a);
+    const int r = f32_rows(a.n, (int64_t)a.B * a.hq);
+    return r == 4 ? window_forward_f32<D, 4>(a, st) : r == 2 ? window_forward_f32<D, 2>(a, st) : window_forward_f32<D, 1>(a, st);
+}
+
+template <int D, int R> gm_status window_dq_f32(gm::WinArgs a, cudaStream_t st)
+{
+    using S = gm::WinF32<D, R>;
+    auto kern = gm::win_dq_f32_kernel<D, R>;
+    if (!raise_smem(kern, S::dq_smem)) return GM_ERR_CUDA;
+    a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
+    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, S::dq_smem, st>>>(a);
     return launched();
+}
+
+template <int D, int R> gm_status window_dkv_f32(gm::WinArgs a, cudaStream_t st)
+{
+    using S = gm::WinF32<D, R>;
+    auto kern = gm::win_dkv_f32_kernel<D, R>;
+    if (!raise_smem(kern, S::dkv_smem)) return GM_ERR_CUDA;
+    a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
+    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, S::dkv_smem, st>>>(a);
+    return launched();
+}
+
+template <int D> gm_status window_backward(const gm::WinArgs &a, cudaStream_t st)
+{
+    gm::win_delta_kernel<D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
+    const int rq = f32_rows(a.n, (int64_t)a.B * a.hq), rk = f32_rows(a.n, (int64_t)a.B * a.hkv);
+    const gm_status s = rq == 4   ? window_dq_f32<D, 4>(a, st)
+                        : rq == 2 ? window_dq_f32<D, 2>(a, st)
+                                  : window_dq_f32<D, 1>(a, st);
+    if (s != GM_OK) return s;
+    return rk == 4 ? window_dkv_f32<D, 4>(a, st) : rk == 2 ? window_dkv_f32<D, 2>(a, st) : window_dkv_f32<D, 1>(a, st);
 }
 
 // A bf16 feature tensor [B, n, heads, d] as a 4-d TMA map whose boxes are 64 elements of d (128

@@ -13,8 +13,11 @@
 // [0, min(sinks, lo)). The kernels walk exactly those ranges in key blocks, so the work follows
 // the visible pairs and not n^2.
 //
-// fp32 kernels (this file). Plain FFMA tiles of 64 queries x 64 keys: 256 threads in a 16 x 16
-// grid, each holding a 4 x 4 piece of the scores and 4 rows x D/16 columns of the output.
+// fp32 kernels (this file). Packed FFMA tiles of 16 R rows x 64 columns: 256 threads in a 16 x 16
+// grid, each holding an R x 4 piece of the scores and R rows x D/16 columns of the output. Rows
+// are queries in the forward and in dq, keys in dk and dv. R = 4 has the fewest shared-memory
+// reads per product; R = 2 and 1 make more and shorter blocks where a call would leave SMs idle
+// (B=1 n=128, two heads: 125 us with R = 4, 53 us with R = 1, forward and backward).
 // Bound by the fp32 pipes; there is no tensor-core type that keeps fp32's 24 bits. The backward
 // is two kernels without atomics: one per query block (dq) and one per key block (dk, dv, summed
 // over the group's heads in the block), so every gradient is written once, in a fixed order.
@@ -79,84 +82,102 @@ __device__ __forceinline__ int query_end(int t0, int t1, int len, int window, in
 
 // ---- fp32 tiles -----------------------------------------------------------------------------
 
-constexpr int WT = 64;    // rows and columns of a tile
+constexpr int WT = 64;    // columns of a tile
 constexpr int WLP = 68;   // padded row of a score tile, floats
 
-template <int D> struct WinF32 {
+template <int D, int R> struct WinF32 {
+    static constexpr int ROWS = 16 * R;
     static constexpr int LD = D + 4;  // padded feature row, floats: rows 4 banks apart
     static constexpr int NC = D / 64; // float4 column groups per thread
-    static constexpr size_t fwd_smem = (size_t)(3 * WT * LD + WT * WLP) * 4;
-    static constexpr size_t bwd_smem = (size_t)(4 * WT * LD + 2 * WT * WLP) * 4;
+    static constexpr size_t fwd_smem = (size_t)((ROWS + 2 * WT) * LD + ROWS * WLP) * 4;
+    static constexpr size_t dq_smem = (size_t)((2 * ROWS + 2 * WT) * LD + ROWS * WLP) * 4;
+    static constexpr size_t dkv_smem = (size_t)((2 * ROWS + 2 * WT) * LD + 2 * ROWS * WLP) * 4;
 };
 
-// Rows [r0, r0 + 64) of one head of a [.., heads, D] tensor into a tile; rows at or past `end`
+// Rows [r0, r0 + N) of one head of a [.., heads, D] tensor into a tile; rows at or past `end`
 // (padding may hold anything) become zeros.
-template <int D>
+template <int D, int N>
 __device__ __forceinline__ void load_tile(float *dst, const float *src, size_t row_stride, int r0, int end)
 {
-    constexpr int C = D / 4;
-    for (int x = threadIdx.x; x < WT * C; x += 256) {
-        const int r = x / C, c = x - r * C;
-        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (r0 + r < end) f = __ldg(reinterpret_cast<const float4 *>(src + (size_t)(r0 + r) * row_stride) + c);
-        *reinterpret_cast<float4 *>(dst + r * WinF32<D>::LD + c * 4) = f;
+    constexpr int C = D / 4, PER = (N * C + 255) / 256;
+    float4 f[PER];
+#pragma unroll
+    for (int y = 0; y < PER; ++y) {
+        const int x = threadIdx.x + 256 * y, r = x / C, c = x - r * C;
+        f[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (x < N * C && r0 + r < end) f[y] = __ldg(reinterpret_cast<const float4 *>(src + (size_t)(r0 + r) * row_stride) + c);
+    }
+#pragma unroll
+    for (int y = 0; y < PER; ++y) {
+        const int x = threadIdx.x + 256 * y, r = x / C, c = x - r * C;
+        if (x < N * C) *reinterpret_cast<float4 *>(dst + r * (D + 4) + c * 4) = f[y];
     }
 }
 
-// acc[i][j] += <a[row ty*4 + i], b[row tx + 16 j]>
-template <int D> __device__ __forceinline__ void tile_dots(const float *a, const float *b, int ty, int tx, float (&acc)[4][4])
+__device__ __forceinline__ float2 lower(const float4 &f) { return make_float2(f.x, f.y); }
+__device__ __forceinline__ float2 upper(const float4 &f) { return make_float2(f.z, f.w); }
+
+// acc[i][j] = <a[row ty*R + i], b[row tx + 16 j]>; even and odd elements sum apart, then together.
+template <int D, int R>
+__device__ __forceinline__ void tile_dots(const float *a, const float *b, int ty, int tx, float (&acc)[R][4])
 {
-    constexpr int LD = WinF32<D>::LD;
+    constexpr int LD = D + 4;
+    float2 s[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-        float4 x[4], y[4];
+        float4 x[R], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (ty * 4 + i) * LD + d);
+        for (int i = 0; i < R; ++i) x[i] = *reinterpret_cast<const float4 *>(a + (ty * R + i) * LD + d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(b + (tx + 16 * j) * LD + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] += x[i].x * y[j].x + x[i].y * y[j].y + x[i].z * y[j].z + x[i].w * y[j].w;
-    }
-}
-
-// acc[i][c] += sum_r w(ty*4 + i, r) f[r][tx*4 + 64 c ..+3], the weights stored [row][r]
-// (ROWS) or transposed, [r][row].
-template <int D, bool ROWS>
-__device__ __forceinline__ void tile_accumulate(const float *w, const float *f, int ty, int tx,
-                                                float4 (&acc)[4][WinF32<D>::NC])
-{
-    constexpr int LD = WinF32<D>::LD, NC = WinF32<D>::NC;
-#pragma unroll 4
-    for (int r = 0; r < WT; ++r) {
-        float p[4];
-        if (ROWS) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = w[(ty * 4 + i) * WLP + r];
-        } else {
-            const float4 t = *reinterpret_cast<const float4 *>(w + r * WLP + ty * 4);
-            p[0] = t.x, p[1] = t.y, p[2] = t.z, p[3] = t.w;
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float4 y = *reinterpret_cast<const float4 *>(f + r * LD + tx * 4 + 64 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i][c].x += p[i] * y.x;
-                acc[i][c].y += p[i] * y.y;
-                acc[i][c].z += p[i] * y.z;
-                acc[i][c].w += p[i] * y.w;
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = __ffma2_rn(lower(x[i]), lower(y[j]), s[i][j]);
+                s[i][j] = __ffma2_rn(upper(x[i]), upper(y[j]), s[i][j]);
             }
-        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = s[i][j].x + s[i][j].y;
+}
+
+// acc[i][c] += sum_r w[row ty*R + i][r] f[r][tx*4 + 64 c ..+3]
+template <int D, int R>
+__device__ __forceinline__ void tile_accumulate(const float *w, const float *f, int ty, int tx, float4 (&acc)[R][D / 64])
+{
+    constexpr int LD = D + 4, NC = D / 64;
+#pragma unroll 2
+    for (int r = 0; r < WT; r += 4) {
+        float4 p[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) p[i] = *reinterpret_cast<const float4 *>(w + (ty * R + i) * WLP + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const float4 y = *reinterpret_cast<const float4 *>(f + (r + e) * LD + tx * 4 + 64 * c);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float pe = (&p[i].x)[e];
+                    const float2 lo = __ffma2_rn(make_float2(pe, pe), lower(y), lower(acc[i][c]));
+                    const float2 hi = __ffma2_rn(make_float2(pe, pe), upper(y), upper(acc[i][c]));
+                    acc[i][c] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
     }
 }
 
-template <int NC> __device__ __forceinline__ void zero(float4 (&acc)[4][NC])
+template <int R, int NC> __device__ __forceinline__ void zero(float4 (&acc)[R][NC])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[i][c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
@@ -175,43 +196,58 @@ __device__ __forceinline__ float row_max(float x)
     return x;
 }
 
-template <int D> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinArgs a)
+// This thread's rows of an output tile, times f; rows at or past n are not written.
+template <int D, int R>
+__device__ __forceinline__ void store_tile(float *dst, size_t row_stride, int r0, int n, int ty, int tx,
+                                           const float4 (&acc)[R][D / 64], const float (&f)[R])
 {
-    using S = WinF32<D>;
-    constexpr int NC = S::NC;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (r0 + ty * R + i < n) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+                *reinterpret_cast<float4 *>(dst + (size_t)(r0 + ty * R + i) * row_stride + tx * 4 + 64 * c) =
+                    make_float4(acc[i][c].x * f[i], acc[i][c].y * f[i], acc[i][c].z * f[i], acc[i][c].w * f[i]);
+        }
+}
+
+template <int D, int R> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinArgs a)
+{
+    using S = WinF32<D, R>;
+    constexpr int NC = S::NC, ROWS = S::ROWS;
     extern __shared__ __align__(16) float wsm[];
-    float *sq = wsm, *sk = sq + WT * S::LD, *sv = sk + WT * S::LD, *sp = sv + WT * S::LD;
+    float *sq = wsm, *sk = sq + ROWS * S::LD, *sv = sk + WT * S::LD, *sp = sv + WT * S::LD;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     // the blocks with the longest prefix first
     const int per = a.B * a.hq;
     const int blk = a.nblk - 1 - (int)(blockIdx.x / (unsigned)per);
     const int bh = (int)(blockIdx.x % (unsigned)per);
     const int b = bh / a.hq, hq = bh - b * a.hq, h = hq / a.G;
-    const int len = win_len(a, b), i0 = blk * WT;
+    const int len = win_len(a, b), i0 = blk * ROWS;
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
     const float *q = (const float *)a.q + (size_t)b * a.n * qs + (size_t)hq * D;
     const float *k = (const float *)a.k + (size_t)b * a.n * ks + (size_t)h * D;
     const float *v = (const float *)a.v + (size_t)b * a.n * ks + (size_t)h * D;
-    const KeyBlocks kb(i0, WT, len, a.window, a.sinks, WT);
+    const KeyBlocks kb(i0, ROWS, len, a.window, a.sinks, WT);
     const float sl2 = a.scale * LOG2E;
 
-    load_tile<D>(sq, q, qs, i0, len);
-    float4 acc[4][NC];
+    load_tile<D, ROWS>(sq, q, qs, i0, len);
+    float4 acc[R][NC];
     zero(acc);
-    float m[4], l[4];
+    float m[R], l[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.0f;
+    for (int i = 0; i < R; ++i) m[i] = -INFINITY, l[i] = 0.0f;
     for (int j = 0; j < kb.na + kb.nb; ++j) {
         const int t0 = kb.start(j, WT), t1 = kb.end(j, WT);
         __syncthreads();
-        load_tile<D>(sk, k, ks, t0, t1);
-        load_tile<D>(sv, v, ks, t0, t1);
+        load_tile<D, WT>(sk, k, ks, t0, t1);
+        load_tile<D, WT>(sv, v, ks, t0, t1);
         __syncthreads();
-        float s[4][4] = {};
-        tile_dots<D>(sq, sk, ty, tx, s);
+        float s[R][4];
+        tile_dots<D, R>(sq, sk, ty, tx, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int qi = i0 + ty * 4 + i;
+        for (int i = 0; i < R; ++i) {
+            const int qi = i0 + ty * R + i;
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -228,7 +264,7 @@ template <int D> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinAr
             for (int c = 0; c < 4; ++c) {
                 const float p = exp2f(s[i][c] - base);
                 sum += p;
-                sp[(ty * 4 + i) * WLP + tx + 16 * c] = p;
+                sp[(ty * R + i) * WLP + tx + 16 * c] = p;
             }
             l[i] = l[i] * f + sum;
             m[i] = mn;
@@ -241,22 +277,18 @@ template <int D> __global__ void __launch_bounds__(256) win_fwd_f32_kernel(WinAr
             }
         }
         __syncwarp();  // a score row belongs to one half of a warp
-        tile_accumulate<D, true>(sp, sv, ty, tx, acc);
+        tile_accumulate<D, R>(sp, sv, ty, tx, acc);
     }
-    float *o = (float *)a.o + (size_t)b * a.n * qs + (size_t)hq * D;
+    float inv[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int qi = i0 + ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int qi = i0 + ty * R + i;
         const float sum = row_sum(l[i]);
-        if (qi >= a.n) continue;
-        const float inv = qi < len ? 1.0f / sum : 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            *reinterpret_cast<float4 *>(o + (size_t)qi * qs + tx * 4 + 64 * c) =
-                make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv, acc[i][c].w * inv);
-        if (a.lse && tx == 0)
+        inv[i] = qi < len ? 1.0f / sum : 0.0f;
+        if (a.lse && tx == 0 && qi < a.n)
             a.lse[((size_t)b * a.n + qi) * a.hq + hq] = qi < len ? m[i] * LN2 + logf(sum) : -INFINITY;
     }
+    store_tile<D, R>((float *)a.o + (size_t)b * a.n * qs + (size_t)hq * D, qs, i0, a.n, ty, tx, acc, inv);
 }
 
 // delta[b, hq, i] = <dout[b, i, hq], o[b, i, hq]>; one warp per row.
@@ -282,103 +314,77 @@ template <int D> __global__ void __launch_bounds__(256) win_delta_kernel(WinArgs
     }
 }
 
-// P and dS of one 64 x 64 tile (queries i0 + ty*4 + i, keys t0 + tx + 16 c), written to sp / sd.
-template <int D, bool WANT_P>
-__device__ __forceinline__ void bwd_scores(const WinArgs &a, const float *sq, const float *sk, const float *sdo,
-                                           const float *sv, float *sp, float *sd, int i0, int len, int t0, int t1,
-                                           const float (&nl)[4], const float (&dl)[4], int ty, int tx)
+template <int D, int R> __global__ void __launch_bounds__(256) win_dq_f32_kernel(WinArgs a)
 {
-    float s[4][4] = {}, dp[4][4] = {};
-    tile_dots<D>(sq, sk, ty, tx, s);
-    tile_dots<D>(sdo, sv, ty, tx, dp);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int qi = i0 + ty * 4 + i;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int t = t0 + tx + 16 * c;
-            const bool see = qi < len && t < t1 && win_sees(qi, t, a.window, a.sinks);
-            const float p = see ? exp2f(fmaf(s[i][c], a.scale * LOG2E, nl[i])) : 0.0f;
-            if (WANT_P) sp[(ty * 4 + i) * WLP + tx + 16 * c] = p;
-            sd[(ty * 4 + i) * WLP + tx + 16 * c] = see ? p * (dp[i][c] - dl[i]) : 0.0f;
-        }
-    }
-}
-
-// -log2(e) lse and delta of the thread's four query rows (0 past the sequence's end).
-__device__ __forceinline__ void row_stats(const WinArgs &a, int b, int hq, int i0, int len, int ty, float (&nl)[4], float (&dl)[4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int qi = i0 + ty * 4 + i;
-        const bool in = qi < len;
-        nl[i] = in ? -LOG2E * __ldg(a.lse_in + ((size_t)b * a.n + qi) * a.hq + hq) : 0.0f;
-        dl[i] = in ? a.delta[((size_t)b * a.hq + hq) * a.n + qi] : 0.0f;
-    }
-}
-
-template <int D> __global__ void __launch_bounds__(256) win_dq_f32_kernel(WinArgs a)
-{
-    using S = WinF32<D>;
-    constexpr int NC = S::NC;
+    using S = WinF32<D, R>;
+    constexpr int NC = S::NC, ROWS = S::ROWS;
     extern __shared__ __align__(16) float wsm[];
-    float *sq = wsm, *sdo = sq + WT * S::LD, *sk = sdo + WT * S::LD, *sv = sk + WT * S::LD, *sd = sv + WT * S::LD;
+    float *sq = wsm, *sdo = sq + ROWS * S::LD, *sk = sdo + ROWS * S::LD, *sv = sk + WT * S::LD, *sd = sv + WT * S::LD;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int per = a.B * a.hq;
     const int blk = a.nblk - 1 - (int)(blockIdx.x / (unsigned)per);
     const int bh = (int)(blockIdx.x % (unsigned)per);
     const int b = bh / a.hq, hq = bh - b * a.hq, h = hq / a.G;
-    const int len = win_len(a, b), i0 = blk * WT;
+    const int len = win_len(a, b), i0 = blk * ROWS;
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
     const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D, ko = (size_t)b * a.n * ks + (size_t)h * D;
-    const KeyBlocks kb(i0, WT, len, a.window, a.sinks, WT);
-    load_tile<D>(sq, (const float *)a.q + qo, qs, i0, len);
-    load_tile<D>(sdo, (const float *)a.dout + qo, qs, i0, len);
-    float nl[4], dl[4];
-    row_stats(a, b, hq, i0, len, ty, nl, dl);
-    float4 acc[4][NC];
+    const KeyBlocks kb(i0, ROWS, len, a.window, a.sinks, WT);
+    load_tile<D, ROWS>(sq, (const float *)a.q + qo, qs, i0, len);
+    load_tile<D, ROWS>(sdo, (const float *)a.dout + qo, qs, i0, len);
+    float nl[R], dl[R], scale[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int qi = i0 + ty * R + i;
+        nl[i] = qi < len ? -LOG2E * __ldg(a.lse_in + ((size_t)b * a.n + qi) * a.hq + hq) : 0.0f;
+        dl[i] = qi < len ? a.delta[((size_t)b * a.hq + hq) * a.n + qi] : 0.0f;
+        scale[i] = a.scale;
+    }
+    float4 acc[R][NC];
     zero(acc);
     for (int j = 0; j < kb.na + kb.nb; ++j) {
         const int t0 = kb.start(j, WT), t1 = kb.end(j, WT);
         __syncthreads();
-        load_tile<D>(sk, (const float *)a.k + ko, ks, t0, t1);
-        load_tile<D>(sv, (const float *)a.v + ko, ks, t0, t1);
+        load_tile<D, WT>(sk, (const float *)a.k + ko, ks, t0, t1);
+        load_tile<D, WT>(sv, (const float *)a.v + ko, ks, t0, t1);
         __syncthreads();
-        bwd_scores<D, false>(a, sq, sk, sdo, sv, nullptr, sd, i0, len, t0, t1, nl, dl, ty, tx);
+        float s[R][4], dp[R][4];
+        tile_dots<D, R>(sq, sk, ty, tx, s);
+        tile_dots<D, R>(sdo, sv, ty, tx, dp);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int qi = i0 + ty * R + i;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int t = t0 + tx + 16 * c;
+                const bool see = qi < len && t < t1 && win_sees(qi, t, a.window, a.sinks);
+                const float p = exp2f(fmaf(s[i][c], a.scale * LOG2E, nl[i]));
+                sd[(ty * R + i) * WLP + tx + 16 * c] = see ? p * (dp[i][c] - dl[i]) : 0.0f;
+            }
+        }
         __syncwarp();
-        tile_accumulate<D, true>(sd, sk, ty, tx, acc);
+        tile_accumulate<D, R>(sd, sk, ty, tx, acc);
     }
-    float *dq = (float *)a.dq + qo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int qi = i0 + ty * 4 + i;
-        if (qi >= a.n) continue;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            *reinterpret_cast<float4 *>(dq + (size_t)qi * qs + tx * 4 + 64 * c) =
-                make_float4(
-                acc[i][c].x * a.scale, acc[i][c].y * a.scale, acc[i][c].z * a.scale, acc[i][c].w * a.scale);
-    }
+    store_tile<D, R>((float *)a.dq + qo, qs, i0, a.n, ty, tx, acc, scale);
 }
 
-template <int D> __global__ void __launch_bounds__(256) win_dkv_f32_kernel(WinArgs a)
+template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_f32_kernel(WinArgs a)
 {
-    using S = WinF32<D>;
-    constexpr int NC = S::NC;
+    using S = WinF32<D, R>;
+    constexpr int NC = S::NC, ROWS = S::ROWS;
     extern __shared__ __align__(16) float wsm[];
-    float *sk = wsm, *sv = sk + WT * S::LD, *sq = sv + WT * S::LD, *sdo = sq + WT * S::LD;
-    float *sp = sdo + WT * S::LD, *sd = sp + WT * WLP;
+    float *sk = wsm, *sv = sk + ROWS * S::LD, *sq = sv + ROWS * S::LD, *sdo = sq + WT * S::LD;
+    float *sp = sdo + WT * S::LD, *sd = sp + ROWS * WLP;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int per = a.B * a.hkv;
     const int blk = (int)(blockIdx.x / (unsigned)per);  // the keys that most queries see first
     const int bh = (int)(blockIdx.x % (unsigned)per);
     const int b = bh / a.hkv, h = bh - b * a.hkv;
-    const int len = win_len(a, b), t0 = blk * WT, t1 = min(t0 + WT, len);
+    const int len = win_len(a, b), t0 = blk * ROWS, t1 = min(t0 + ROWS, len);
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
     const size_t ko = (size_t)b * a.n * ks + (size_t)h * D;
-    load_tile<D>(sk, (const float *)a.k + ko, ks, t0, len);
-    load_tile<D>(sv, (const float *)a.v + ko, ks, t0, len);
-    float4 gk[4][NC], gv[4][NC];
+    load_tile<D, ROWS>(sk, (const float *)a.k + ko, ks, t0, len);
+    load_tile<D, ROWS>(sv, (const float *)a.v + ko, ks, t0, len);
+    float4 gk[R][NC], gv[R][NC];
     zero(gk);
     zero(gv);
     const int qend = t1 > t0 ? query_end(t0, t1, len, a.window, a.sinks) : t0;
@@ -387,30 +393,41 @@ template <int D> __global__ void __launch_bounds__(256) win_dkv_f32_kernel(WinAr
         const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D;
         for (int i0 = t0; i0 < qend; i0 += WT) {
             __syncthreads();
-            load_tile<D>(sq, (const float *)a.q + qo, qs, i0, len);
-            load_tile<D>(sdo, (const float *)a.dout + qo, qs, i0, len);
-            float nl[4], dl[4];
-            row_stats(a, b, hq, i0, len, ty, nl, dl);
+            load_tile<D, WT>(sq, (const float *)a.q + qo, qs, i0, len);
+            load_tile<D, WT>(sdo, (const float *)a.dout + qo, qs, i0, len);
+            float nl[4], dl[4];  // of queries i0 + tx + 16 c
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int qi = i0 + tx + 16 * c;
+                nl[c] = qi < len ? -LOG2E * __ldg(a.lse_in + ((size_t)b * a.n + qi) * a.hq + hq) : 0.0f;
+                dl[c] = qi < len ? a.delta[((size_t)b * a.hq + hq) * a.n + qi] : 0.0f;
+            }
             __syncthreads();
-            bwd_scores<D, true>(a, sq, sk, sdo, sv, sp, sd, i0, len, t0, t1, nl, dl, ty, tx);
-            __syncthreads();
-            tile_accumulate<D, false>(sp, sdo, ty, tx, gv);
-            tile_accumulate<D, false>(sd, sq, ty, tx, gk);
+            float s[R][4], dp[R][4];
+            tile_dots<D, R>(sk, sq, ty, tx, s);
+            tile_dots<D, R>(sv, sdo, ty, tx, dp);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int t = t0 + ty * R + i;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int qi = i0 + tx + 16 * c;
+                    const bool see = qi < len && t < len && win_sees(qi, t, a.window, a.sinks);
+                    const float p = see ? exp2f(fmaf(s[i][c], a.scale * LOG2E, nl[c])) : 0.0f;
+                    sp[(ty * R + i) * WLP + tx + 16 * c] = p;
+                    sd[(ty * R + i) * WLP + tx + 16 * c] = see ? p * (dp[i][c] - dl[c]) : 0.0f;
+                }
+            }
+            __syncwarp();
+            tile_accumulate<D, R>(sp, sdo, ty, tx, gv);
+            tile_accumulate<D, R>(sd, sq, ty, tx, gk);
         }
     }
-    float *dk = (float *)a.dk + ko, *dv = (float *)a.dv + ko;
+    float scale[R], one[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = t0 + ty * 4 + i;
-        if (t >= a.n) continue;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            *reinterpret_cast<float4 *>(dk + (size_t)t * ks + tx * 4 + 64 * c) =
-                make_float4(
-                gk[i][c].x * a.scale, gk[i][c].y * a.scale, gk[i][c].z * a.scale, gk[i][c].w * a.scale);
-            *reinterpret_cast<float4 *>(dv + (size_t)t * ks + tx * 4 + 64 * c) = gv[i][c];
-        }
-    }
+    for (int i = 0; i < R; ++i) scale[i] = a.scale, one[i] = 1.0f;
+    store_tile<D, R>((float *)a.dk + ko, ks, t0, a.n, ty, tx, gk, scale);
+    store_tile<D, R>((float *)a.dv + ko, ks, t0, a.n, ty, tx, gv, one);
 }
 
 }  // namespace gm

@@ -627,9 +627,9 @@ def gm_dense_refresh_edges(q, k, lse, sf: int, scale=None, out_idx=None, out_w=N
 
 def _on(dev, stream):
     """Context in which `dev` is current and torch's current stream is the call's: outputs then
-    belong to the stream that writes them."""
+    belong to the stream that writes them. None if that is so already."""
     if stream is None:
-        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     if stream.device != dev:
@@ -637,15 +637,24 @@ def _on(dev, stream):
     return torch.cuda.stream(stream)
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
+def _current_stream(dev) -> int:
+    """torch's current stream of a device as a handle (the Stream object alone takes 3 us)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _arg(t, shape, dtype, dev, name):
     """Pointer of a contiguous tensor of this shape, type and device."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
+    if t.get_device() != dev.index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -667,10 +676,12 @@ def _window(window, sinks):
     return min(window, 2**31 - 1), min(int(sinks), 2**31 - 1)
 
 
-def _out(t, shape, dtype, dev, name):
+def _out(t, like, shape, dtype, dev, name):
     """An output: the caller's tensor, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty_like(like) if like.dtype is dtype and like.shape == shape \
+            else like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
     return t, _arg(t, shape, dtype, dev, name)
 
 
@@ -684,13 +695,13 @@ def gm_window_attention_forward(q, k, v, window=None, sinks: int = 0, lens=None,
     B, n, hq, _ = q.shape
     dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
     window, sinks = _window(window, sinks)
-    with _on(dev, stream):
-        o, po = _out(o, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream) or _HERE_AND_NOW:
+        o, po = _out(o, q, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
         st = load_library().gm_window_attention_forward(
             _arg(q, q.shape, dt, dev, "q"), _arg(k, kv, dt, dev, "k"), _arg(v, kv, dt, dev, "v"), _fdtype(q),
             None if lens is None else _arg(lens, (B,), torch.int32, dev, "lens"), B, n, hq, hkv, d, window, sinks,
-            _scale(scale, d), po, pl, torch.cuda.current_stream().cuda_stream)
+            _scale(scale, d), po, pl, _current_stream(dev))
     _check(st, "gm_window_attention_forward")
     return o, lse
 
@@ -714,10 +725,10 @@ def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int 
     dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
     window, sinks = _window(window, sinks)
     lib = load_library()
-    with _on(dev, stream):
-        dq, pdq = _out(dq, q.shape, dt, dev, "dq")
-        dk, pdk = _out(dk, kv, dt, dev, "dk")
-        dv, pdv = _out(dv, kv, dt, dev, "dv")
+    with _on(dev, stream) or _HERE_AND_NOW:
+        dq, pdq = _out(dq, q, q.shape, dt, dev, "dq")
+        dk, pdk = _out(dk, k, kv, dt, dev, "dk")
+        dv, pdv = _out(dv, v, kv, dt, dev, "dv")
         if workspace is None:
             workspace = torch.empty(
                 lib.gm_window_attention_backward_workspace_size(_fdtype(q), B, n, hq, hkv, d, window, sinks),
@@ -728,7 +739,7 @@ def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int 
             _arg(lse, q.shape[:3], torch.float32, dev, "lse"), _fdtype(q),
             None if lens is None else _arg(lens, (B,), torch.int32, dev, "lens"), B, n, hq, hkv, d, window, sinks,
             _scale(scale, d), pdq, pdk, pdv, _arg(workspace, workspace.shape, torch.uint8, dev, "workspace"),
-            workspace.numel(), torch.cuda.current_stream().cuda_stream)
+            workspace.numel(), _current_stream(dev))
     _check(st, "gm_window_attention_backward")
     return dq, dk, dv
 
@@ -760,11 +771,11 @@ def gm_kv8_append(k, v, kq, vq, kscale, vscale, table, lens, new_lens=None, stre
     if kq.dim() != 4 or kq.shape[1] != hkv:
         raise ValueError(f"kq must be [num_pages, {hkv}, page, {d}]")
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
-    with _on(dev, stream):
+    with _on(dev, stream) or _HERE_AND_NOW:
         st = load_library().gm_kv8_append(
             _arg(k, k.shape, k.dtype, dev, "k"), _arg(v, k.shape, k.dtype, dev, "v"), _fdtype(k), B, t, hkv, d, *cache,
             None if new_lens is None else _arg(new_lens, (B,), torch.int32, dev, "new_lens"),
-            torch.cuda.current_stream().cuda_stream)
+            _current_stream(dev))
     _check(st, "gm_kv8_append")
 
 
@@ -787,9 +798,9 @@ def gm_kv8_attention_forward(q, kq, vq, kscale, vscale, table, lens, window=None
     window, sinks = _window(window, sinks)
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
     lib = load_library()
-    with _on(dev, stream):
-        o, po = _out(o, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream) or _HERE_AND_NOW:
+        o, po = _out(o, q, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
         if workspace is None:
             need = lib.gm_kv8_attention_workspace_size(B, t, hq, hkv, d, kq.shape[2], table.shape[1], window, sinks)
             workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -798,7 +809,7 @@ def gm_kv8_attention_forward(q, kq, vq, kscale, vscale, table, lens, window=None
         st = lib.gm_kv8_attention_forward(
             _arg(q, q.shape, dt, dev, "q"), _fdtype(q), B, t, hq, hkv, d, *cache,
             None if q_lens is None else _arg(q_lens, (B,), torch.int32, dev, "q_lens"), window, sinks,
-            _scale(scale, d), po, pl, ws, size, torch.cuda.current_stream().cuda_stream)
+            _scale(scale, d), po, pl, ws, size, _current_stream(dev))
     _check(st, "gm_kv8_attention_forward")
     return o, lse
 
@@ -813,14 +824,14 @@ def gm_kv8_sea_forward(q, idx, w, kq, vq, kscale, vscale, table, lens, q_lens=No
     dt, s = q.dtype, idx.shape[-1]
     edges = torch.Size((B, t, hkv, s))
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
-    with _on(dev, stream):
-        o, po = _out(o, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream) or _HERE_AND_NOW:
+        o, po = _out(o, q, q.shape, dt, dev, "o")
+        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
         st = load_library().gm_kv8_sea_forward(
             _arg(q, q.shape, dt, dev, "q"), _fdtype(q), _arg(idx, edges, torch.int32, dev, "idx"),
             _arg(w, edges, torch.float32, dev, "w"), s, B, t, hq, hkv, d, *cache,
             None if q_lens is None else _arg(q_lens, (B,), torch.int32, dev, "q_lens"), _scale(scale, d), po, pl,
-            torch.cuda.current_stream().cuda_stream)
+            _current_stream(dev))
     _check(st, "gm_kv8_sea_forward")
     return o, lse
 

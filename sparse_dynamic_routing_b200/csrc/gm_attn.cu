@@ -2,6 +2,7 @@
 // argument checks, choice of the kernel, launch on the caller's stream. A translation unit of
 // its own so that it compiles beside gm_api.cu.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -26,9 +27,18 @@ bool gm_attn_take_errors(unsigned *flag)
 
 namespace {
 
-template <typename F> bool raise_smem(F kern, size_t bytes)
+// Lets a kernel have `bytes` of dynamic shared memory on the current device; asked of the runtime
+// once per kernel and device.
+template <auto KERNEL> bool raise_smem(size_t bytes)
 {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // ---- windowed attention -------------------------------------------------------------------------
@@ -69,8 +79,8 @@ int f32_rows(int n, int64_t heads)
 template <int D, int R> gm_status window_forward_f32(gm::WinArgs a, cudaStream_t st)
 {
     using S = gm::WinF32<D, R>;
-    auto kern = gm::win_fwd_f32_kernel<D, R>;
-    if (!raise_smem(kern, S::fwd_smem)) return GM_ERR_CUDA;
+    constexpr auto kern = gm::win_fwd_f32_kernel<D, R>;
+    if (!raise_smem<kern>(S::fwd_smem)) return GM_ERR_CUDA;
     a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
     kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, S::fwd_smem, st>>>(a);
     return launched();
@@ -85,8 +95,8 @@ template <int D> gm_status window_forward(const gm::WinArgs &a, cudaStream_t st)
 template <int D, int R> gm_status window_dq_f32(gm::WinArgs a, cudaStream_t st)
 {
     using S = gm::WinF32<D, R>;
-    auto kern = gm::win_dq_f32_kernel<D, R>;
-    if (!raise_smem(kern, S::dq_smem)) return GM_ERR_CUDA;
+    constexpr auto kern = gm::win_dq_f32_kernel<D, R>;
+    if (!raise_smem<kern>(S::dq_smem)) return GM_ERR_CUDA;
     a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
     kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hq), 256, S::dq_smem, st>>>(a);
     return launched();
@@ -95,8 +105,8 @@ template <int D, int R> gm_status window_dq_f32(gm::WinArgs a, cudaStream_t st)
 template <int D, int R> gm_status window_dkv_f32(gm::WinArgs a, cudaStream_t st)
 {
     using S = gm::WinF32<D, R>;
-    auto kern = gm::win_dkv_f32_kernel<D, R>;
-    if (!raise_smem(kern, S::dkv_smem)) return GM_ERR_CUDA;
+    constexpr auto kern = gm::win_dkv_f32_kernel<D, R>;
+    if (!raise_smem<kern>(S::dkv_smem)) return GM_ERR_CUDA;
     a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
     kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, S::dkv_smem, st>>>(a);
     return launched();
@@ -155,8 +165,8 @@ template <int D> gm_status window_forward_bf16(gm::WinArgs a, cudaStream_t st)
     if (!sequence_tmap(tq, a.q, a.B, a.n, a.hq, D) || !sequence_tmap(tk, a.k, a.B, a.n, a.hkv, D, gm::FK) ||
         !sequence_tmap(tv, a.v, a.B, a.n, a.hkv, D, gm::FK) || !sequence_tmap(to, a.o, a.B, a.n, a.hq, D))
         return GM_ERR_CUDA;
-    auto kern = gm::win_fwd_umma_kernel<D>;
-    if (!raise_smem(kern, Geo::SMEM)) return GM_ERR_CUDA;
+    constexpr auto kern = gm::win_fwd_umma_kernel<D>;
+    if (!raise_smem<kern>(Geo::SMEM)) return GM_ERR_CUDA;
     gm::WinPairs wp;
     wp.items = window_pairs(a, wp);
     a.scale = base2_scale(a.scale);
@@ -213,9 +223,9 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
     if (!sequence_tmap(tq, w.q, w.B, w.n, w.hq, D) || !sequence_tmap(tdo, w.dout, w.B, w.n, w.hq, D) ||
         !sequence_tmap(tk, w.k, w.B, w.n, w.hkv, D) || !sequence_tmap(tv, w.v, w.B, w.n, w.hkv, D))
         return GM_ERR_CUDA;
-    auto kq = gm::win_dq_umma_kernel<D>;
-    auto kkv = gm::win_dkv_umma_kernel<D>;
-    if (!raise_smem(kq, Geo::SMEM) || !raise_smem(kkv, Geo::SMEM)) return GM_ERR_CUDA;
+    constexpr auto kq = gm::win_dq_umma_kernel<D>;
+    constexpr auto kkv = gm::win_dkv_umma_kernel<D>;
+    if (!raise_smem<kq>(Geo::SMEM) || !raise_smem<kkv>(Geo::SMEM)) return GM_ERR_CUDA;
     const WinBwdPlan p = window_backward_plan(w.B, w.n, w.hq, w.hkv, D, w.window, w.sinks);
     gm::WinBwdArgs a{};
     a.w = w;
@@ -334,8 +344,8 @@ int64_t kv8_keys(int64_t room, int window, int sinks, int t)
 template <typename T, int D, int NT> gm_status launch_kv8_attention(const gm::Kv8AttnArgs &a, int B, int64_t items, cudaStream_t st)
 {
     using Smem = gm::Kv8Smem<D, NT, sizeof(T) == 4>;
-    auto kern = gm::kv8_attention_kernel<T, D, NT>;
-    if (!raise_smem(kern, sizeof(Smem))) return GM_ERR_CUDA;
+    constexpr auto kern = gm::kv8_attention_kernel<T, D, NT>;
+    if (!raise_smem<kern>(sizeof(Smem))) return GM_ERR_CUDA;
     kern<<<(unsigned)(items * a.splits), gm::KV8_W * 32, sizeof(Smem), st>>>(a);
     if (a.splits > 1) {
         cudaLaunchConfig_t cfg = {};
@@ -360,8 +370,8 @@ template <typename T, int D> gm_status kv8_attention(const gm::Kv8AttnArgs &a, i
 template <typename T, int D, int NP> gm_status launch_kv8_sea(const gm::Kv8SeaArgs &a, cudaStream_t st)
 {
     constexpr int smem = 4 * (int)sizeof(gm::Kv8SeaSmem<T, D, NP>);
-    auto kern = gm::kv8_sea_kernel<T, D, NP>;
-    if (!raise_smem(kern, smem)) return GM_ERR_CUDA;
+    constexpr auto kern = gm::kv8_sea_kernel<T, D, NP>;
+    if (!raise_smem<kern>(smem)) return GM_ERR_CUDA;
     // as many warps as the GPU holds at once, each taking step after step
     const int per_sm = std::max(1, std::min(4, (227 * 1024) / (smem + 1024)));
     const int64_t steps = a.tiles * ((a.G + 7) / 8);

@@ -519,12 +519,15 @@ gm_status gm_dense_refresh_edges(const void *q, const void *k, gm_dtype dtype, c
  * lse[b,i,hq] = ln sum_t exp(z_t). Rows at or past lens[b] give o = 0 and lse = -inf.
  *
  *   q, k, v   device, `dtype`, [B, n, hq | hkv, d], 16-byte aligned. Rows at or past lens[b] are
- *             not used and may hold anything, also infinities and NaN
+ *             not used and may hold anything, also infinities and NaN. The others are expected
+ *             finite: an infinity or NaN in one may show in any row of its sequence, also in
+ *             rows that do not see it (its weight there is 0, and 0 times NaN is NaN)
  *   lens      device int32 [B]: tokens of each sequence, taken as 0..n; NULL: n each
  *   window    >= 1 (n or more: every earlier token is visible)
  *   sinks     >= 0 first tokens that stay visible outside the window
  *   o         device, `dtype`, [B, n, hq, d], 16-byte aligned, written in full
- *   lse       device fp32 [B, n, hq], written in full; may be NULL
+ *   lse       device fp32 [B, n, hq], written in full; may be NULL. Outputs must not overlap the
+ *             inputs or one another (here and below)
  *   limits    d in {64, 128}; any hq / hkv; n < 2^30, B * n * hq < 2^31
  * Scores, softmax statistics and sums are fp32; for GM_BF16 the probabilities are rounded to
  * bf16 before they meet v. Deterministic.
@@ -584,7 +587,7 @@ size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n,
  *   lens        device int32 [B]: tokens that each sequence holds before the call
  *   new_lens    device int32 [B]: rows of k and v that belong to the sequence, taken as 0..t;
  *               NULL: t each
- *   page        16, 32, 64 or 128 tokens; limits: d in {64, 128}
+ *   page        16, 32, 64 or 128 tokens; limits: d in {64, 128}, num_pages * hkv * page < 2^32
  * No two sequences may write the same page in one call (fork a page by copying it first). A
  * page outside [0, num_pages), a negative length, or a token past max_pages * page is not
  * written and raises the device index-range flag (gm_check_device_errors).

@@ -612,7 +612,7 @@ __global__ void wait_timeout_selftest_kernel()
 
 extern "C" {
 
-int gm_version(void) { return 100; }
+int gm_version(void) { return 200; }
 
 gm_status gm_selftest_wait_timeout(cudaStream_t stream)
 {

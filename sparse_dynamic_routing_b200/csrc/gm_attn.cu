@@ -318,14 +318,17 @@ Kv8Plan kv8_plan(int B, int t, int hq, int hkv, int d, int64_t keys)
     // per warp and a start and end worth about four of them. The splits with the least of it.
     const int64_t room = 148 * gm::KV8_PER_SM, units = (keys + 31) / 32;
     const int64_t most = std::min<int64_t>(room, std::max<int64_t>(1, units / (2 * gm::KV8_W)));
+    // Tried: no split, and as many as fill one to eight rounds.
     int64_t best = INT64_MAX;
-    for (int64_t s = 1; s <= most; ++s) {
-        if (s > 1 && p.items * s > 8 * room) break;
+    for (int64_t rounds = 0; rounds <= 8; ++rounds) {
+        const int64_t s = rounds == 0 ? 1 : std::min(most, rounds * room / p.items);
+        if (s < 1) continue;
         const int64_t cost = ((p.items * s + room - 1) / room) * ((units + s * gm::KV8_W - 1) / (s * gm::KV8_W) + 4);
         if (cost < best) {
             best = cost;
             p.splits = (int)s;
         }
+        if (rounds > 0 && s == most) break;
     }
     if (p.splits > 1) {
         const size_t rows = (size_t)p.items * p.splits * 8 * p.nt;

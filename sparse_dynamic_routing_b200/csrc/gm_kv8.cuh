@@ -38,12 +38,61 @@ __device__ __forceinline__ float kv8_scale(uint32_t amax_bits)
     return __uint_as_float((uint32_t)(max(e, KV8_MIN_EXP) + 127) << 23);
 }
 
-// Four fp32 values to four e4m3 bytes, round to nearest even (callers pass at most 448).
+// Two fp32 values to two e4m3 bytes, round to nearest even (callers pass at most 448).
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d)
 {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+    return to_e4m3x2(a, b) | (to_e4m3x2(c, d) << 16);
+}
+
+// Largest magnitude so far and in a 16-byte chunk; NaN once there is one. bf16 goes two at a time.
+__device__ __forceinline__ __nv_bfloat162 chunk_amax(__nv_bfloat162 m, const uint4 &u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[x])));
+    return m;
+}
+__device__ __forceinline__ uint32_t chunk_amax(uint32_t m, const uint4 &u)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) m = max(m, w[x] & 0x7fffffffu);
+    return m;
+}
+// The magnitude's fp32 bits (an infinity or NaN: at least 0x7f800000).
+__device__ __forceinline__ uint32_t amax_bits(__nv_bfloat162 m)
+{
+    return max((uint32_t)__bfloat16_as_ushort(m.x) << 16, (uint32_t)__bfloat16_as_ushort(m.y) << 16) & 0x7fffffffu;
+}
+__device__ __forceinline__ uint32_t amax_bits(uint32_t m) { return m; }
+template <typename T> struct AmaxOf { using type = uint32_t; };
+template <> struct AmaxOf<__nv_bfloat16> { using type = __nv_bfloat162; };
+
+// A chunk's elements times a power of two, as e4m3 bytes. (bf16 products are exact; what they lose
+// below 2^-126 is 0 in e4m3.)
+__device__ __forceinline__ uint2 chunk_e4m3(const uint4 &u, float inv, __nv_bfloat16 *)
+{
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const __nv_bfloat162 f = __float2bfloat162_rn(inv);
+    uint32_t r[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[x]), f);
+        const uint32_t b = *reinterpret_cast<const uint32_t *>(&y);
+        r[x] = to_e4m3x2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    }
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+}
+__device__ __forceinline__ uint32_t chunk_e4m3(const uint4 &u, float inv, float *)
+{
+    return to_e4m3x4(__uint_as_float(u.x) * inv, __uint_as_float(u.y) * inv, __uint_as_float(u.z) * inv,
+                     __uint_as_float(u.w) * inv);
 }
 
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t two)
@@ -99,7 +148,6 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
     // row r of the page is new token first + r - have
     const T *src = (const T *)(kv ? a.v : a.k) + (((size_t)b * a.t + (size_t)(first - have + r0)) * a.hkv + h) * D;
     uint4 u[NCH];
-    uint32_t amax = 0;
     const int nch = (r1 - r0) * C;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -107,14 +155,10 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
         u[i] = make_uint4(0, 0, 0, 0);
         if (ch < nch) u[i] = ld16_stream(src + (size_t)r * a.hkv * D + (ch - r * C) * VEC);
     }
+    typename AmaxOf<T>::type big{};
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        float f[VEC];
-        unpack<T>(u[i], f);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
-    }
-    amax = __reduce_max_sync(FULL, amax);
+    for (int i = 0; i < NCH; ++i) big = chunk_amax(big, u[i]);
+    uint32_t amax = __reduce_max_sync(FULL, amax_bits(big));
     if ((threadIdx.x & 31) == 0) samax[threadIdx.x >> 5] = amax;
     float *scales = kv ? a.c.vscale : a.c.kscale;
     const float old = r0 > 0 ? scales[blk] : 0.0f;
@@ -142,22 +186,16 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
     }
     // the elements of a block whose scale is NaN are 0: no byte of a token is itself a NaN, so a
     // reader's weight of 0 always gives 0
-    const float inv = scale == scale ? 1.0f / scale : 0.0f;
+    const bool whole = scale == scale;
+    const float inv = whole ? 1.0f / scale : 0.0f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int ch = threadIdx.x + 256 * i;
         if (ch < nch) {
-            float f[VEC];
-            unpack<T>(u[i], f);
-            uint32_t w[VEC / 4];
-#pragma unroll
-            for (int e = 0; e < VEC / 4; ++e)
-                w[e] = inv == 0.0f ? 0u : to_e4m3x4(f[4 * e] * inv, f[4 * e + 1] * inv, f[4 * e + 2] * inv, f[4 * e + 3] * inv);
-            uint8_t *p = dst + (size_t)r0 * D + (size_t)ch * VEC;  // rows of a block are contiguous
-            if constexpr (VEC == 8)
-                *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<uint32_t *>(p) = w[0];
+            auto w = chunk_e4m3(u[i], inv, (T *)nullptr);
+            if (!whole) w = decltype(w){};
+            // rows of a block are contiguous
+            *reinterpret_cast<decltype(w) *>(dst + (size_t)r0 * D + (size_t)ch * VEC) = w;
         }
     }
 }

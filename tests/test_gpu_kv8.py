@@ -376,6 +376,73 @@ def test_decode_step_captured_and_replayed():
     gm.gm_check_device_errors()
 
 
+def test_pool_past_32_bit_offsets():
+    """Pages whose bytes lie beyond 4 GiB give what the same pages give in a small pool."""
+    page, hkv, d = 64, 8, 128
+    pages = 70000  # x 64 KiB
+    small = make_cache(31, [200, 65], 4, hkv, page, d, stale=None)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(2, 1, 16, d, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(2, 3, hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    idx = torch.tensor([199, 3, 64, 130], dtype=torch.int32).expand(2, 1, hkv, 4).contiguous()
+    idx[1] = torch.tensor([0, 64, 63, 7], dtype=torch.int32)
+    w = torch.rand(2, 1, hkv, 4, generator=g).cuda()
+    a = to_gpu(small)
+    b = {x: torch.empty((pages, *a[x].shape[1:]), dtype=a[x].dtype, device="cuda") for x in ("kq", "vq", "ks", "vs")}
+    far = (pages - 1 - torch.arange(a["kq"].shape[0], device="cuda") * 37).long()
+    for x in ("kq", "vq"):
+        b[x].view(torch.uint8)[far] = a[x].view(torch.uint8)
+    for x in ("ks", "vs"):
+        b[x][far] = a[x]
+    b["table"], b["lens"] = far[a["table"].long()].to(torch.int32), a["lens"].clone()
+    out = []
+    for c in (a, b):
+        gm.gm_kv8_append(k, v, *args(c))
+        c["lens"] += 3
+        out.append((*gm.gm_kv8_attention_forward(q, *args(c)), *gm.gm_kv8_sea_forward(q, idx.cuda(), w, *args(c))))
+    gm.gm_check_device_errors()
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
+    assert same_bytes(a["kq"], b["kq"].view(torch.uint8)[far].view(R.F8))
+
+
+def test_given_outputs_and_workspace():
+    c = to_gpu(make_cache(14, [5000, 333], 90, 2, 64, 64))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(2, 1, 4, 64, generator=g, device="cuda").bfloat16()
+    want = gm.gm_kv8_attention_forward(q, *args(c), None, 0)
+    need = gm.gm_kv8_attention_workspace_size(2, 1, 4, 2, 64, 64, 90)
+    assert need > 0
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    o, lse = torch.full_like(want[0], 9.0), torch.full_like(want[1], 9.0)
+    for _ in range(2):
+        gm.gm_kv8_attention_forward(q, *args(c), None, 0, o=o, lse=lse, workspace=ws)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    with pytest.raises(gm.GMError):
+        gm.gm_kv8_attention_forward(q, *args(c), None, 0, workspace=ws[: need - 1])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = gm.gm_kv8_attention_forward(q, *args(c), None, 0, stream=s)
+    s.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_scales_and_small(dtype):
+    """Blocks whose scales lie far apart, and queries of large and small magnitude."""
+    c = make_cache(21, [150], 10, 1, 16, 64)
+    c["ks"][:] = 2.0 ** -7
+    c["vs"][:] = torch.exp2(torch.arange(c["vs"].numel()).reshape(c["vs"].shape).float() * 9 - 50)
+    for size in (1e-20, 1.0, 1e4):
+        q = (torch.randn(1, 2, 2, 64, generator=torch.Generator().manual_seed(1)) * size).to(dtype)
+        scale = 0.125 / size
+        dev = to_gpu(c)
+        o, lse = gm.gm_kv8_attention_forward(q.cuda(), *args(dev), 100, 3, scale=scale)
+        ro, rl, eo, el = R.cache_attention(q, c, 100, 3, None, scale, dtype)
+        R.check(o, ro, eo, f"o {size}")
+        R.check(lse, rl, el, f"lse {size}")
+
+
 def test_cache_refusals():
     c = to_gpu(make_cache(8, [20], 2, 2, 16, 64))
     q = torch.ones(1, 1, 4, 64, device="cuda").bfloat16()

@@ -225,6 +225,66 @@ def test_stream_argument():
         assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_tensors_at_16_bytes(dtype):
+    """Every tensor starts 16 bytes past a larger boundary."""
+    (q, k, v, dout, _), want = run_and_check(1, 200, 4, 2, 64, dtype, 50, 3, seed=71)
+    step = 16 // q.element_size()
+
+    def moved(x):
+        y = torch.empty(x.numel() + step, dtype=x.dtype, device="cuda")[step:].view(x.shape)
+        y.copy_(x)
+        return y
+
+    q, k, v, dout = (moved(x) for x in (q, k, v, dout))
+    o, dq, dk, dv = (moved(torch.full_like(x, 5.0)) for x in (want[0], *want[2:]))
+    _, lse = gm.gm_window_attention_forward(q, k, v, 50, 3, o=o)
+    gm.gm_window_attention_backward(q, k, v, o, dout, lse, 50, 3, dq=dq, dk=dk, dv=dv)
+    for a, b in zip((o, lse, dq, dk, dv), want):
+        assert torch.equal(a, b)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own outputs and workspace, do not disturb each other."""
+    jobs = []
+    for seed in (1, 2):
+        (q, k, v, dout, _), want = run_and_check(2, 900, 8, 4, 64, torch.bfloat16, 100, 4, seed=seed)
+        jobs.append((torch.cuda.Stream(), q, k, v, dout, want))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s, q, k, v, dout, _ in jobs:
+            o, lse = gm.gm_window_attention_forward(q, k, v, 100, 4, stream=s)
+            got.append((o, lse, *gm.gm_window_attention_backward(q, k, v, o, dout, lse, 100, 4, stream=s)))
+    torch.cuda.synchronize()
+    for y, g in enumerate(got):
+        for a, b in zip(g, jobs[y % 2][5]):
+            assert torch.equal(a, b)
+
+
+def test_outputs_are_written_whole_and_nothing_behind_them():
+    B, n, hq, hkv, d = 2, 133, 4, 2, 64
+    q, k, v, dout = make(81, B, n, hq, hkv, d, torch.bfloat16)
+    lens = torch.tensor([100, 7], dtype=torch.int32, device="cuda")
+    guard = 4096
+
+    def room(shape, dtype):
+        n = math.prod(shape)
+        x = torch.full((n + 2 * guard,), -77.0, dtype=dtype, device="cuda")
+        return x, x[guard: guard + n].view(shape)
+
+    store, view = zip(*(room(s, t) for s, t in ((q.shape, q.dtype), (q.shape[:3], torch.float32), (q.shape, q.dtype),
+                                                (k.shape, k.dtype), (v.shape, v.dtype))))
+    gm.gm_window_attention_forward(q, k, v, 30, 2, lens=lens, o=view[0], lse=view[1])
+    gm.gm_window_attention_backward(q, k, v, view[0], dout, view[1], 30, 2, lens=lens, dq=view[2], dk=view[3], dv=view[4])
+    for x, y in zip(store, view):
+        assert (x[:guard] == -77).all() and (x[-guard:] == -77).all()
+        assert not (y == -77).any()
+        if y.dim() == 4:
+            assert (y[0, 100:] == 0).all() and (y[1, 7:] == 0).all()
+    assert view[1][1, 7:].isneginf().all()
+
+
 def test_empty_batch():
     for B, n in ((0, 5), (3, 0)):
         q, k, v, dout = make(1, B, n, 4, 2, 64, torch.bfloat16)

@@ -488,3 +488,32 @@ def test_empty_calls():
                                          torch.zeros(1, dtype=torch.int32, device="cuda"))
     gm.gm_check_device_errors()
     assert (o == 0).all() and lse.isneginf().all()
+
+
+def test_checked_build_reports_bad_edges():
+    """libgm_b200_checked.so verifies the edges of the rows below q_lens, and only those."""
+    from sparse_dynamic_routing_b200 import _binding as bnd
+
+    c = to_gpu(make_cache(8, [20], 2, 1, 16, 64))
+    q = torch.ones(1, 2, 1, 64, device="cuda").bfloat16()
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 1, device="cuda")
+    ql = torch.tensor([1], dtype=torch.int32, device="cuda")
+    lib = bnd.open_library(bnd.CHECKED_LIB_PATH)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(idx, w):
+        idx = torch.tensor(idx, dtype=torch.int32, device="cuda").reshape(1, 2, 1, 1)
+        w = torch.tensor(w, device="cuda").reshape(1, 2, 1, 1)
+        st = lib.gm_kv8_sea_forward(q.data_ptr(), bnd.GM_BF16, idx.data_ptr(), w.data_ptr(), 1, 1, 2, 1, 1, 64,
+                                    c["kq"].data_ptr(), c["vq"].data_ptr(), c["ks"].data_ptr(), c["vs"].data_ptr(),
+                                    c["kq"].shape[0], 16, c["table"].data_ptr(), 2, c["lens"].data_ptr(), ql.data_ptr(),
+                                    0.125, o.data_ptr(), lse.data_ptr(), stream)
+        assert st == bnd.GM_OK
+        return lib.gm_check_device_errors(stream)
+
+    assert call([19, 0], [1.0, 1.0]) == bnd.GM_OK
+    assert call([19, 99], [1.0, -1.0]) == bnd.GM_OK  # row 1 is padding
+    assert call([3, 0], [-0.5, 1.0]) == bnd.GM_ERR_EDGE_INVALID
+    assert call([3, 0], [math.nan, 1.0]) == bnd.GM_ERR_EDGE_INVALID
+    assert call([20, 0], [1.0, 1.0]) == bnd.GM_ERR_EDGE_INVALID  # past its own position
+    assert call([3, 0], [0.0, 1.0]) == bnd.GM_OK

@@ -244,7 +244,8 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
     a.ndelta = ndelta;
     a.next = (int *)(ndelta + rows);
     a.part = (float *)((char *)w.delta + p.stats_bytes);
-    gm::win_stats_kernel<D><<<(unsigned)((rows * (D / 8) + 1023) / 1024), 256, 0, st>>>(a, nl, ndelta);
+    const unsigned per_seq = (unsigned)(((int64_t)a.npad * w.hq * (D / 8) + 511) / 512);  // blocks of 512 / (D / 8) rows
+    gm::win_stats_kernel<D><<<(unsigned)w.B * per_seq, 256, 0, st>>>(a, gm::FastDiv((uint32_t)w.hq), per_seq, nl, ndelta);
     a.items = (int64_t)p.nblk * w.B * w.hq;
     kq<<<(unsigned)std::min<int64_t>(a.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, a);
     a.items = p.items;

@@ -111,47 +111,46 @@ template <int D> struct WinBwdGeom {
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
-// nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking four rows 256 / (D/8)
-// apart so that eight 16-byte loads are in flight. Also sets both counters to 0. Bound by HBM: o
-// and dout once.
-template <int D> __global__ void __launch_bounds__(256) win_stats_kernel(WinBwdArgs a, float *nl, float *ndelta)
+// nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking two rows so that
+// four 16-byte loads are in flight. A block stays within one sequence, whose rows are contiguous.
+// Also sets both counters to 0. Bound by HBM: o and dout once.
+template <int D> __global__ void __launch_bounds__(256)
+win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, float *nl, float *ndelta)
 {
     if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
-    constexpr int C = D / 8, RPB = 256 / C, N = 4;
+    constexpr int C = D / 8, RPB = 256 / C, N = 2;
     const WinArgs &w = a.w;
-    const int c = threadIdx.x % C;
-    const int64_t row0 = (int64_t)blockIdx.x * (RPB * N) + threadIdx.x / C;
+    const int c = threadIdx.x % C, b = (int)(blockIdx.x / per_seq);
+    const uint32_t y0 = (blockIdx.x - (uint32_t)b * per_seq) * (RPB * N) + threadIdx.x / C;  // row of the sequence
+    const uint32_t rows = (uint32_t)a.npad * w.hq, real = (uint32_t)win_len(w, b) * w.hq;
+    const size_t first = (size_t)b * w.n * w.hq;
     uint4 uo[N], ug[N];
     float lse[N];
-    bool in[N], valid[N];
-    int64_t to[N];
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const int64_t row = row0 + r * RPB, bi = row / w.hq, b = bi / a.npad;
-        const int hq = (int)(row - bi * w.hq), i = (int)(bi - b * a.npad);
-        in[r] = b < w.B;
-        valid[r] = in[r] && i < win_len(w, (int)b);
-        to[r] = (b * w.hq + hq) * a.npad + i;
-        const int64_t src = (b * w.n + i) * w.hq + hq;
+        const uint32_t y = y0 + r * RPB;
         uo[r] = ug[r] = make_uint4(0, 0, 0, 0);
         lse[r] = 0.0f;
-        if (valid[r]) {
-            uo[r] = ld16_stream((const __nv_bfloat16 *)w.o_in + src * D + c * 8);
-            ug[r] = ld16((const __nv_bfloat16 *)w.dout + src * D + c * 8);
-            if (c == 0) lse[r] = __ldg(w.lse_in + src);
+        if (y < real) {
+            uo[r] = ld16_stream((const __nv_bfloat16 *)w.o_in + (first + y) * D + c * 8);
+            ug[r] = ld16((const __nv_bfloat16 *)w.dout + (first + y) * D + c * 8);
+            if (c == 0) lse[r] = __ldg(w.lse_in + first + y);
         }
     }
 #pragma unroll
     for (int r = 0; r < N; ++r) {
+        const uint32_t y = y0 + r * RPB;
         float fo[8], fg[8], x = 0.0f;
         unpack<__nv_bfloat16>(uo[r], fo);
         unpack<__nv_bfloat16>(ug[r], fg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += fo[e] * fg[e];
         x = seg_sum<C>(x);
-        if (in[r] && c == 0) {
-            nl[to[r]] = valid[r] ? -LOG2E * lse[r] : -INFINITY;
-            ndelta[to[r]] = -x;
+        if (y < rows && c == 0) {
+            const uint32_t i = div_hq.div(y), hq = y - i * div_hq.d;
+            const size_t to = ((size_t)b * w.hq + hq) * a.npad + i;
+            nl[to] = y < real ? -LOG2E * lse[r] : -INFINITY;
+            ndelta[to] = -x;
         }
     }
 }
@@ -280,7 +279,7 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const uint32_t q_full = sb, q_empty = sb + 8, tail = sb + 16, k_full = sb + 24, k_empty = k_full + 8 * NK;
     const uint32_t v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV, s_full = v_empty + 8 * NV, s_empty = s_full + 8;
     const uint32_t dp_full = s_empty + 8, ds_full = dp_full + 16, dq_full = ds_full + 16, dq_empty = dq_full + 8;
-    const uint32_t mma_done = dq_empty + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
+    const uint32_t do_full = dq_empty + 8, do_empty = do_full + 8, mma_done = do_empty + 8, tslot = base + Geo::OFF_BAR + Geo::NBAR * 8;
     const uint32_t *tslot_p = reinterpret_cast<const uint32_t *>(sm + Geo::OFF_BAR + Geo::NBAR * 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ItemQueue queue(base + Geo::OFF_BAR + (Geo::NBAR - 8) * 8, sm + Geo::OFF_QUEUE);
@@ -288,6 +287,8 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
+        mbar_init(do_full, 1);
+        mbar_init(do_empty, 1);
         mbar_init(tail, 1);
 #pragma unroll
         for (int s = 0; s < NK; ++s) mbar_init(k_full + 8 * s, 1), mbar_init(k_empty + 8 * s, 1);
@@ -349,10 +350,13 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             ok = __shfl_sync(FULL, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect(q_full, 2 * TILE);
+                mbar_arrive_expect(q_full, TILE);
                 load(sq, &tmq, w.hq, w.i0, q_full);
-                load(sdo, &tmdo, w.hq, w.i0, q_full);
+                if (qc > 0) ok = mbar_wait(do_empty, (qc - 1) & 1);
+                mbar_arrive_expect(do_full, TILE);
+                load(sdo, &tmdo, w.hq, w.i0, do_full);
             }
+            ok = __shfl_sync(FULL, ok, 0);
             ++qc;
             for (int j = 0; ok && j < w.nt; ++j, ++kc) {
                 const uint32_t s3 = kc % NK, s2 = kc % NV;
@@ -384,6 +388,7 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         }
         if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
             mbar_wait(q_full, (qc - 1) & 1);
+            mbar_wait(do_full, (qc - 1) & 1);
             for (uint32_t y = kc > NK ? kc - NK : 0; y < kc; ++y) mbar_wait(k_full + 8 * (y % NK), (y / NK) & 1);
             for (uint32_t y = kc > NV ? kc - NV : 0; y < kc; ++y) mbar_wait(v_full + 8 * (y % NV), (y / NV) & 1);
         }
@@ -411,12 +416,14 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 umma::fence_after_sync();
                 mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
                 umma::commit_if(lead, s_full);
+                if (j == w.nt - 1) umma::commit_if(lead, q_empty);
+                if (j == 0 && !mbar_wait_warp(do_full, qc & 1)) return false;
                 if (!mbar_wait_warp(v_full + 8 * s2, (y / NV) & 1)) return false;
                 umma::fence_after_sync();
                 mma_tiles<D>(lead, tP + (y & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
                 umma::commit_if(lead, dp_full + 8 * (y & 1));
                 umma::commit_if(lead, v_empty + 8 * s2);
-                if (j == w.nt - 1) umma::commit_if(lead, q_empty);
+                if (j == w.nt - 1) umma::commit_if(lead, do_empty);
                 return true;
             };
             ok = mbar_wait_warp(q_full, qc & 1) && first(0);
@@ -444,14 +451,19 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         uint32_t kc = 0;
         int qc = 0;
         bool ok = true;
-        while (ok) {
-            const int item = queue.pop(lane);
-            if (item < 0 || item >= ba.items) break;
+        // an item is taken, and its row's statistics asked for, before the output of the one before
+        int item = queue.pop(lane);
+        float nl = 0.0f, dl = 0.0f;
+        const auto statistics = [&](const Item &w) {
+            const size_t st = ((size_t)w.b * a.hq + w.hq) * ba.npad + w.i0 + r;  // rows are padded to npad
+            nl = __ldg(ba.nl + st);
+            dl = __ldg(ba.ndelta + st);
+        };
+        if (item >= 0 && item < ba.items) statistics(Item(a, item, per));
+        while (item >= 0 && item < ba.items) {
             const Item w(a, item, per);
             const int len = w.len, i0 = w.i0, i = i0 + r;
             const bool valid = i < len;
-            const size_t st = ((size_t)w.b * a.hq + w.hq) * ba.npad + i;  // i < npad
-            const float nl = valid ? __ldg(ba.nl + st) : 0.0f, dl = valid ? __ldg(ba.ndelta + st) : 0.0f;
             for (int j = 0; j < w.nt; ++j) {
                 const uint32_t y = kc + j;
                 const int t0 = w.kb.start(j, UW), t1 = w.kb.end(j, UW);
@@ -528,6 +540,8 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
             }
             kc += w.nt;
             if (!ok) break;
+            item = queue.pop(lane);
+            if (item >= 0 && item < ba.items) statistics(Item(a, item, per));
             if (w.nt > 0) {
                 ok = mbar_wait_warp(dq_full, qc & 1);
                 if (!ok) break;

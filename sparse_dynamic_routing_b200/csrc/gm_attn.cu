@@ -63,6 +63,7 @@ gm::WinArgs window_args(int B, int n, int hq, int hkv, int window, int sinks, fl
     a.G = hq / hkv;
     a.window = std::min(window, n);
     a.sinks = std::min(sinks, n);
+    a.lone = a.window + a.sinks == 1 ? n : 1;
     a.scale = scale;
     a.lens = lens;
     return a;
@@ -102,25 +103,61 @@ template <int D, int R> gm_status window_dq_f32(gm::WinArgs a, cudaStream_t st)
     return launched();
 }
 
-template <int D, int R> gm_status window_dkv_f32(gm::WinArgs a, cudaStream_t st)
+// The fp32 dk, dv kernel's cut of key blocks with sinks (gm_window.cuh).
+struct WinF32Plan {
+    int rows, nblk, sink_blocks, chunks, steps;  // rows: per thread
+    size_t delta_bytes, bytes;                   // workspace: delta, then the pieces
+};
+
+WinF32Plan window_f32_plan(int B, int n, int hq, int hkv, int d, int window, int sinks)
+{
+    WinF32Plan p{};
+    const int G = hq / hkv;
+    window = std::min(window, n);
+    sinks = std::min(sinks, n);
+    p.rows = f32_rows(n, (int64_t)B * hkv);
+    const int tile = 16 * p.rows;
+    p.nblk = (n + tile - 1) / tile;
+    // query tiles of the longest block, with and without sinks
+    const int all = (n + gm::WT - 1) / gm::WT;
+    const int near = (int)std::min<int64_t>(all, ((int64_t)tile - 1 + window + gm::WT - 1) / gm::WT);
+    p.steps = std::max(near * G, 4);
+    p.chunks = (all * G + p.steps - 1) / p.steps;
+    p.sink_blocks = p.chunks > 1 ? std::min(p.nblk, (sinks + tile - 1) / tile) : 0;
+    p.delta_bytes = ((size_t)B * n * hq * 4 + 15) / 16 * 16;
+    p.bytes = p.delta_bytes + (size_t)B * hkv * p.sink_blocks * p.chunks * 2 * tile * d * 4;
+    return p;
+}
+
+template <int D, int R> gm_status window_dkv_f32(gm::WinArgs a, const WinF32Plan &p, cudaStream_t st)
 {
     using S = gm::WinF32<D, R>;
     constexpr auto kern = gm::win_dkv_f32_kernel<D, R>;
     if (!raise_smem<kern>(S::dkv_smem)) return GM_ERR_CUDA;
-    a.nblk = (a.n + S::ROWS - 1) / S::ROWS;
-    kern<<<(unsigned)((int64_t)a.nblk * a.B * a.hkv), 256, S::dkv_smem, st>>>(a);
+    a.nblk = p.nblk;
+    a.sink_blocks = p.sink_blocks;
+    a.chunks = p.chunks;
+    a.steps = p.steps;
+    a.part = (float *)((char *)a.delta + p.delta_bytes);
+    const int64_t per = (int64_t)a.B * a.hkv;
+    const int64_t grid = per * (a.nblk - a.sink_blocks) + per * a.sink_blocks * a.chunks;
+    if (grid >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    kern<<<(unsigned)grid, 256, S::dkv_smem, st>>>(a);
+    if (a.sink_blocks > 0)
+        gm::win_dkv_join_f32_kernel<D, R><<<(unsigned)(per * a.sink_blocks * (2 * S::ROWS * D / 4) / 256), 256, 0, st>>>(a);
     return launched();
 }
 
 template <int D> gm_status window_backward(const gm::WinArgs &a, cudaStream_t st)
 {
     gm::win_delta_kernel<D><<<(unsigned)(((int64_t)a.B * a.n * a.hq + 7) / 8), 256, 0, st>>>(a);
-    const int rq = f32_rows(a.n, (int64_t)a.B * a.hq), rk = f32_rows(a.n, (int64_t)a.B * a.hkv);
+    const int rq = f32_rows(a.n, (int64_t)a.B * a.hq);
     const gm_status s = rq == 4   ? window_dq_f32<D, 4>(a, st)
                         : rq == 2 ? window_dq_f32<D, 2>(a, st)
                                   : window_dq_f32<D, 1>(a, st);
     if (s != GM_OK) return s;
-    return rk == 4 ? window_dkv_f32<D, 4>(a, st) : rk == 2 ? window_dkv_f32<D, 2>(a, st) : window_dkv_f32<D, 1>(a, st);
+    const WinF32Plan p = window_f32_plan(a.B, a.n, a.hq, a.hkv, D, a.window, a.sinks);
+    return p.rows == 4 ? window_dkv_f32<D, 4>(a, p, st) : p.rows == 2 ? window_dkv_f32<D, 2>(a, p, st) : window_dkv_f32<D, 1>(a, p, st);
 }
 
 // A bf16 feature tensor [B, n, heads, d] as a 4-d TMA map whose boxes are 64 elements of d (128
@@ -413,7 +450,7 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
 size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n, int hq, int hkv, int d, int window, int sinks)
 {
     if (check_window(dtype, B, n, hq, hkv, d, window, sinks, 1.0f) != GM_OK || (int64_t)B * n == 0) return 0;
-    if (dtype == GM_F32) return ((size_t)B * n * hq * 4 + 15) / 16 * 16;
+    if (dtype == GM_F32) return window_f32_plan(B, n, hq, hkv, d, window, sinks).bytes;
     return window_backward_plan(B, n, hq, hkv, d, window, sinks).bytes;
 }
 

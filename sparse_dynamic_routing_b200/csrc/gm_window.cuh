@@ -20,7 +20,9 @@
 // (B=1 n=128, two heads: 125 us with R = 4, 53 us with R = 1, forward and backward).
 // Bound by the fp32 pipes; there is no tensor-core type that keeps fp32's 24 bits. The backward
 // is two kernels without atomics: one per query block (dq) and one per key block (dk, dv, summed
-// over the group's heads in the block), so every gradient is written once, in a fixed order.
+// over the group's heads in the block), so every gradient is written once, in a fixed order. Key
+// blocks with sinks, which every query sees, are cut into pieces of about the other blocks' length
+// whose sums a last kernel adds (B=4 n=1000 window 200, 2 sinks: 659 -> 349 us for the backward).
 #pragma once
 
 #include <math.h>
@@ -43,6 +45,11 @@ struct WinArgs {
     int window, sinks;
     float scale;
     int nblk;                // blocks along the sequence
+    int lone;                // backward: the first rows that see one key alone (1, or n with window 1 and no sinks)
+    // fp32 dk, dv: the first sink_blocks key blocks are cut into `chunks` pieces of `steps` query tiles,
+    // whose sums go to part [piece][dk, dv][rows][D]
+    int sink_blocks, chunks, steps;
+    float *part;
 };
 
 __device__ __forceinline__ int win_len(const WinArgs &a, int b)
@@ -356,7 +363,7 @@ template <int D, int R> __global__ void __launch_bounds__(256) win_dq_f32_kernel
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int t = t0 + tx + 16 * c;
-                const bool see = qi < len && t < t1 && win_sees(qi, t, a.window, a.sinks);
+                const bool see = qi < len && qi >= a.lone && t < t1 && win_sees(qi, t, a.window, a.sinks);
                 const float p = exp2f(fmaf(s[i][c], a.scale * LOG2E, nl[i]));
                 sd[(ty * R + i) * WLP + tx + 16 * c] = see ? p * (dp[i][c] - dl[i]) : 0.0f;
             }
@@ -375,9 +382,12 @@ template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_f32_kerne
     float *sk = wsm, *sv = sk + ROWS * S::LD, *sq = sv + ROWS * S::LD, *sdo = sq + WT * S::LD;
     float *sp = sdo + WT * S::LD, *sd = sp + ROWS * WLP;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const int per = a.B * a.hkv;
-    const int blk = (int)(blockIdx.x / (unsigned)per);  // the keys that most queries see first
-    const int bh = (int)(blockIdx.x % (unsigned)per);
+    const unsigned per = (unsigned)(a.B * a.hkv), pieces = per * (unsigned)(a.sink_blocks * a.chunks);
+    const bool cut = blockIdx.x < pieces;  // a piece of a block that (nearly) every query sees; those come first
+    const unsigned x = cut ? blockIdx.x / (unsigned)a.chunks : blockIdx.x - pieces;
+    const int chunk = cut ? (int)(blockIdx.x - x * (unsigned)a.chunks) : 0;
+    const int blk = (cut ? 0 : a.sink_blocks) + (int)(x / per);
+    const int bh = (int)(x % per);
     const int b = bh / a.hkv, h = bh - b * a.hkv;
     const int len = win_len(a, b), t0 = blk * ROWS, t1 = min(t0 + ROWS, len);
     const size_t qs = (size_t)a.hq * D, ks = (size_t)a.hkv * D;
@@ -388,10 +398,12 @@ template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_f32_kerne
     zero(gk);
     zero(gv);
     const int qend = t1 > t0 ? query_end(t0, t1, len, a.window, a.sinks) : t0;
-    for (int g = 0; g < a.G; ++g) {
-        const int hq = h * a.G + g;
-        const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D;
-        for (int i0 = t0; i0 < qend; i0 += WT) {
+    const int nq = (qend - t0 + WT - 1) / WT;  // query tiles per head
+    const int j0 = cut ? min(chunk * a.steps, nq * a.G) : 0, j1 = cut ? min(j0 + a.steps, nq * a.G) : nq * a.G;
+    {
+        for (int j = j0; j < j1; ++j) {
+            const int g = j / nq, hq = h * a.G + g, i0 = t0 + (j - g * nq) * WT;
+            const size_t qo = (size_t)b * a.n * qs + (size_t)hq * D;
             __syncthreads();
             load_tile<D, WT>(sq, (const float *)a.q + qo, qs, i0, len);
             load_tile<D, WT>(sdo, (const float *)a.dout + qo, qs, i0, len);
@@ -415,7 +427,7 @@ template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_f32_kerne
                     const bool see = qi < len && t < len && win_sees(qi, t, a.window, a.sinks);
                     const float p = see ? exp2f(fmaf(s[i][c], a.scale * LOG2E, nl[c])) : 0.0f;
                     sp[(ty * R + i) * WLP + tx + 16 * c] = p;
-                    sd[(ty * R + i) * WLP + tx + 16 * c] = see ? p * (dp[i][c] - dl[c]) : 0.0f;
+                    sd[(ty * R + i) * WLP + tx + 16 * c] = see && qi >= a.lone ? p * (dp[i][c] - dl[c]) : 0.0f;
                 }
             }
             __syncwarp();
@@ -426,8 +438,34 @@ template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_f32_kerne
     float scale[R], one[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) scale[i] = a.scale, one[i] = 1.0f;
-    store_tile<D, R>((float *)a.dk + ko, ks, t0, a.n, ty, tx, gk, scale);
-    store_tile<D, R>((float *)a.dv + ko, ks, t0, a.n, ty, tx, gv, one);
+    if (cut) {
+        float *part = a.part + (size_t)blockIdx.x * (2 * ROWS * D);
+        store_tile<D, R>(part, D, 0, ROWS, ty, tx, gk, scale);
+        store_tile<D, R>(part + ROWS * D, D, 0, ROWS, ty, tx, gv, one);
+    } else {
+        store_tile<D, R>((float *)a.dk + ko, ks, t0, a.n, ty, tx, gk, scale);
+        store_tile<D, R>((float *)a.dv + ko, ks, t0, a.n, ty, tx, gv, one);
+    }
+}
+
+// dk and dv of the key blocks that were cut: their pieces added in order, four elements per thread.
+template <int D, int R> __global__ void __launch_bounds__(256) win_dkv_join_f32_kernel(WinArgs a)
+{
+    constexpr int ROWS = 16 * R, PER = 2 * ROWS * D / 4;
+    const unsigned x = (blockIdx.x * 256u + threadIdx.x) / PER;  // (block, sequence, head)
+    const int e = (int)((blockIdx.x * 256u + threadIdx.x) - x * PER), kv = e / (PER / 2), at = (e - kv * (PER / 2)) * 4;
+    const unsigned per = (unsigned)(a.B * a.hkv);
+    const int blk = (int)(x / per), bh = (int)(x % per), b = bh / a.hkv, h = bh - b * a.hkv;
+    const int t = blk * ROWS + at / D;
+    if (t >= a.n) return;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = 0; c < a.chunks; ++c) {  // a piece without steps holds zeros
+        const float4 v = *reinterpret_cast<const float4 *>(
+            a.part + ((size_t)x * a.chunks + c) * (2 * ROWS * D) + (size_t)kv * ROWS * D + at);
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    float *dst = (float *)(kv ? a.dv : a.dk) + (((size_t)b * a.n + t) * a.hkv + h) * D + at % D;
+    *reinterpret_cast<float4 *>(dst) = sum;
 }
 
 }  // namespace gm

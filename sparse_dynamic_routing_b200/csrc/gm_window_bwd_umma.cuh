@@ -30,6 +30,9 @@
 // cut into chunks, each an item of its own that writes fp32 partial sums to the workspace, and
 // win_dkv_join_kernel adds those in chunk order.
 //
+// A row that sees one key has P = 1 whatever its score: its dS is 0, not the difference of two equal
+// sums (WinArgs::lone).
+//
 // Every wait is bounded (gm_common.cuh, mbar_wait).
 #pragma once
 
@@ -114,6 +117,13 @@ template <int D> struct WinBwdGeom {
 // nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking two rows so that
 // four 16-byte loads are in flight. A block stays within one sequence, whose rows are contiguous.
 // Also sets both counters to 0. Bound by HBM: o and dout once.
+//
+// delta = <dout, o> inherits the rounding of o to bf16, an error that reaches dS as P times a
+// constant of the row. Averaged over many keys it is lost in the other roundings, but a row of
+// few keys has o as large as v and dS = P (dP - delta) as a difference of near values. Rows that
+// see at most FEW keys get delta = sum_t P dP instead, from q, k, v and dout.
+constexpr int FEW = 24;
+
 template <int D> __global__ void __launch_bounds__(256)
 win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, float *nl, float *ndelta)
 {
@@ -134,22 +144,48 @@ win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, float *nl, floa
         if (y < real) {
             uo[r] = ld16_stream((const __nv_bfloat16 *)w.o_in + (first + y) * D + c * 8);
             ug[r] = ld16((const __nv_bfloat16 *)w.dout + (first + y) * D + c * 8);
-            if (c == 0) lse[r] = __ldg(w.lse_in + first + y);
+            lse[r] = __ldg(w.lse_in + first + y);
         }
     }
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const uint32_t y = y0 + r * RPB;
+        const uint32_t y = y0 + r * RPB, i = div_hq.div(y), hq = y - i * div_hq.d;
+        const float mynl = y < real ? -LOG2E * lse[r] : -INFINITY;
         float fo[8], fg[8], x = 0.0f;
         unpack<__nv_bfloat16>(uo[r], fo);
         unpack<__nv_bfloat16>(ug[r], fg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += fo[e] * fg[e];
         x = seg_sum<C>(x);
+        const int64_t seen = min((int64_t)i + 1, (int64_t)w.window + w.sinks);
+        const int keys = y < real && seen <= FEW ? (int)seen : 0;
+        const int most = __reduce_max_sync(FULL, keys);
+        if (most > 0) {
+            float fq[8], sum = 0.0f;
+            const int lo = max((int)i - w.window + 1, 0), ns = min(w.sinks, lo);  // sinks before the window
+            unpack<__nv_bfloat16>(keys ? ld16((const __nv_bfloat16 *)w.q + (first + y) * D + c * 8) : make_uint4(0, 0, 0, 0), fq);
+            for (int u = 0; u < most; ++u) {
+                const int t = u < ns ? u : lo + u - ns;
+                const size_t at = (((size_t)b * w.n + t) * w.hkv + hq / w.G) * D + c * 8;
+                uint4 uk = make_uint4(0, 0, 0, 0), uv = uk;
+                if (u < keys) uk = ld16((const __nv_bfloat16 *)w.k + at), uv = ld16((const __nv_bfloat16 *)w.v + at);
+                float fk[8], fv[8];
+                float2 dots = make_float2(0.0f, 0.0f);
+                unpack<__nv_bfloat16>(uk, fk);
+                unpack<__nv_bfloat16>(uv, fv);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dots.x += fq[e] * fk[e];
+                    dots.y += fg[e] * fv[e];
+                }
+                dots = seg_sum2<C>(dots);
+                if (u < keys) sum += ex2_ftz(fmaf(dots.x, w.scale, mynl)) * dots.y;
+            }
+            if (keys) x = sum;
+        }
         if (y < rows && c == 0) {
-            const uint32_t i = div_hq.div(y), hq = y - i * div_hq.d;
             const size_t to = ((size_t)b * w.hq + hq) * a.npad + i;
-            nl[to] = y < real ? -LOG2E * lse[r] : -INFINITY;
+            nl[to] = mynl;
             ndelta[to] = -x;
         }
     }
@@ -487,8 +523,8 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                     const int col = c0 + c * 32;
                     piece[c] = key_piece(i0 + (warp & 3) * 32, t0 + col, t1, len, a.window, a.sinks);
                     if (whole) piece[c] = c < nch ? Piece::all : Piece::none;
-                    mask[c] = piece[c] == Piece::some ? column_mask(col, i - a.window + 1 - t0, valid ? min(i, t1 - 1) - t0 : -1,
-                                                                    a.sinks - t0)
+                    mask[c] = piece[c] == Piece::some ? column_mask(col, i - a.window + 1 - t0,
+                                                                    valid && i >= a.lone ? min(i, t1 - 1) - t0 : -1, a.sinks - t0)
                                                       : 0u;
                     if (piece[c] == Piece::none) continue;
 #pragma unroll
@@ -824,6 +860,13 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                                                                     make_float2(z.z, z.w)));
                             x[2 * e] = bf16_pair(x0.x, x0.y);
                             x[2 * e + 1] = bf16_pair(x1.x, x1.y);
+                        }
+                        if (i0 + c0 + c * 32 < a.lone) {  // queries that see one key
+                            x[0] &= 0xffff0000u;
+                            if (a.lone > 1) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) x[e] = 0u;
+                            }
                         }
                     }
                     // dS of piece c lies over dP of this or an earlier piece of the group

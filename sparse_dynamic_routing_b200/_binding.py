@@ -625,19 +625,19 @@ def gm_dense_refresh_edges(q, k, lse, sf: int, scale=None, out_idx=None, out_w=N
 # ---- dense layers and serving ---------------------------------------------------------------------
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _on(dev, stream):
     """Context in which `dev` is current and torch's current stream is the call's: outputs then
-    belong to the stream that writes them. None if that is so already."""
+    belong to the stream that writes them."""
     if stream is None:
-        return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return _HERE_AND_NOW if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=dev) if int(stream) else torch.cuda.default_stream(dev)
     if stream.device != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
     return torch.cuda.stream(stream)
-
-
-_HERE_AND_NOW = contextlib.nullcontext()
 
 
 def _current_stream(dev) -> int:
@@ -648,7 +648,7 @@ def _current_stream(dev) -> int:
 
 def _arg(t, shape, dtype, dev, name):
     """Pointer of a contiguous tensor of this shape, type and device."""
-    if t.get_device() != dev.index or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+    if t.device != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         if t.device != dev:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
         if t.dtype != dtype:
@@ -660,13 +660,13 @@ def _arg(t, shape, dtype, dev, name):
 
 
 def _queries(q, hkv):
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    if q.dim() != 4:
-        raise ValueError("q must be [B, n, hq, d]")
-    if hkv < 1 or q.shape[2] % hkv:
-        raise ValueError(f"{q.shape[2]} query heads do not divide into {hkv} KV heads")
-    return q.device
+    """Device and sizes of a query tensor [B, n, hq, d]."""
+    if not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, n, hq, d]")
+    B, n, hq, d = q.shape
+    if hkv < 1 or hq % hkv:
+        raise ValueError(f"{hq} query heads do not divide into {hkv} KV heads")
+    return q.device, B, n, hq, d
 
 
 def _window(window, sinks):
@@ -679,10 +679,18 @@ def _window(window, sinks):
 def _out(t, like, shape, dtype, dev, name):
     """An output: the caller's tensor, checked, or a new one."""
     if t is None:
-        t = torch.empty_like(like) if like.dtype is dtype and like.shape == shape \
-            else like.new_empty(shape, dtype=dtype)
+        t = torch.empty_like(like) if like.dtype is dtype and like.shape == shape else like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     return t, _arg(t, shape, dtype, dev, name)
+
+
+def _out_rows(o, lse, q, dev):
+    """The outputs o and lse of attention over queries q, and their pointers."""
+    shape = q.shape
+    o, po = (torch.empty_like(q), None) if o is None else (o, _arg(o, shape, q.dtype, dev, "o"))
+    lse, pl = (q.new_empty(shape[:3], dtype=torch.float32), None) if lse is None else (
+        lse, _arg(lse, shape[:3], torch.float32, dev, "lse"))
+    return o, po or o.data_ptr(), lse, pl or lse.data_ptr()
 
 
 def gm_window_attention_forward(q, k, v, window=None, sinks: int = 0, lens=None, scale=None, o=None, lse=None,
@@ -690,14 +698,12 @@ def gm_window_attention_forward(q, k, v, window=None, sinks: int = 0, lens=None,
     """Causal attention with a sliding window (None: every earlier token) and `sinks` first tokens
     that stay visible. q [B, n, hq, d], k and v [B, n, hkv, d]; lens int32 [B] or None. Returns
     (o, lse [B, n, hq] fp32); gm_dense_refresh_edges takes the lse of a call without a window."""
-    hkv, d = k.shape[-2:]
-    dev = _queries(q, hkv)
-    B, n, hq, _ = q.shape
-    dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
+    hkv = k.shape[-2]
+    dev, B, n, hq, d = _queries(q, hkv)
+    dt, kv = q.dtype, (B, n, hkv, d)
     window, sinks = _window(window, sinks)
-    with _on(dev, stream) or _HERE_AND_NOW:
-        o, po = _out(o, q, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream):
+        o, po, lse, pl = _out_rows(o, lse, q, dev)
         st = load_library().gm_window_attention_forward(
             _arg(q, q.shape, dt, dev, "q"), _arg(k, kv, dt, dev, "k"), _arg(v, kv, dt, dev, "v"), _fdtype(q),
             None if lens is None else _arg(lens, (B,), torch.int32, dev, "lens"), B, n, hq, hkv, d, window, sinks,
@@ -719,13 +725,12 @@ def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int 
     """Gradients of gm_window_attention_forward from its o and lse. Returns (dq, dk, dv) in the
     features' dtype. workspace: a uint8 CUDA tensor of at least
     gm_window_attention_backward_workspace_size(...) bytes; None allocates one."""
-    hkv, d = k.shape[-2:]
-    dev = _queries(q, hkv)
-    B, n, hq, _ = q.shape
-    dt, kv = q.dtype, torch.Size((B, n, hkv, q.shape[3]))
+    hkv = k.shape[-2]
+    dev, B, n, hq, d = _queries(q, hkv)
+    dt, kv = q.dtype, (B, n, hkv, d)
     window, sinks = _window(window, sinks)
     lib = load_library()
-    with _on(dev, stream) or _HERE_AND_NOW:
+    with _on(dev, stream):
         dq, pdq = _out(dq, q, q.shape, dt, dev, "dq")
         dk, pdk = _out(dk, k, kv, dt, dev, "dk")
         dv, pdv = _out(dv, v, kv, dt, dev, "dv")
@@ -746,17 +751,18 @@ def gm_window_attention_backward(q, k, v, o, dout, lse, window=None, sinks: int 
 
 def _cache(kq, vq, kscale, vscale, table, lens, B, d, dev):
     """The C arguments of a cache (kq .. max_pages, lens), checked."""
-    if kq.dim() != 4 or kq.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    dt = kq.dtype
+    if kq.dim() != 4 or (dt is not torch.float8_e4m3fn and dt is not torch.uint8):
         raise ValueError("kq must be [num_pages, hkv, page, d] in float8_e4m3fn or uint8")
-    pages, hkv, page, _ = kq.shape
-    if kq.shape[3] != d:
-        raise ValueError(f"the cache has head_dim {kq.shape[3]}, the features {d}")
-    if table.dim() != 2 or table.shape[0] != B:
+    shape = kq.shape
+    pages, hkv, page, dc = shape
+    if dc != d:
+        raise ValueError(f"the cache has head_dim {dc}, the features {d}")
+    if table.dim() != 2:
         raise ValueError("table must be [B, max_pages]")
-    f32, i32 = torch.float32, torch.int32
-    return (_arg(kq, kq.shape, kq.dtype, dev, "kq"), _arg(vq, kq.shape, kq.dtype, dev, "vq"),
-            _arg(kscale, kq.shape[:2], f32, dev, "kscale"), _arg(vscale, kq.shape[:2], f32, dev, "vscale"),
-            pages, page, _arg(table, table.shape, i32, dev, "table"), table.shape[1],
+    maxp, blocks, f32, i32 = table.shape[1], (pages, hkv), torch.float32, torch.int32
+    return (_arg(kq, shape, dt, dev, "kq"), _arg(vq, shape, dt, dev, "vq"), _arg(kscale, blocks, f32, dev, "kscale"),
+            _arg(vscale, blocks, f32, dev, "vscale"), pages, page, _arg(table, (B, maxp), i32, dev, "table"), maxp,
             _arg(lens, (B,), i32, dev, "lens"))
 
 
@@ -771,7 +777,7 @@ def gm_kv8_append(k, v, kq, vq, kscale, vscale, table, lens, new_lens=None, stre
     if kq.dim() != 4 or kq.shape[1] != hkv:
         raise ValueError(f"kq must be [num_pages, {hkv}, page, {d}]")
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
-    with _on(dev, stream) or _HERE_AND_NOW:
+    with _on(dev, stream):
         st = load_library().gm_kv8_append(
             _arg(k, k.shape, k.dtype, dev, "k"), _arg(v, k.shape, k.dtype, dev, "v"), _fdtype(k), B, t, hkv, d, *cache,
             None if new_lens is None else _arg(new_lens, (B,), torch.int32, dev, "new_lens"),
@@ -792,15 +798,13 @@ def gm_kv8_attention_forward(q, kq, vq, kscale, vscale, table, lens, window=None
     8-bit cache; lens counts the query tokens too. Returns (o, lse [B, t, hq]). workspace: a uint8
     CUDA tensor of at least gm_kv8_attention_workspace_size(...) bytes; None allocates one."""
     hkv = kq.shape[1]
-    dev = _queries(q, hkv)
-    B, t, hq, d = q.shape
+    dev, B, t, hq, d = _queries(q, hkv)
     dt = q.dtype
     window, sinks = _window(window, sinks)
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
     lib = load_library()
-    with _on(dev, stream) or _HERE_AND_NOW:
-        o, po = _out(o, q, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream):
+        o, po, lse, pl = _out_rows(o, lse, q, dev)
         if workspace is None:
             need = lib.gm_kv8_attention_workspace_size(B, t, hq, hkv, d, kq.shape[2], table.shape[1], window, sinks)
             workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
@@ -819,14 +823,12 @@ def gm_kv8_sea_forward(q, idx, w, kq, vq, kscale, vscale, table, lens, q_lens=No
     """gm_sea_forward for the last tokens of each sequence (q [B, t, hq, d], idx and w
     [B, t, hkv, s]) over the 8-bit cache. Returns (o, lse [B, t, hq])."""
     hkv = kq.shape[1]
-    dev = _queries(q, hkv)
-    B, t, hq, d = q.shape
+    dev, B, t, hq, d = _queries(q, hkv)
     dt, s = q.dtype, idx.shape[-1]
-    edges = torch.Size((B, t, hkv, s))
+    edges = (B, t, hkv, s)
     cache = _cache(kq, vq, kscale, vscale, table, lens, B, d, dev)
-    with _on(dev, stream) or _HERE_AND_NOW:
-        o, po = _out(o, q, q.shape, dt, dev, "o")
-        lse, pl = _out(lse, q, q.shape[:3], torch.float32, dev, "lse")
+    with _on(dev, stream):
+        o, po, lse, pl = _out_rows(o, lse, q, dev)
         st = load_library().gm_kv8_sea_forward(
             _arg(q, q.shape, dt, dev, "q"), _fdtype(q), _arg(idx, edges, torch.int32, dev, "idx"),
             _arg(w, edges, torch.float32, dev, "w"), s, B, t, hq, hkv, d, *cache,

@@ -551,7 +551,9 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
  *                gm_window_attention_backward_workspace_size(...) bytes; its contents do not
  *                matter and are garbage on return. Calls that overlap on the GPU need one each
  *   limits       as the forward; every pointer 16-byte aligned except lens and lse
- * For GM_BF16, P and dz are rounded to bf16 before their products. Deterministic.
+ * For GM_BF16, P and dz are rounded to bf16 before their products. A row that sees one key has
+ * exactly dz = 0; rows of at most 24 keys take delta from sum_t P_t <dout, v_t>, which does not
+ * carry the rounding of o. Deterministic.
  */
 gm_status gm_window_attention_backward(const void *q, const void *k, const void *v, const void *o,
                                        const void *dout, const float *lse, gm_dtype dtype,
@@ -650,7 +652,8 @@ gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, 
 /*
  * gm_check_device_errors - synchronise `stream`, then read and clear this device's error
  * flag. Returns GM_ERR_INDEX_RANGE if any kernel of this library on the current device met
- * an active slot whose index lay outside [0, n) since the last check, GM_ERR_EDGE_INVALID if
+ * an active slot whose index lay outside [0, n), or a cache page or length outside its pool or
+ * table, since the last check, GM_ERR_EDGE_INVALID if
  * (checked build) an input edge broke the edge invariants (see gm_checked_build),
  * GM_ERR_WAIT_TIMEOUT if a kernel gave up on a bounded wait (an asynchronous copy, a
  * tensor-core operation, or the backward scan's look-back at earlier blocks; its outputs are
@@ -665,7 +668,7 @@ gm_status gm_check_device_errors(cudaStream_t stream);
  * second; the kernel then sets the device error flag and returns, so the following
  * gm_check_device_errors returns GM_ERR_WAIT_TIMEOUT and the device stays usable. The
  * library's real waits (asynchronous copies and tensor-core operations of
- * gm_dense_refresh_edges, the look-back of the backward's scan) give up the same way.
+ * gm_dense_refresh_edges and gm_window_attention_*, the look-back of the backward's scan) give up the same way.
  */
 gm_status gm_selftest_wait_timeout(cudaStream_t stream);
 

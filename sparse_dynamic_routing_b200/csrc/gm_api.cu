@@ -629,7 +629,9 @@ const char *gm_status_string(gm_status status)
     case GM_ERR_INVALID_ARG: return "GM_ERR_INVALID_ARG: invalid argument";
     case GM_ERR_UNSUPPORTED: return "GM_ERR_UNSUPPORTED: no kernel in this library for the shape";
     case GM_ERR_CUDA: return "GM_ERR_CUDA: CUDA launch or synchronisation failed";
-    case GM_ERR_INDEX_RANGE: return "GM_ERR_INDEX_RANGE: an active edge index was outside [0, n)";
+    case GM_ERR_INDEX_RANGE:
+        return "GM_ERR_INDEX_RANGE: an active edge index was outside [0, n), or a cache page or length "
+               "outside its pool or table";
     case GM_ERR_SCRATCH_TOO_SMALL:
         return "GM_ERR_SCRATCH_TOO_SMALL: the problem needs more scratch than the library's fixed "
                "array holds (see gm_sea_backward_noalloc_max_scratch)";

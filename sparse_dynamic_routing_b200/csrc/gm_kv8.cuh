@@ -215,7 +215,7 @@ template <typename T, int D, int PAGE> __global__ void __launch_bounds__(256) kv
 // warps are joined in shared memory; with more than one split the blocks write partial outputs
 // to the workspace and a second kernel joins those, in a fixed order. (A cluster that joins
 // through distributed shared memory needs no workspace, but a GPU holds only 7 clusters of 16 such
-// blocks, and one sequence of 8 KV heads then waits for two rounds: 72 us against 35 us for 65536
+// blocks, and one sequence of 8 KV heads then waits for two rounds: 72 us against 33 us for 65536
 // tokens.)
 //
 // Arithmetic. mma.sync m16n8k16 with fp16 operands and fp32 sums, computed transposed

@@ -37,16 +37,6 @@ __host__ __device__ constexpr uint64_t sdesc_sw128_kmajor(uint32_t smem_addr)
 // The same descriptor with B held MN-major (bit 16): B's N runs along the contiguous dimension.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) { return idesc_bf16_f32(M, N) | (1u << 16); }
 
-// Shared-memory matrix descriptor of an MN-major operand in the 128-byte swizzle layout: rows of
-// 128 bytes hold 64 bf16 along M/N, one row per K index, eight-row groups of 1024 bytes stacked
-// along K. Leading byte offset: from one 64-element block of M/N to the next; stride byte
-// offset: between eight-row groups. A K step of 16 rows advances the start address by 2048 bytes.
-__host__ __device__ constexpr uint64_t sdesc_sw128_mnmajor(uint32_t smem_addr, uint32_t block_bytes)
-{
-    return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | ((uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 #if defined(__CUDACC__)
 
 // ---- MMA issue by a whole warp -----------------------------------------------------------------
@@ -65,6 +55,10 @@ __device__ __forceinline__ uint32_t elect_lead()
     return lead;
 }
 
+// K-major operands: as sdesc_sw128_kmajor. MN-major ones: rows of 128 bytes hold 64 bf16 along M/N, one
+// row per K index, eight-row groups of 1024 bytes stacked along K (the stride byte offset);
+// block_bytes, the leading byte offset, leads from one 64-element block of M/N to the next. A K
+// step of 16 advances the start address by 32 bytes K-major, by 2048 bytes MN-major.
 constexpr uint32_t SDESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // as in sdesc_sw128_*
 __device__ __forceinline__ uint32_t sdesc_lo(uint32_t smem_addr, uint32_t block_bytes)
 {

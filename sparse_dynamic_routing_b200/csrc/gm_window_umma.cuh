@@ -1,28 +1,34 @@
 // gm_window_umma.cuh - the windowed attention's bf16 kernels, on the tensor cores (tcgen05).
 //
 // Forward. A CTA works on two tiles of 128 query rows that share their keys: two heads of one
-// group over the same rows (groups of even size), or one head's next 256 rows. Per block of 64
-// keys and tile: S = Q K^T into one of the tile's two score buffers in TMEM; one thread per query
-// row reads its 64 scores, keeps the running maximum and sum, and writes P as bf16 over S;
-// O += P V with P as the TMEM operand. The score buffers let S run a block ahead, so the softmax
-// threads, whose exponentials bound the kernel (16 per SM and cycle: 2048 cycles per 128 keys of
-// both tiles, as long as the products), go from block to block without waiting for a product.
-// With one 128-key buffer per tile they waited for P V and the next S each time (2.2 against
-// 1.6 us per 128 keys).
+// group over the same rows (groups of even size), or one head's next 256 rows. Per block of 128
+// keys and tile: S = Q K^T into TMEM; one thread per query row reads its scores, keeps the running
+// maximum and sum, and writes P as bf16 over S; O += P V with P as the TMEM operand. While one
+// tile's rows are in the softmax, the tensor cores work on the other's.
 //   warps 0-3, 4-7  softmax of tile 0, 1 (and their output)
-//   warp 8          TMA loads: Q per item, K and V through four stages each
+//   warp 8          TMA loads: Q per item, K and V through their stages
 //   warp 9          MMA issue
-// TMEM: two tiles x two buffers of 64 columns for S, then O0, O1 (D columns each).
+// TMEM: S0, S1 (128 columns each), O0, O1 (D columns each).
+//
+// A thread reads its scores twice, 32 columns at a time, once for the maximum and once for the
+// exponentials: 128 of them kept in registers spill, and TMEM has the bandwidth. P is handed over
+// in two halves, so that the first half's products run under the second half's exponentials.
+// With the softmax replaced by nothing the kernel takes 738 us for n = 16384 (16 heads, full), with
+// it 935: the products (at 90 % of the measured bf16 rate when alone) bound it, then the wait for
+// each block's exponentials (16 per SM and cycle). Blocks of 64 keys with two score buffers per
+// tile remove that wait but run the products at N = 64, 976 us alone.
 //
 // The grid is one CTA per SM; each takes item after item (longest first, every second round in
 // reverse order), so the next item's loads and first scores run under the output of the one
-// before.
+// before (window 512, B=8 n=4096: 276 us with a CTA per item, 240 us).
 //
 // The running maximum is allowed to lag: O is rescaled only when a row's maximum has grown by
 // more than 2^8 since the last time (P then stays below 2^8, far inside fp32's and bf16's range),
 // so O rarely leaves TMEM before the end. Key blocks are the two ranges of gm_window.cuh; a block
-// narrower than 64 keys (a few sinks) takes only as many 32-column pieces as it has keys, and
-// pieces that none of a warp's rows sees are skipped.
+// narrower than 128 keys (a few sinks) takes only as many 32-column pieces as it has keys, and
+// pieces that none of a warp's rows sees are skipped. The path of blocks that are seen in part
+// stays a rolled loop: unrolled like the other it costs more in instruction fetches than it saves
+// (225 against 243 us).
 //
 // Rows at or past the sequence's end may hold anything: scores of such keys are masked by
 // selection, and their rows of the V tile are zeroed in shared memory before the MMA (only a
@@ -39,7 +45,7 @@
 
 namespace gm {
 
-constexpr int UW = 128;                 // rows of a tile (keys of a block in the backward)
+constexpr int UW = 128;                 // rows of a tile, keys of a block in the backward
 constexpr int UATOM = UW * 128;         // bytes of one 64-column block of a tile
 constexpr int FK = 128;                 // keys of a block in the forward
 constexpr int FATOM = FK * 128;
@@ -127,11 +133,6 @@ __device__ __forceinline__ Piece key_piece(int r0, int t, int t1, int len, int w
     if (t >= t1 || t > last || (t + 31 <= r0 - window && t >= sinks)) return Piece::none;
     if (t + 31 < t1 && t + 31 <= r0 && r0 + 31 < len && (t > r0 + 31 - window || t + 31 < sinks)) return Piece::all;
     return Piece::some;
-}
-
-__device__ __forceinline__ void named_sync(int id, int count)
-{
-    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
 }
 
 // Whole warp: zeroes rows [first, ROWS) of a ROWS x D tile.

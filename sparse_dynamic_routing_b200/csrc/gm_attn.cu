@@ -282,7 +282,12 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
     a.next = (int *)(ndelta + rows);
     a.part = (float *)((char *)w.delta + p.stats_bytes);
     const unsigned per_seq = (unsigned)(((int64_t)a.npad * w.hq * (D / 8) + 511) / 512);  // blocks of 512 / (D / 8) rows
-    gm::win_stats_kernel<D><<<(unsigned)w.B * per_seq, 256, 0, st>>>(a, gm::FastDiv((uint32_t)w.hq), per_seq, nl, ndelta);
+    // rows that see few keys: all of them, or those at a sequence's start
+    const int few = (int64_t)w.window + w.sinks <= gm::FEW ? w.n : std::min(w.n, gm::FEW);
+    const unsigned few_per_seq = (unsigned)(((int64_t)few * w.hq * (D / 8) + 255) / 256);
+    const unsigned few_blocks = (unsigned)w.B * few_per_seq;
+    gm::win_stats_kernel<D><<<few_blocks + (unsigned)w.B * per_seq, 256, 0, st>>>(
+        a, gm::FastDiv((uint32_t)w.hq), per_seq, few, few_per_seq, few_blocks, nl, ndelta);
     a.items = (int64_t)p.nblk * w.B * w.hq;
     kq<<<(unsigned)std::min<int64_t>(a.items, 148), Geo::THREADS, Geo::SMEM, st>>>(tq, tdo, tk, tv, a);
     a.items = p.items;

@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
     constexpr bool SPLIT = sizeof(T) == 4;
     using Smem = Kv8Smem<D, NT, SPLIT>;
     constexpr int ROWS = Smem::ROWS;
-    constexpr int KS = D / 16;            // k steps of the scores
     constexpr int NK = D / 64;            // 16-byte chunks of a key row per lane
     constexpr int VW = D / 32;            // 4-byte words of a value row per lane
     extern __shared__ __align__(16) unsigned char kv8_smem[];

@@ -114,25 +114,83 @@ template <int D> struct WinBwdGeom {
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
-// nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking two rows so that
-// four 16-byte loads are in flight. A block stays within one sequence, whose rows are contiguous.
-// Also sets both counters to 0. Bound by HBM: o and dout once.
+// -delta of the first `few` rows of a sequence, those that see at most FEW keys.
 //
 // delta = <dout, o> inherits the rounding of o to bf16, an error that reaches dS as P times a
 // constant of the row. Averaged over many keys it is lost in the other roundings, but a row of
-// few keys has o as large as v and dS = P (dP - delta) as a difference of near values. Rows that
-// see at most FEW keys get delta = sum_t P dP instead, from q, k, v and dout.
+// few keys has o as large as v and dS = P (dP - delta) as a difference of near values. Such rows
+// get delta = sum_t P dP from q, k, v and dout (2-norm error of dq at windows of 2 to 8 keys:
+// 0.0034 -> 0.0023, two roundings to bf16 alone give 0.0023). D/8 lanes per row, two keys at a
+// time so that their loads overlap.
 constexpr int FEW = 24;
 
-template <int D> __global__ void __launch_bounds__(256)
-win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, float *nl, float *ndelta)
+template <int D> __device__ __forceinline__ void few_rows(const WinBwdArgs &a, const FastDiv &div_hq, int b,
+                                                          uint32_t y0, int few, float *ndelta)
+{
+    constexpr int C = D / 8, N = 2;
+    const WinArgs &w = a.w;
+    const int c = threadIdx.x % C;
+    const uint32_t y = y0 + threadIdx.x / C;
+    const uint32_t real = (uint32_t)min(win_len(w, b), few) * w.hq;
+    const uint32_t i = div_hq.div(y), hq = y - i * div_hq.d;
+    const size_t row = (size_t)b * w.n * w.hq + y;
+    const bool in = y < real;
+    const int keys = in ? (int)min((int64_t)i + 1, (int64_t)w.window + w.sinks) : 0;
+    const int lo = max((int)i - w.window + 1, 0), ns = min(w.sinks, lo);  // sinks before the window
+    float fq[8], fg[8], sum = 0.0f;
+    unpack<__nv_bfloat16>(in ? ld16((const __nv_bfloat16 *)w.q + row * D + c * 8) : make_uint4(0, 0, 0, 0), fq);
+    unpack<__nv_bfloat16>(in ? ld16((const __nv_bfloat16 *)w.dout + row * D + c * 8) : make_uint4(0, 0, 0, 0), fg);
+    const float nl = in ? -LOG2E * __ldg(w.lse_in + row) : 0.0f;
+    const int most = __reduce_max_sync(FULL, keys);
+    for (int u0 = 0; u0 < most; u0 += N) {
+        uint4 uk[N], uv[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const int u = u0 + e, t = u < ns ? u : lo + u - ns;
+            const size_t at = (((size_t)b * w.n + t) * w.hkv + hq / w.G) * D + c * 8;
+            uk[e] = uv[e] = make_uint4(0, 0, 0, 0);
+            if (u < keys) uk[e] = ld16((const __nv_bfloat16 *)w.k + at), uv[e] = ld16((const __nv_bfloat16 *)w.v + at);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            float fk[8], fv[8];
+            float2 dots = make_float2(0.0f, 0.0f);
+            unpack<__nv_bfloat16>(uk[e], fk);
+            unpack<__nv_bfloat16>(uv[e], fv);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) {
+                dots.x += fq[z] * fk[z];
+                dots.y += fg[z] * fv[z];
+            }
+            dots = seg_sum2<C>(dots);
+            if (u0 + e < keys) sum += ex2_ftz(fmaf(dots.x, w.scale, nl)) * dots.y;
+        }
+    }
+    if (in && c == 0) ndelta[((size_t)b * w.hq + hq) * a.npad + i] = -sum;
+}
+
+// nl and -delta of every row (b, i < npad, hq); D/8 lanes per row, each taking two rows so that
+// four 16-byte loads are in flight. A block stays within one sequence, whose rows are contiguous.
+// Also sets both counters to 0. Bound by HBM: o and dout once (B=8 n=4096, 16 heads: 47 us).
+// The first few_blocks blocks take few_rows, few_per_seq of them per sequence: they start with the
+// others and are bound by latency, so they end within the others' time at large sizes.
+template <int D> __global__ void __launch_bounds__(256, 5)
+win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, int few, unsigned few_per_seq, unsigned few_blocks,
+                 float *nl, float *ndelta)
 {
     if (blockIdx.x == 0 && threadIdx.x < 2) a.next[threadIdx.x] = 0;
     constexpr int C = D / 8, RPB = 256 / C, N = 2;
+    if (blockIdx.x < few_blocks) {
+        const unsigned b = blockIdx.x / few_per_seq;
+        few_rows<D>(a, div_hq, (int)b, (blockIdx.x - b * few_per_seq) * RPB, few, ndelta);
+        return;
+    }
     const WinArgs &w = a.w;
-    const int c = threadIdx.x % C, b = (int)(blockIdx.x / per_seq);
-    const uint32_t y0 = (blockIdx.x - (uint32_t)b * per_seq) * (RPB * N) + threadIdx.x / C;  // row of the sequence
+    const unsigned bx = blockIdx.x - few_blocks;
+    const int c = threadIdx.x % C, b = (int)(bx / per_seq);
+    const uint32_t y0 = (bx - (uint32_t)b * per_seq) * (RPB * N) + threadIdx.x / C;  // row of the sequence
     const uint32_t rows = (uint32_t)a.npad * w.hq, real = (uint32_t)win_len(w, b) * w.hq;
+    const uint32_t skip = min((uint32_t)few * w.hq, real);  // rows that few_rows takes
     const size_t first = (size_t)b * w.n * w.hq;
     uint4 uo[N], ug[N];
     float lse[N];
@@ -141,52 +199,26 @@ win_stats_kernel(WinBwdArgs a, FastDiv div_hq, unsigned per_seq, float *nl, floa
         const uint32_t y = y0 + r * RPB;
         uo[r] = ug[r] = make_uint4(0, 0, 0, 0);
         lse[r] = 0.0f;
-        if (y < real) {
+        if (y >= skip && y < real) {
             uo[r] = ld16_stream((const __nv_bfloat16 *)w.o_in + (first + y) * D + c * 8);
             ug[r] = ld16((const __nv_bfloat16 *)w.dout + (first + y) * D + c * 8);
-            lse[r] = __ldg(w.lse_in + first + y);
         }
+        if (y < real && c == 0) lse[r] = __ldg(w.lse_in + first + y);
     }
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const uint32_t y = y0 + r * RPB, i = div_hq.div(y), hq = y - i * div_hq.d;
-        const float mynl = y < real ? -LOG2E * lse[r] : -INFINITY;
+        const uint32_t y = y0 + r * RPB;
         float fo[8], fg[8], x = 0.0f;
         unpack<__nv_bfloat16>(uo[r], fo);
         unpack<__nv_bfloat16>(ug[r], fg);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x += fo[e] * fg[e];
         x = seg_sum<C>(x);
-        const int64_t seen = min((int64_t)i + 1, (int64_t)w.window + w.sinks);
-        const int keys = y < real && seen <= FEW ? (int)seen : 0;
-        const int most = __reduce_max_sync(FULL, keys);
-        if (most > 0) {
-            float fq[8], sum = 0.0f;
-            const int lo = max((int)i - w.window + 1, 0), ns = min(w.sinks, lo);  // sinks before the window
-            unpack<__nv_bfloat16>(keys ? ld16((const __nv_bfloat16 *)w.q + (first + y) * D + c * 8) : make_uint4(0, 0, 0, 0), fq);
-            for (int u = 0; u < most; ++u) {
-                const int t = u < ns ? u : lo + u - ns;
-                const size_t at = (((size_t)b * w.n + t) * w.hkv + hq / w.G) * D + c * 8;
-                uint4 uk = make_uint4(0, 0, 0, 0), uv = uk;
-                if (u < keys) uk = ld16((const __nv_bfloat16 *)w.k + at), uv = ld16((const __nv_bfloat16 *)w.v + at);
-                float fk[8], fv[8];
-                float2 dots = make_float2(0.0f, 0.0f);
-                unpack<__nv_bfloat16>(uk, fk);
-                unpack<__nv_bfloat16>(uv, fv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dots.x += fq[e] * fk[e];
-                    dots.y += fg[e] * fv[e];
-                }
-                dots = seg_sum2<C>(dots);
-                if (u < keys) sum += ex2_ftz(fmaf(dots.x, w.scale, mynl)) * dots.y;
-            }
-            if (keys) x = sum;
-        }
         if (y < rows && c == 0) {
+            const uint32_t i = div_hq.div(y), hq = y - i * div_hq.d;
             const size_t to = ((size_t)b * w.hq + hq) * a.npad + i;
-            nl[to] = mynl;
-            ndelta[to] = -x;
+            nl[to] = y < real ? -LOG2E * lse[r] : -INFINITY;
+            if (y >= skip) ndelta[to] = -x;
         }
     }
 }

@@ -15,8 +15,10 @@
 // in two halves, so that the first half's products run under the second half's exponentials.
 // With the softmax replaced by nothing the kernel takes 738 us for n = 16384 (16 heads, full), with
 // it 935: the products (at 90 % of the measured bf16 rate when alone) bound it, then the wait for
-// each block's exponentials (16 per SM and cycle). Blocks of 64 keys with two score buffers per
-// tile remove that wait but run the products at N = 64, 976 us alone.
+// each block's exponentials (16 per SM and cycle). A quarter of them therefore runs on the FMA pipe
+// (ex2_poly), in blocks that are seen whole: window 512 224 -> 206 us, n = 16384 1063 -> 1002 us in
+// turn; an eighth gives 223 and 1046, three eighths 206 and 1031. Blocks of 64 keys with two score
+// buffers per tile remove the wait but run the products at N = 64, 976 us alone.
 //
 // The grid is one CTA per SM; each takes item after item (longest first, every second round in
 // reverse order), so the next item's loads and first scores run under the output of the one
@@ -440,14 +442,13 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                 const float nm = m == -INFINITY ? 0.0f : -m;
                 const float2 sl22 = make_float2(sl2, sl2), nm2 = make_float2(nm, nm);
                 float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                // a hidden score is an infinity of the sign that gives 2^-inf = 0
-                const auto exponentials = [&](const uint32_t(&v)[32], uint32_t(&p)[16]) {
+                // a hidden score is an infinity of the sign that gives 2^-inf = 0 (not by ex2_poly)
+                const auto exponentials = [&](const uint32_t(&v)[32], uint32_t(&p)[16], bool all) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float2 x = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                         x = __ffma2_rn(x, sl22, nm2);
-                        x.x = ex2_ftz(x.x);
-                        x.y = ex2_ftz(x.y);
+                        x = all ? ex2_pair<4>(x, e) : ex2_pair<0>(x, e);
                         sum[e & 1] = __fadd2_rn(sum[e & 1], x);
                         p[e] = bf16_pair(x.x, x.y);
                     }
@@ -464,7 +465,7 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                     for (int c = 0; c < 4; ++c) {
                         umma::tmem_wait_ld32(s[c & 1]);
                         if (c < 3) umma::tmem_ld32(ts + (c + 1) * 32, s[(c + 1) & 1]);
-                        exponentials(s[c & 1], p);
+                        exponentials(s[c & 1], p, true);
                         umma::tmem_st16(ts + c * 16, p);
                         if (c & 1) hand_over(c >> 1);
                     }
@@ -474,7 +475,7 @@ win_fwd_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                         if (key_piece(r0, t0 + c * 32, t1, len, a.window, a.sinks) != Piece::none) {
                             umma::tmem_ld32(ts + c * 32, s[0]);
                             umma::tmem_wait_ld32(s[0]);
-                            exponentials(s[0], p);
+                            exponentials(s[0], p, false);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; ++e) p[e] = 0;

@@ -132,6 +132,26 @@ def test_rising_scores(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d,size", [(128, 60.0), (64, 60.0), (128, 0.0), (64, -8.0)])
+def test_scores_far_below_the_maximum(d, size, dtype):
+    """Spreads of many hundred between a row's scores (2^x below the type's range), and none."""
+    run_and_check(1, 600, 2, 1, d, dtype, None, 0, seed=5, size=size)
+    run_and_check(2, 450, 2, 2, d, dtype, 300, 140, lens=[450, 333], seed=6, size=size)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nan_that_is_seen_reaches_its_rows(dtype):
+    """A key of NaN is seen by every later row, in blocks seen whole and in part."""
+    q, k, v, _ = make(9, 1, 520, 2, 1, 128, dtype)
+    for t in range(3, 12):  # whichever way a column's exponential is taken
+        bad = k.clone()
+        bad[:, t] = math.nan
+        o, lse = gm.gm_window_attention_forward(q, bad, v)
+        assert o[:, t:].isnan().all() and lse[:, t:].isnan().all()
+        assert o[:, :t].isfinite().all() and lse[:, :t].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("fill", [math.nan, math.inf])
 def test_padding_may_hold_anything(fill, dtype):
     lens = [100, 37, 0]

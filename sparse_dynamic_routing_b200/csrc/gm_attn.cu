@@ -28,14 +28,17 @@ bool gm_attn_take_errors(unsigned *flag)
 namespace {
 
 // Lets a kernel have `bytes` of dynamic shared memory on the current device; asked of the runtime
-// once per kernel and device.
-template <auto KERNEL> bool raise_smem(size_t bytes)
+// once per kernel and device. A kernel that splits its registers among warpgroups also says how many
+// per thread a launch has to bring: with fewer, warps would wait for registers without end.
+template <auto KERNEL> bool raise_smem(size_t bytes, int regs = 0)
 {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (done.load(std::memory_order_relaxed) & bit) return true;
+    cudaFuncAttributes attr;
+    if (regs > 0 && (cudaFuncGetAttributes(&attr, KERNEL) != cudaSuccess || attr.numRegs < regs)) return false;
     if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
     done.fetch_or(bit, std::memory_order_relaxed);
     return true;
@@ -262,7 +265,7 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
         return GM_ERR_CUDA;
     constexpr auto kq = gm::win_dq_umma_kernel<D>;
     constexpr auto kkv = gm::win_dkv_umma_kernel<D>;
-    if (!raise_smem<kq>(Geo::SMEM) || !raise_smem<kkv>(Geo::SMEM)) return GM_ERR_CUDA;
+    if (!raise_smem<kq>(Geo::SMEM, Geo::REGS) || !raise_smem<kkv>(Geo::SMEM, Geo::REGS)) return GM_ERR_CUDA;
     const WinBwdPlan p = window_backward_plan(w.B, w.n, w.hq, w.hkv, D, w.window, w.sinks);
     gm::WinBwdArgs a{};
     a.w = w;

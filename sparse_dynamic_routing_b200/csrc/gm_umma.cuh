@@ -117,6 +117,11 @@ __device__ __forceinline__ void commit(uint32_t bar)
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 
+// A warpgroup's registers per thread, by all its warps; the others of the SM's share stay with the
+// block, so all warpgroups together may take as many as the launch gave them.
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
 // Whole-warp TMEM allocation of `ncols` columns (a power of two >= 32); the base address is
 // written to shared memory at `slot`.
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols)

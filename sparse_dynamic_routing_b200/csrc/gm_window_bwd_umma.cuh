@@ -112,7 +112,11 @@ template <int D> struct WinBwdGeom {
     static constexpr int NEED = OFF_QUEUE + 16;
     // more than half of the SM's shared memory: a second CTA would wait there for TMEM columns
     static constexpr int SMEM = NEED < 120 * 1024 ? 120 * 1024 : NEED;
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = 384;                // warps 10 and 11 only fill their warpgroup
+    // Registers per thread: at the launch, of warps 8-11, of warps 0-7. At 168 the dq threads spill
+    // (window 512 868 -> 805 us, window 128 567 -> 509 us in turn with the split).
+    static constexpr int REGS = 168, REGS_LOAD = 88, REGS_ELEM = 208;
+    static_assert(REGS_LOAD + 2 * REGS_ELEM <= 3 * REGS, "a split above the launch's registers would wait forever");
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
@@ -399,122 +403,126 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         }
     };
 
-    if (warp == 8) {
-        uint32_t kc = 0, fixes = 0;
-        int qc = 0;
-        bool ok = true;
-        // the first item by position, the others from the counter, asked for one item ahead
-        int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
-        for (;;) {
-            ok = queue.push(item, lane);
-            if (!ok || item >= ba.items) break;
-            const Item w(a, item, per);
-            item = __shfl_sync(FULL, ahead, 0);
-            if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
-            if (w.nt == 0) continue;
-            const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
-#pragma unroll
-                for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
-            };
-            if (lane == 0 && qc > 0) ok = mbar_wait(q_empty, (qc - 1) & 1);
-            ok = __shfl_sync(FULL, ok, 0);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect(q_full, TILE);
-                load(sq, &tmq, w.hq, w.i0, q_full);
-                if (qc > 0) ok = mbar_wait(do_empty, (qc - 1) & 1);
-                mbar_arrive_expect(do_full, TILE);
-                load(sdo, &tmdo, w.hq, w.i0, do_full);
-            }
-            ok = __shfl_sync(FULL, ok, 0);
-            ++qc;
-            for (int j = 0; ok && j < w.nt; ++j, ++kc) {
-                const uint32_t s3 = kc % NK, s2 = kc % NV;
-                const int t0 = w.kb.start(j, UW);
-                if (lane == 0 && kc >= NK) ok = mbar_wait(k_empty + 8 * s3, ((kc / NK) - 1) & 1);
+    if (warp >= 8) {
+        umma::regs_dec<Geo::REGS_LOAD>();
+        if (warp == 8) {
+            uint32_t kc = 0, fixes = 0;
+            int qc = 0;
+            bool ok = true;
+            // the first item by position, the others from the counter, asked for one item ahead
+            int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
+            for (;;) {
+                ok = queue.push(item, lane);
+                if (!ok || item >= ba.items) break;
+                const Item w(a, item, per);
+                item = __shfl_sync(FULL, ahead, 0);
+                if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
+                if (w.nt == 0) continue;
+                const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
+    #pragma unroll
+                    for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
+                };
+                if (lane == 0 && qc > 0) ok = mbar_wait(q_empty, (qc - 1) & 1);
                 ok = __shfl_sync(FULL, ok, 0);
                 if (!ok) break;
-                const bool fix = t0 + UW > w.len && w.len < a.n;  // the last block alone: dQ sums over K's rows
-                const uint32_t bar = fix ? tail : k_full + 8 * s3;
                 if (lane == 0) {
-                    mbar_arrive_expect(bar, TILE);
-                    load(sk + s3 * TILE, &tmk, w.h, t0, bar);
-                }
-                if (fix) {
-                    ok = mbar_wait_warp(tail, fixes++ & 1);
-                    if (ok) zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - t0, 0), lane);
-                    umma::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0 && ok) mbar_arrive(k_full + 8 * s3);
-                }
-                if (lane == 0 && ok && kc >= NV) ok = mbar_wait(v_empty + 8 * s2, ((kc / NV) - 1) & 1);
-                if (lane == 0 && ok) {
-                    mbar_arrive_expect(v_full + 8 * s2, TILE);
-                    load(sv + s2 * TILE, &tmv, w.h, t0, v_full + 8 * s2);
+                    mbar_arrive_expect(q_full, TILE);
+                    load(sq, &tmq, w.hq, w.i0, q_full);
+                    if (qc > 0) ok = mbar_wait(do_empty, (qc - 1) & 1);
+                    mbar_arrive_expect(do_full, TILE);
+                    load(sdo, &tmdo, w.hq, w.i0, do_full);
                 }
                 ok = __shfl_sync(FULL, ok, 0);
-            }
-            if (!ok) break;
-        }
-        if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
-            mbar_wait(q_full, (qc - 1) & 1);
-            mbar_wait(do_full, (qc - 1) & 1);
-            for (uint32_t y = kc > NK ? kc - NK : 0; y < kc; ++y) mbar_wait(k_full + 8 * (y % NK), (y / NK) & 1);
-            for (uint32_t y = kc > NV ? kc - NV : 0; y < kc; ++y) mbar_wait(v_full + 8 * (y % NV), (y / NV) & 1);
-        }
-    } else if (warp == 9) {
-        // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
-        const uint32_t lead = umma::elect_lead();
-        const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), do_lo = umma::sdesc_lo(sdo, umma::KMAJOR);
-        const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), kt_lo = umma::sdesc_lo(sk, UATOM);
-        const uint32_t v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
-        uint32_t kc = 0;
-        int qc = 0;
-        bool ok = true;
-        while (ok) {
-            const int item = queue.pop(lane);
-            if (item < 0 || item >= ba.items) break;
-            const Item w(a, item, per);
-            if (w.nt == 0) continue;
-            const auto width = [&](int j) { return (w.kb.end(j, UW) - w.kb.start(j, UW) + 31) & ~31; };
-            const auto first = [&](int j) {  // S(j), then dP(j)
-                const uint32_t y = kc + j, s3 = y % NK, s2 = y % NV;
-                const int n = width(j);
-                bool ok = mbar_wait_warp(k_full + 8 * s3, (y / NK) & 1);
-                if (ok && y > 0) ok = mbar_wait_warp(s_empty, (y - 1) & 1);
-                if (!ok) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
-                umma::commit_if(lead, s_full);
-                if (j == w.nt - 1) umma::commit_if(lead, q_empty);
-                if (j == 0 && !mbar_wait_warp(do_full, qc & 1)) return false;
-                if (!mbar_wait_warp(v_full + 8 * s2, (y / NV) & 1)) return false;
-                umma::fence_after_sync();
-                mma_tiles<D>(lead, tP + (y & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
-                umma::commit_if(lead, dp_full + 8 * (y & 1));
-                umma::commit_if(lead, v_empty + 8 * s2);
-                if (j == w.nt - 1) umma::commit_if(lead, do_empty);
-                return true;
-            };
-            ok = mbar_wait_warp(q_full, qc & 1) && first(0);
-            for (int j = 0; ok && j < w.nt; ++j) {
-                const uint32_t y = kc + j;
-                if (j + 1 < w.nt) ok = first(j + 1);
-                if (ok && j == 0 && qc > 0) ok = mbar_wait_warp(dq_empty, (qc - 1) & 1);
-                if (ok) ok = mbar_wait_warp(ds_full + 8 * (y & 1), (y >> 1) & 1);
+                ++qc;
+                for (int j = 0; ok && j < w.nt; ++j, ++kc) {
+                    const uint32_t s3 = kc % NK, s2 = kc % NV;
+                    const int t0 = w.kb.start(j, UW);
+                    if (lane == 0 && kc >= NK) ok = mbar_wait(k_empty + 8 * s3, ((kc / NK) - 1) & 1);
+                    ok = __shfl_sync(FULL, ok, 0);
+                    if (!ok) break;
+                    const bool fix = t0 + UW > w.len && w.len < a.n;  // the last block alone: dQ sums over K's rows
+                    const uint32_t bar = fix ? tail : k_full + 8 * s3;
+                    if (lane == 0) {
+                        mbar_arrive_expect(bar, TILE);
+                        load(sk + s3 * TILE, &tmk, w.h, t0, bar);
+                    }
+                    if (fix) {
+                        ok = mbar_wait_warp(tail, fixes++ & 1);
+                        if (ok) zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - t0, 0), lane);
+                        umma::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(k_full + 8 * s3);
+                    }
+                    if (lane == 0 && ok && kc >= NV) ok = mbar_wait(v_empty + 8 * s2, ((kc / NV) - 1) & 1);
+                    if (lane == 0 && ok) {
+                        mbar_arrive_expect(v_full + 8 * s2, TILE);
+                        load(sv + s2 * TILE, &tmv, w.h, t0, v_full + 8 * s2);
+                    }
+                    ok = __shfl_sync(FULL, ok, 0);
+                }
                 if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(lead, tQ, tP + (y & 1) * 128, kt_lo + (y % NK) * (TILE >> 4), width(j), j > 0);
-                umma::commit_if(lead, k_empty + 8 * (y % NK));
             }
-            if (ok) umma::commit_if(lead, dq_full);
-            kc += w.nt;
-            ++qc;
+            if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
+                mbar_wait(q_full, (qc - 1) & 1);
+                mbar_wait(do_full, (qc - 1) & 1);
+                for (uint32_t y = kc > NK ? kc - NK : 0; y < kc; ++y) mbar_wait(k_full + 8 * (y % NK), (y / NK) & 1);
+                for (uint32_t y = kc > NV ? kc - NV : 0; y < kc; ++y) mbar_wait(v_full + 8 * (y % NV), (y / NV) & 1);
+            }
+        } else if (warp == 9) {
+            // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
+            const uint32_t lead = umma::elect_lead();
+            const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), do_lo = umma::sdesc_lo(sdo, umma::KMAJOR);
+            const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), kt_lo = umma::sdesc_lo(sk, UATOM);
+            const uint32_t v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
+            uint32_t kc = 0;
+            int qc = 0;
+            bool ok = true;
+            while (ok) {
+                const int item = queue.pop(lane);
+                if (item < 0 || item >= ba.items) break;
+                const Item w(a, item, per);
+                if (w.nt == 0) continue;
+                const auto width = [&](int j) { return (w.kb.end(j, UW) - w.kb.start(j, UW) + 31) & ~31; };
+                const auto first = [&](int j) {  // S(j), then dP(j)
+                    const uint32_t y = kc + j, s3 = y % NK, s2 = y % NV;
+                    const int n = width(j);
+                    bool ok = mbar_wait_warp(k_full + 8 * s3, (y / NK) & 1);
+                    if (ok && y > 0) ok = mbar_wait_warp(s_empty, (y - 1) & 1);
+                    if (!ok) return false;
+                    umma::fence_after_sync();
+                    mma_tiles<D>(lead, tS, q_lo, k_lo + s3 * (TILE >> 4), n);
+                    umma::commit_if(lead, s_full);
+                    if (j == w.nt - 1) umma::commit_if(lead, q_empty);
+                    if (j == 0 && !mbar_wait_warp(do_full, qc & 1)) return false;
+                    if (!mbar_wait_warp(v_full + 8 * s2, (y / NV) & 1)) return false;
+                    umma::fence_after_sync();
+                    mma_tiles<D>(lead, tP + (y & 1) * 128, do_lo, v_lo + s2 * (TILE >> 4), n);
+                    umma::commit_if(lead, dp_full + 8 * (y & 1));
+                    umma::commit_if(lead, v_empty + 8 * s2);
+                    if (j == w.nt - 1) umma::commit_if(lead, do_empty);
+                    return true;
+                };
+                ok = mbar_wait_warp(q_full, qc & 1) && first(0);
+                for (int j = 0; ok && j < w.nt; ++j) {
+                    const uint32_t y = kc + j;
+                    if (j + 1 < w.nt) ok = first(j + 1);
+                    if (ok && j == 0 && qc > 0) ok = mbar_wait_warp(dq_empty, (qc - 1) & 1);
+                    if (ok) ok = mbar_wait_warp(ds_full + 8 * (y & 1), (y >> 1) & 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    mma_accumulate<D>(lead, tQ, tP + (y & 1) * 128, kt_lo + (y % NK) * (TILE >> 4), width(j), j > 0);
+                    umma::commit_if(lead, k_empty + 8 * (y % NK));
+                }
+                if (ok) umma::commit_if(lead, dq_full);
+                kc += w.nt;
+                ++qc;
+            }
+            // every MMA issued has completed before the CTA releases its tensor memory
+            umma::commit_if(lead, mma_done);
+            mbar_wait_warp(mma_done, 0);
         }
-        // every MMA issued has completed before the CTA releases its tensor memory
-        umma::commit_if(lead, mma_done);
-        mbar_wait_warp(mma_done, 0);
     } else {
+        umma::regs_inc<Geo::REGS_ELEM>();
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
         const float sl2 = a.scale;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -681,131 +689,135 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
     const uint32_t tmem = *tslot_p;
     const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 256 + D;
 
-    if (warp == 8) {
-        uint32_t kc = 0, fixes = 0;  // steps so far
-        int qc = 0;                  // items with steps so far
-        bool ok = true;
-        // the first item by position, the others from the counter, asked for one item ahead
-        int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
-        for (;;) {
-            ok = queue.push(item, lane);
-            if (!ok || item >= ba.items) break;
-            const DkvItem w(ba, item);
-            item = __shfl_sync(FULL, ahead, 0);
-            if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
-            if (w.j1 <= w.j0) continue;
-            const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
-#pragma unroll
-                for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
-            };
-            if (lane == 0 && qc > 0) ok = mbar_wait(kv_empty, (qc - 1) & 1);
-            ok = __shfl_sync(FULL, ok, 0);
-            if (!ok) break;
-            if (lane == 0) {
-                mbar_arrive_expect(kv_full, 2 * TILE);
-                load(sk, &tmk, w.h, w.t0, kv_full);
-                load(sv, &tmv, w.h, w.t0, kv_full);
-            }
-            ++qc;
-            for (int j = w.j0; ok && j < w.j1; ++j, ++kc) {
-                const uint32_t s3 = kc % NQ, s2 = kc % ND;
-                const int g = j / w.nq, i0 = w.t0 + (j - g * w.nq) * UW, hq = w.h * a.G + g;
-                const float *nl = ba.nl + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
-                const float *dl = ba.ndelta + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
-                const bool fix = i0 + UW > w.len && w.len < a.n;  // dK and dV sum over these rows
-                if (lane == 0 && kc >= NQ) ok = mbar_wait(q_empty + 8 * s3, ((kc / NQ) - 1) & 1);
-                if (lane == 0 && ok && kc >= ND) ok = mbar_wait(do_empty + 8 * s2, ((kc / ND) - 1) & 1);
+    if (warp >= 8) {
+        umma::regs_dec<Geo::REGS_LOAD>();
+        if (warp == 8) {
+            uint32_t kc = 0, fixes = 0;  // steps so far
+            int qc = 0;                  // items with steps so far
+            bool ok = true;
+            // the first item by position, the others from the counter, asked for one item ahead
+            int item = (int)blockIdx.x, ahead = lane == 0 ? (int)gridDim.x + atomicAdd(ba.next, 1) : 0;
+            for (;;) {
+                ok = queue.push(item, lane);
+                if (!ok || item >= ba.items) break;
+                const DkvItem w(ba, item);
+                item = __shfl_sync(FULL, ahead, 0);
+                if (lane == 0) ahead = (int)gridDim.x + atomicAdd(ba.next, 1);
+                if (w.j1 <= w.j0) continue;
+                const auto load = [&](uint32_t dst, const CUtensorMap *m, int head, int row, uint32_t bar) {
+    #pragma unroll
+                    for (int at = 0; at < NA; ++at) umma::tma_load_4d(dst + at * UATOM, m, at * 64, head, row, w.b, bar);
+                };
+                if (lane == 0 && qc > 0) ok = mbar_wait(kv_empty, (qc - 1) & 1);
                 ok = __shfl_sync(FULL, ok, 0);
                 if (!ok) break;
                 if (lane == 0) {
-                    const uint32_t bq = fix ? tail : q_full + 8 * s3, bd = fix ? tail : do_full + 8 * s2;
+                    mbar_arrive_expect(kv_full, 2 * TILE);
+                    load(sk, &tmk, w.h, w.t0, kv_full);
+                    load(sv, &tmv, w.h, w.t0, kv_full);
+                }
+                ++qc;
+                for (int j = w.j0; ok && j < w.j1; ++j, ++kc) {
+                    const uint32_t s3 = kc % NQ, s2 = kc % ND;
+                    const int g = j / w.nq, i0 = w.t0 + (j - g * w.nq) * UW, hq = w.h * a.G + g;
+                    const float *nl = ba.nl + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
+                    const float *dl = ba.ndelta + ((size_t)w.b * a.hq + hq) * ba.npad + i0;
+                    const bool fix = i0 + UW > w.len && w.len < a.n;  // dK and dV sum over these rows
+                    if (lane == 0 && kc >= NQ) ok = mbar_wait(q_empty + 8 * s3, ((kc / NQ) - 1) & 1);
+                    if (lane == 0 && ok && kc >= ND) ok = mbar_wait(do_empty + 8 * s2, ((kc / ND) - 1) & 1);
+                    ok = __shfl_sync(FULL, ok, 0);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        const uint32_t bq = fix ? tail : q_full + 8 * s3, bd = fix ? tail : do_full + 8 * s2;
+                        if (fix) {
+                            mbar_arrive_expect(tail, 2 * (TILE + 512));
+                        } else {
+                            mbar_arrive_expect(bq, TILE + 512);
+                            mbar_arrive_expect(bd, TILE + 512);
+                        }
+                        load(sq + s3 * TILE, &tmq, hq, i0, bq);
+                        bulk_load(base + Geo::OFF_NL + s3 * 512, nl, 512, bq);
+                        load(sdo + s2 * TILE, &tmdo, hq, i0, bd);
+                        bulk_load(base + Geo::OFF_DELTA + s2 * 512, dl, 512, bd);
+                    }
                     if (fix) {
-                        mbar_arrive_expect(tail, 2 * (TILE + 512));
-                    } else {
-                        mbar_arrive_expect(bq, TILE + 512);
-                        mbar_arrive_expect(bd, TILE + 512);
-                    }
-                    load(sq + s3 * TILE, &tmq, hq, i0, bq);
-                    bulk_load(base + Geo::OFF_NL + s3 * 512, nl, 512, bq);
-                    load(sdo + s2 * TILE, &tmdo, hq, i0, bd);
-                    bulk_load(base + Geo::OFF_DELTA + s2 * 512, dl, 512, bd);
-                }
-                if (fix) {
-                    ok = mbar_wait_warp(tail, fixes++ & 1);
-                    if (ok) {
-                        zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - i0, 0), lane);
-                        zero_rows<NA, UW>(sm + Geo::OFF_2 + s2 * TILE, max(w.len - i0, 0), lane);
-                    }
-                    umma::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0 && ok) {
-                        mbar_arrive(q_full + 8 * s3);
-                        mbar_arrive(do_full + 8 * s2);
+                        ok = mbar_wait_warp(tail, fixes++ & 1);
+                        if (ok) {
+                            zero_rows<NA, UW>(sm + Geo::OFF_3 + s3 * TILE, max(w.len - i0, 0), lane);
+                            zero_rows<NA, UW>(sm + Geo::OFF_2 + s2 * TILE, max(w.len - i0, 0), lane);
+                        }
+                        umma::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0 && ok) {
+                            mbar_arrive(q_full + 8 * s3);
+                            mbar_arrive(do_full + 8 * s2);
+                        }
                     }
                 }
-            }
-            if (!ok) break;
-        }
-        if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
-            mbar_wait(kv_full, (qc - 1) & 1);
-            for (uint32_t y = kc > NQ ? kc - NQ : 0; y < kc; ++y) mbar_wait(q_full + 8 * (y % NQ), (y / NQ) & 1);
-            for (uint32_t y = kc > ND ? kc - ND : 0; y < kc; ++y) mbar_wait(do_full + 8 * (y % ND), (y / ND) & 1);
-        }
-    } else if (warp == 9) {
-        // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
-        const uint32_t lead = umma::elect_lead();
-        const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
-        const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), qt_lo = umma::sdesc_lo(sq, UATOM);
-        const uint32_t do_lo = umma::sdesc_lo(sdo, umma::KMAJOR), dot_lo = umma::sdesc_lo(sdo, UATOM);
-        const auto scores = [&](uint32_t y) {
-            if (!mbar_wait_warp(q_full + 8 * (y % NQ), (y / NQ) & 1)) return false;
-            umma::fence_after_sync();
-            mma_tiles<D>(lead, tS, k_lo, q_lo + (y % NQ) * (TILE >> 4), UW);
-            umma::commit_if(lead, s_full);
-            return true;
-        };
-        const auto dps = [&](uint32_t y, bool last) {
-            if (!mbar_wait_warp(do_full + 8 * (y % ND), (y / ND) & 1)) return false;
-            umma::fence_after_sync();
-            mma_tiles<D>(lead, tP, v_lo, do_lo + (y % ND) * (TILE >> 4), UW);
-            umma::commit_if(lead, dp_full);
-            if (last) umma::commit_if(lead, kv_empty);
-            return true;
-        };
-        uint32_t kc = 0;
-        int qc = 0;
-        bool ok = true;
-        while (ok) {
-            const int item = queue.pop(lane);
-            if (item < 0 || item >= ba.items) break;
-            const DkvItem w(ba, item);
-            const int nt = w.j1 - w.j0;
-            if (nt <= 0) continue;
-            ok = mbar_wait_warp(kv_full, qc & 1) && scores(kc) && dps(kc, nt == 1);
-            for (int j = 0; ok && j < nt; ++j) {
-                const uint32_t y = kc + j;
-                if (j == 0 && qc > 0) ok = mbar_wait_warp(acc_empty, (qc - 1) & 1);
-                if (ok) ok = mbar_wait_warp(p_full, y & 1);
                 if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(lead, tV, tS, dot_lo + (y % ND) * (TILE >> 4), UW, j > 0);
-                if (j + 1 < nt) ok = scores(y + 1);
-                if (ok) ok = mbar_wait_warp(ds_full, y & 1);
-                if (!ok) break;
-                umma::fence_after_sync();
-                mma_accumulate<D>(lead, tK, tP, qt_lo + (y % NQ) * (TILE >> 4), UW, j > 0);
-                umma::commit_if(lead, q_empty + 8 * (y % NQ));
-                umma::commit_if(lead, do_empty + 8 * (y % ND));
-                if (j + 1 < nt) ok = dps(y + 1, j + 2 == nt);
             }
-            if (ok) umma::commit_if(lead, acc_full);
-            kc += nt;
-            ++qc;
+            if (lane == 0 && !ok && qc > 0) {  // gave up: copies in flight land before the CTA ends (bounded)
+                mbar_wait(kv_full, (qc - 1) & 1);
+                for (uint32_t y = kc > NQ ? kc - NQ : 0; y < kc; ++y) mbar_wait(q_full + 8 * (y % NQ), (y / NQ) & 1);
+                for (uint32_t y = kc > ND ? kc - ND : 0; y < kc; ++y) mbar_wait(do_full + 8 * (y % ND), (y / ND) & 1);
+            }
+        } else if (warp == 9) {
+            // ---- MMAs (the whole warp runs along, one lane issues) ----------------------------
+            const uint32_t lead = umma::elect_lead();
+            const uint32_t k_lo = umma::sdesc_lo(sk, umma::KMAJOR), v_lo = umma::sdesc_lo(sv, umma::KMAJOR);
+            const uint32_t q_lo = umma::sdesc_lo(sq, umma::KMAJOR), qt_lo = umma::sdesc_lo(sq, UATOM);
+            const uint32_t do_lo = umma::sdesc_lo(sdo, umma::KMAJOR), dot_lo = umma::sdesc_lo(sdo, UATOM);
+            const auto scores = [&](uint32_t y) {
+                if (!mbar_wait_warp(q_full + 8 * (y % NQ), (y / NQ) & 1)) return false;
+                umma::fence_after_sync();
+                mma_tiles<D>(lead, tS, k_lo, q_lo + (y % NQ) * (TILE >> 4), UW);
+                umma::commit_if(lead, s_full);
+                return true;
+            };
+            const auto dps = [&](uint32_t y, bool last) {
+                if (!mbar_wait_warp(do_full + 8 * (y % ND), (y / ND) & 1)) return false;
+                umma::fence_after_sync();
+                mma_tiles<D>(lead, tP, v_lo, do_lo + (y % ND) * (TILE >> 4), UW);
+                umma::commit_if(lead, dp_full);
+                if (last) umma::commit_if(lead, kv_empty);
+                return true;
+            };
+            uint32_t kc = 0;
+            int qc = 0;
+            bool ok = true;
+            while (ok) {
+                const int item = queue.pop(lane);
+                if (item < 0 || item >= ba.items) break;
+                const DkvItem w(ba, item);
+                const int nt = w.j1 - w.j0;
+                if (nt <= 0) continue;
+                ok = mbar_wait_warp(kv_full, qc & 1) && scores(kc) && dps(kc, nt == 1);
+                for (int j = 0; ok && j < nt; ++j) {
+                    const uint32_t y = kc + j;
+                    if (j == 0 && qc > 0) ok = mbar_wait_warp(acc_empty, (qc - 1) & 1);
+                    if (ok) ok = mbar_wait_warp(p_full, y & 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    mma_accumulate<D>(lead, tV, tS, dot_lo + (y % ND) * (TILE >> 4), UW, j > 0);
+                    if (j + 1 < nt) ok = scores(y + 1);
+                    if (ok) ok = mbar_wait_warp(ds_full, y & 1);
+                    if (!ok) break;
+                    umma::fence_after_sync();
+                    mma_accumulate<D>(lead, tK, tP, qt_lo + (y % NQ) * (TILE >> 4), UW, j > 0);
+                    umma::commit_if(lead, q_empty + 8 * (y % NQ));
+                    umma::commit_if(lead, do_empty + 8 * (y % ND));
+                    if (j + 1 < nt) ok = dps(y + 1, j + 2 == nt);
+                }
+                if (ok) umma::commit_if(lead, acc_full);
+                kc += nt;
+                ++qc;
+            }
+            // every MMA issued has completed before the CTA releases its tensor memory
+            umma::commit_if(lead, mma_done);
+            mbar_wait_warp(mma_done, 0);
         }
-        // every MMA issued has completed before the CTA releases its tensor memory
-        umma::commit_if(lead, mma_done);
-        mbar_wait_warp(mma_done, 0);
     } else {
+        umma::regs_inc<Geo::REGS_ELEM>();
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
         const float sl2 = a.scale;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;

@@ -582,23 +582,20 @@ win_dq_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
                 if (!ok) break;
                 umma::fence_after_sync();
                 const uint32_t tp = tP + (y & 1) * 128 + lane_off + c0;
-                uint32_t d[2][32];
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (piece[c] != Piece::none) umma::tmem_ld32(tp + c * 32, d[c]);
-                umma::tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t x[16];
+                    uint32_t x[16], d[32];
                     if (piece[c] == Piece::none) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) x[e] = 0u;
                     } else {
+                        umma::tmem_ld32(tp + c * 32, d);
+                        umma::tmem_wait_ld32(d);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float2 p = make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1]));
                             const float2 z = __fmul2_rn(
-                                p, __fadd2_rn(make_float2(__uint_as_float(d[c][2 * e]), __uint_as_float(d[c][2 * e + 1])),
+                                p, __fadd2_rn(make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])),
                                               make_float2(dl, dl)));
                             x[e] = bf16_pair(z.x, z.y);
                         }
@@ -847,11 +844,12 @@ win_dkv_umma_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_consta
                 for (int c = 0; c < 2; ++c) {
                     piece[c] = whole ? Piece::all : query_piece(t0 + (warp & 3) * 32, i0 + c0 + c * 32, len, a.window, a.sinks);
                     mask[c] = piece[c] == Piece::some ? column_mask(c0 + c * 32, t - i0, last - i0, 0) : 0u;
-                    if (piece[c] != Piece::none) umma::tmem_ld32(tS + lane_off + c0 + c * 32, s[c]);
                 }
-                umma::tmem_wait_ld();
+                if (piece[0] != Piece::none) umma::tmem_ld32(tS + lane_off + c0, s[0]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    umma::tmem_wait_ld32(s[c]);
+                    if (c == 0 && piece[1] != Piece::none) umma::tmem_ld32(tS + lane_off + c0 + 32, s[1]);
                     uint32_t x[16];
                     if (piece[c] == Piece::none) {
 #pragma unroll

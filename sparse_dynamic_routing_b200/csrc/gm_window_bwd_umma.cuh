@@ -23,6 +23,14 @@
 // the exponentials runs on the FMA pipe (n = 16384 3661 -> 3547 us, window 1024 1266 -> 1254 us in
 // turn; three sixteenths 3609, 1262).
 //
+// The threads read scores and dP from TMEM 32 columns at a time, the next under the arithmetic of the
+// one before (window 1024 1207 -> 1163 us in turn; all 64 at once need fewer waits but hold every
+// warp at the same place).
+//
+// B=8 n=4096, 16/8 heads, d=128: window 512 800 us, window 1024 1150 us; B=1 n=16384 full 3440 us
+// (at the power limit). The tensor pipe is busy half of the time (dq 50 %): a step's products wait for its
+// elements and the other way round, at one CTA per SM.
+//
 // Both kernels run one CTA per SM, which takes item after item from a counter in the workspace
 // (items differ in length, by the mask and by the sequences): the loads, S and dP of the next item
 // start under the last elements and the output of the one before. Output rows go from registers to

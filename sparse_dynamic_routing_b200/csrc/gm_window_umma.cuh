@@ -23,7 +23,13 @@
 //
 // The grid is one CTA per SM; each takes item after item (longest first, every second round in
 // reverse order), so the next item's loads and first scores run under the output of the one
-// before (window 512, B=8 n=4096: 276 us with a CTA per item, 240 us).
+// before (window 512, B=8 n=4096: 276 us with a CTA per item, 240 us at that time).
+//
+// B=8 n=4096, 16/8 heads, d=128: window 512 206 us, window 1024 305 us; B=1 n=16384 full 997 us
+// (1.1 PFLOP/s, at the power limit). At window 1024 the tensor pipe is busy 47 % of the time, the
+// exponential unit 34 %, the issue slots 38 %: what is left is the chain scores - maximum -
+// exponentials - product of one tile, which the other tile covers only in part, and the blocks seen
+// in part at both ends of a window.
 //
 // The running maximum is allowed to lag: O is rescaled only when a row's maximum has grown by
 // more than 2^8 since the last time (P then stays below 2^8, far inside fp32's and bf16's range),

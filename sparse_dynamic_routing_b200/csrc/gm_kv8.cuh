@@ -474,8 +474,9 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
         ids[1] = raw_page(2 * (u + 2 * stride) + 1);
         cp_async_wait<1>();
         __syncwarp();  // the unit is complete
-        // a second piece past the end starts where nothing is seen
-        const int t0[2] = {piece(2 * u) << 4, 2 * u + 1 < np ? piece(2 * u + 1) << 4 : 0x3fffffff};
+        // a second piece past the end starts past every position (max_pages * page < 2^31, so a
+        // sequence's last one is at most 2^31 - 17), where nothing is seen; its 16 rows stay within 32 bits
+        const int t0[2] = {piece(2 * u) << 4, 2 * u + 1 < np ? piece(2 * u + 1) << 4 : 0x7ffffff0};
         const float kf[2] = {sm.scales[warp][st][0][0], sm.scales[warp][st][1][0]};
         const float vf[2] = {sm.scales[warp][st][0][1], sm.scales[warp][st][1][1]};
         // S^T = K q^T
@@ -595,7 +596,7 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
                     vr[y][0] = x.x, vr[y][1] = x.y;
                 }
             }
-            if (t0[p] + 16 > len) {  // rows past the sequence's end may hold any bytes, NaN among them
+            if (t0[p] > len - 16) {  // rows past the sequence's end may hold any bytes, NaN among them
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     if (t0[p] + 2 * c + (y & 1) + 8 * (y >> 1) >= len) {

@@ -311,6 +311,12 @@ __device__ __forceinline__ void kv8_store_row(const Kv8AttnArgs &a, size_t row, 
     if (a.lse && d == 0) a.lse[row] = none ? -INFINITY : (mx + lg2(sum)) * LN2;
 }
 
+// A weight 2^(s - m) is multiplied by vf 2^(m - mv) 2^14 (vf: the value scale, m: the row's largest
+// score, mv: the largest of score + log2 vf). While vf 2^(m - mv) is at most 2^KV8_FAR that product is
+// taken as it stands: the factor is far inside fp32's range, and a weight that is flushed below 2^-126
+// would have been below 2^-48 of fp16's 2^14. A block of zeros (vf = 2^-100) that holds the largest
+// score, beside one of large values, has factors past fp32's range.
+constexpr float KV8_FAR = 64.0f;
 constexpr int KV8_W = 4;       // warps per block
 constexpr int KV8_PER_SM = 3;  // blocks per SM (shared memory: the rings)
 
@@ -525,8 +531,8 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
         uint32_t pt[2][NT][2], pl[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float mb[2], up[2][2], f[2];
-            bool see[2][4], moved = false;
+            float mb[2], vb[2], up[2][2], f[2];
+            bool see[2][4], moved = false, far = false;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -544,25 +550,44 @@ __global__ void __launch_bounds__(KV8_W * 32, KV8_PER_SM) kv8_attention_kernel(K
                     m1 = fmaxf(m1, __shfl_xor_sync(FULL, m1, sft));
                 }
                 const float mn = fmaxf(m[n][e], fmaxf(m0, m1)), vn = fmaxf(mv[n][e], fmaxf(m0 + lv[0], m1 + lv[1]));
-                const float vb = vn == -INFINITY ? 0.0f : vn;
+                vb[e] = vn == -INFINITY ? 0.0f : vn;
                 mb[e] = mn == -INFINITY ? 0.0f : mn;
                 l[n][e] *= ex2_ftz(m[n][e] - mb[e]);
-                f[e] = ex2_ftz(mv[n][e] - vb);
+                f[e] = ex2_ftz(mv[n][e] - vb[e]);
                 moved |= vn != mv[n][e];
+                far |= fmaxf(lv[0], lv[1]) + (mb[e] - vb[e]) > KV8_FAR;
                 m[n][e] = mn;
                 mv[n][e] = vn;
-                const float x = ex2_ftz(mb[e] - vb) * 0x1p14f;
+                const float x = ex2_ftz(mb[e] - vb[e]) * 0x1p14f;
                 up[0][e] = vf[0] * x;
                 up[1][e] = vf[1] * x;
             }
+            if (__any_sync(FULL, far)) {
+                // a factor that could overflow gives up 2^over to the exponential it multiplies, which
+                // is then at most 2^-KV8_FAR: s + lv <= vb for every key that is seen
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = see[p][e] ? ex2_ftz(s[p][n][e] - mb[e & 1]) : 0.0f;
-                    l[n][e & 1] += x;
-                    s[p][n][e] = see[p][e] ? x * up[p][e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const float over = fmaxf(lv[p] + (mb[e] - vb[e]) - KV8_FAR, 0.0f);
+                        up[p][e] = vf[p] * (ex2_ftz(mb[e] - vb[e] - over) * 0x1p14f);
+#pragma unroll
+                        for (int y = 0; y < 4; y += 2) {
+                            const float x = s[p][n][e + y] - mb[e];
+                            l[n][e] += see[p][e + y] ? ex2_ftz(x) : 0.0f;
+                            s[p][n][e + y] = see[p][e + y] ? ex2_ftz(x + over) * up[p][e] : 0.0f;
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = see[p][e] ? ex2_ftz(s[p][n][e] - mb[e & 1]) : 0.0f;
+                        l[n][e & 1] += x;
+                        s[p][n][e] = see[p][e] ? x * up[p][e & 1] : 0.0f;  // a NaN scale reaches only rows that see its block
+                    }
+            }
             if (__any_sync(FULL, moved)) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)

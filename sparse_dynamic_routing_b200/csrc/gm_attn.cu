@@ -306,16 +306,26 @@ template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream
 
 // ---- 8-bit cache -----------------------------------------------------------------------------------
 
+// The sizes of a call over the cache, without its pool.
+gm_status check_cache_sizes(int B, int t, int heads, int hkv, int d, int page, int max_pages)
+{
+    if (B < 0 || t < 0 || heads < 1 || hkv < 1 || d < 1 || heads % hkv != 0) return GM_ERR_INVALID_ARG;
+    if (max_pages < 0 || page < 1) return GM_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
+    if (page != 16 && page != 32 && page != 64 && page != 128) return GM_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    // two factors at a time: B * t * heads alone can pass 64 bits
+    if ((int64_t)B * t >= MAX_ROWS || (int64_t)B * t * heads >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    return GM_OK;
+}
+
 gm_status check_cache(gm::Kv8 &c, void *kq, void *vq, float *kscale, float *vscale, int num_pages, int page,
                       const int32_t *table, int max_pages, const int32_t *lens, int B, int t, int heads, int hkv, int d,
                       gm_dtype dtype)
 {
-    if (B < 0 || t < 0 || heads < 1 || hkv < 1 || d < 1 || heads % hkv != 0) return GM_ERR_INVALID_ARG;
-    if (num_pages < 0 || max_pages < 0 || page < 1) return GM_ERR_INVALID_ARG;
-    if (dtype != GM_F32 && dtype != GM_BF16) return GM_ERR_INVALID_ARG;
-    if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
-    if (page != 16 && page != 32 && page != 64 && page != 128) return GM_ERR_UNSUPPORTED;
-    if ((int64_t)max_pages * page >= MAX_ROWS || (int64_t)B * t * heads >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
+    if (num_pages < 0 || (dtype != GM_F32 && dtype != GM_BF16)) return GM_ERR_INVALID_ARG;
+    const gm_status sizes = check_cache_sizes(B, t, heads, hkv, d, page, max_pages);
+    if (sizes != GM_OK) return sizes;
     // pool rows are counted in 32 bits (2^32 of them are 256 GB and more)
     if ((int64_t)num_pages * hkv >= ((int64_t)1 << 32) / page) return GM_ERR_UNSUPPORTED;
     if ((int64_t)B * t == 0) return GM_OK;
@@ -515,8 +525,7 @@ gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int
 
 size_t gm_kv8_attention_workspace_size(int B, int t, int hq, int hkv, int d, int page, int max_pages, int window, int sinks)
 {
-    if (B < 1 || t < 1 || hkv < 1 || hq < hkv || hq % hkv != 0 || d < 1 || page < 1 || max_pages < 0 || window < 1 || sinks < 0)
-        return 0;
+    if (check_cache_sizes(B, t, hq, hkv, d, page, max_pages) != GM_OK || (int64_t)B * t == 0 || window < 1 || sinks < 0) return 0;
     return kv8_plan(B, t, hq, hkv, d, kv8_keys((int64_t)max_pages * page, window, sinks, t)).bytes;
 }
 

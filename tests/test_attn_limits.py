@@ -1,0 +1,60 @@
+"""Sizes at the edge of 32 and 64 bits at the C boundary of the windowed-attention and 8-bit-cache calls,
+without a GPU. Each probe runs in a process of its own, so that a call that ends the process shows as
+a failed test; a misaligned output keeps every accepted-looking call from launching anything."""
+import ast
+import os
+import subprocess
+import sys
+
+import pytest
+
+from sparse_dynamic_routing_b200 import _binding as bnd
+from sparse_dynamic_routing_b200 import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BIG = 2 ** 31 - 1
+PROBE = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import test_attn_abi as A
+from sparse_dynamic_routing_b200 import _binding as bnd
+lib = bnd.load_library()
+print("RESULT", [{calls}])
+"""
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    build.build()
+
+
+def probe(*calls):
+    """The values of these expressions in a process of its own (lib: the library, A: test_attn_abi)."""
+    run = subprocess.run([sys.executable, "-c", PROBE.format(root=ROOT, calls=", ".join(calls))], capture_output=True,
+                         text=True, timeout=300)
+    assert run.returncode == 0, f"{calls}: the process ended with {run.returncode}: {run.stderr[-500:]}"
+    return ast.literal_eval(run.stdout.split("RESULT", 1)[1].strip())
+
+
+HUGE = [dict(B=2 ** 30, t=2 ** 30, hq=2 ** 30, hkv=2 ** 30), dict(B=2 ** 30, t=2 ** 30, hq=2 ** 4, hkv=2 ** 4),
+        dict(B=BIG, t=BIG, hq=BIG, hkv=BIG), dict(B=BIG, t=BIG, hq=BIG, hkv=1), dict(B=2 ** 16, t=2 ** 16, hq=1, hkv=1),
+        dict(B=2 ** 15, t=2 ** 15, hq=2, hkv=1)]
+
+
+def test_products_of_sizes_past_64_bits_are_refused():
+    calls = []
+    for sizes in HUGE:
+        kw = ", ".join(f"{k}={v}" for k, v in sizes.items())
+        calls += [f"A.attention(lib, {kw})", f"A.sea(lib, {kw})",
+                  f"A.append(lib, B={sizes['B']}, t={sizes['t']}, hkv={sizes['hq']})"]
+    assert probe(*calls) == [bnd.GM_ERR_UNSUPPORTED] * len(calls)
+
+
+def test_workspace_size_of_a_shape_that_is_not_taken():
+    """0, as for every shape the call does not take."""
+    size = "lib.gm_kv8_attention_workspace_size"
+    calls = [f"{size}({s['B']}, {s['t']}, {s['hq']}, {s['hkv']}, 64, 64, 1024, {BIG}, {BIG})" for s in HUGE]
+    calls += [f"{size}(1, 1, 16, 8, {d}, {page}, {pages}, {BIG}, 0)"
+              for d, page, pages in ((96, 64, 1024), (128, 24, 1024), (128, 64, 2 ** 25))]
+    assert probe(*calls) == [0] * len(calls)
+    assert probe(f"{size}(1, 1, 16, 8, 128, 64, {2 ** 25 - 1}, {BIG}, {BIG})")[0] > 0

@@ -550,7 +550,8 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
  *   workspace    device scratch owned by the caller, 16-byte aligned, at least
  *                gm_window_attention_backward_workspace_size(...) bytes; its contents do not
  *                matter and are garbage on return. Calls that overlap on the GPU need one each
- *   limits       as the forward; every pointer 16-byte aligned except lens and lse
+ *   limits       as the forward; every pointer 16-byte aligned except lens and lse. For GM_BF16,
+ *                with n rounded up to a multiple of 128: n * hq < 2^31, B * n * hq < 2^36
  * For GM_BF16, P and dz are rounded to bf16 before their products. A row that sees one key has
  * exactly dz = 0; rows of at most 24 keys take delta from sum_t P_t <dout, v_t>, which does not
  * carry the rounding of o. Deterministic.

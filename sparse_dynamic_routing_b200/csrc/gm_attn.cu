@@ -256,6 +256,14 @@ WinBwdPlan window_backward_plan(int B, int n, int hq, int hkv, int d, int window
     return p;
 }
 
+// Whether the bf16 backward takes the shape: its statistics pass counts the padded rows of a sequence in
+// 32 bits and takes 32 or more of them per block, its items are counted in 32 bits.
+bool window_backward_fits(gm_dtype dtype, int B, int n, int hq)
+{
+    const int64_t rows = ((int64_t)n + gm::UW - 1) / gm::UW * gm::UW * hq;
+    return dtype != GM_BF16 || (rows < MAX_ROWS && B * rows < (int64_t)1 << 36);
+}
+
 template <int D> gm_status window_backward_bf16(const gm::WinArgs &w, cudaStream_t st)
 {
     using Geo = gm::WinBwdGeom<D>;
@@ -468,6 +476,7 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
 size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n, int hq, int hkv, int d, int window, int sinks)
 {
     if (check_window(dtype, B, n, hq, hkv, d, window, sinks, 1.0f) != GM_OK || (int64_t)B * n == 0) return 0;
+    if (!window_backward_fits(dtype, B, n, hq)) return 0;
     if (dtype == GM_F32) return window_f32_plan(B, n, hq, hkv, d, window, sinks).bytes;
     return window_backward_plan(B, n, hq, hkv, d, window, sinks).bytes;
 }
@@ -479,6 +488,7 @@ gm_status gm_window_attention_backward(const void *q, const void *k, const void 
 {
     const gm_status st = check_window(dtype, B, n, hq, hkv, d, window, sinks, scale);
     if (st != GM_OK || (int64_t)B * n == 0) return st;
+    if (!window_backward_fits(dtype, B, n, hq)) return GM_ERR_UNSUPPORTED;
     if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !workspace) return GM_ERR_INVALID_ARG;
     for (const void *p : {q, k, v, o, dout, (const void *)dq, (const void *)dk, (const void *)dv, (const void *)workspace})
         if (!aligned16(p)) return GM_ERR_INVALID_ARG;

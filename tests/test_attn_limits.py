@@ -56,5 +56,22 @@ def test_workspace_size_of_a_shape_that_is_not_taken():
     calls = [f"{size}({s['B']}, {s['t']}, {s['hq']}, {s['hkv']}, 64, 64, 1024, {BIG}, {BIG})" for s in HUGE]
     calls += [f"{size}(1, 1, 16, 8, {d}, {page}, {pages}, {BIG}, 0)"
               for d, page, pages in ((96, 64, 1024), (128, 24, 1024), (128, 64, 2 ** 25))]
-    assert probe(*calls) == [0] * len(calls)
-    assert probe(f"{size}(1, 1, 16, 8, 128, 64, {2 ** 25 - 1}, {BIG}, {BIG})")[0] > 0
+    *none, most = probe(*calls, f"{size}(1, 1, 16, 8, 128, 64, {2 ** 25 - 1}, {BIG}, {BIG})")
+    assert none == [0] * len(calls) and most > 0
+
+
+def test_padded_rows_of_the_bf16_backward_are_counted():
+    """Sequences of few tokens and very many heads: rows are padded to 128 per head there."""
+    size = "lib.gm_window_attention_backward_workspace_size"
+    shapes = ((1, 1, 2 ** 24), (1, 129, 2 ** 23), (1, 100, 2 ** 24), (2 ** 30, 1, 1))
+    calls = []
+    for B, n, hq in shapes:
+        calls += [f"A.backward(lib, B={B}, n={n}, hq={hq}, hkv=1)", f"{size}({bnd.GM_BF16}, {B}, {n}, {hq}, 1, 64, 1, 0)",
+                  f"A.backward(lib, B={B}, n={n}, hq={hq}, hkv=1, dtype={bnd.GM_F32})",
+                  f"{size}({bnd.GM_F32}, {B}, {n}, {hq}, 1, 64, 1, 0)", f"A.forward(lib, B={B}, n={n}, hq={hq}, hkv=1)"]
+    got = probe(*calls, f"{size}({bnd.GM_BF16}, 1, 1, {2 ** 24 - 1}, 1, 64, 1, 0)")
+    for x, shape in enumerate(shapes):
+        bf16, need, f32, need32, forward = got[5 * x: 5 * x + 5]
+        assert (bf16, need) == (bnd.GM_ERR_UNSUPPORTED, 0), shape
+        assert need32 > 0 and f32 == forward == bnd.GM_ERR_INVALID_ARG, shape  # taken, but for their misaligned outputs
+    assert got[-1] > 0

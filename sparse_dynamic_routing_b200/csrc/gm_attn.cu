@@ -126,7 +126,13 @@ WinF32Plan window_f32_plan(int B, int n, int hq, int hkv, int d, int window, int
     const int near = (int)std::min<int64_t>(all, ((int64_t)tile - 1 + window + gm::WT - 1) / gm::WT);
     p.steps = std::max(near * G, 4);
     p.chunks = (all * G + p.steps - 1) / p.steps;
-    p.sink_blocks = p.chunks > 1 ? std::min(p.nblk, (sinks + tile - 1) / tile) : 0;
+    // Pieces take 2 x tile x d fp32 sums of workspace each. Eight per SM fill the GPU whatever their
+    // length; with sinks in many blocks more of them would only let the workspace grow with n^2.
+    const int sink_blocks = std::min(p.nblk, (sinks + tile - 1) / tile);
+    const int64_t whole = (int64_t)B * hkv * sink_blocks;
+    if (whole > 0) p.chunks = (int)std::min<int64_t>(p.chunks, std::max<int64_t>(1, 8 * 148 / whole));
+    p.steps = std::max(p.steps, (all * G + p.chunks - 1) / p.chunks);
+    p.sink_blocks = p.chunks > 1 ? sink_blocks : 0;
     p.delta_bytes = ((size_t)B * n * hq * 4 + 15) / 16 * 16;
     p.bytes = p.delta_bytes + (size_t)B * hkv * p.sink_blocks * p.chunks * 2 * tile * d * 4;
     return p;
@@ -144,8 +150,7 @@ template <int D, int R> gm_status window_dkv_f32(gm::WinArgs a, const WinF32Plan
     a.part = (float *)((char *)a.delta + p.delta_bytes);
     const int64_t per = (int64_t)a.B * a.hkv;
     const int64_t grid = per * (a.nblk - a.sink_blocks) + per * a.sink_blocks * a.chunks;
-    if (grid >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
-    kern<<<(unsigned)grid, 256, S::dkv_smem, st>>>(a);
+    kern<<<(unsigned)grid, 256, S::dkv_smem, st>>>(a);  // no more blocks than rows of k, and the pieces
     if (a.sink_blocks > 0)
         gm::win_dkv_join_f32_kernel<D, R><<<(unsigned)(per * a.sink_blocks * (2 * S::ROWS * D / 4) / 256), 256, 0, st>>>(a);
     return launched();

@@ -75,3 +75,14 @@ def test_padded_rows_of_the_bf16_backward_are_counted():
         assert (bf16, need) == (bnd.GM_ERR_UNSUPPORTED, 0), shape
         assert need32 > 0 and f32 == forward == bnd.GM_ERR_INVALID_ARG, shape  # taken, but for their misaligned outputs
     assert got[-1] > 0
+
+
+def test_fp32_backward_workspace_does_not_grow_with_the_square():
+    """Beyond delta (a float per row and head) the workspace holds pieces of key blocks with sinks: not
+    more than about eight per SM, however many blocks have sinks."""
+    size = "lib.gm_window_attention_backward_workspace_size"
+    shapes = [(B, n, hq, hkv, d, w, sinks) for B, hq, hkv in ((1, 1, 1), (1, 16, 8), (8, 8, 2)) for d in (64, 128)
+              for n in (1000, 16384, 131072, 2 ** 20) for w, sinks in ((1, 4), (64, n // 2), (512, n - 1), (n, n))]
+    got = probe(*(f"{size}({bnd.GM_F32}, {', '.join(map(str, x))})" for x in shapes))
+    for (B, n, hq, hkv, d, w, sinks), need in zip(shapes, got):
+        assert 4 * B * n * hq <= need <= 4 * B * n * hq + 16 + 8 * 148 * 2 * 64 * d * 4, (B, n, hq, hkv, d, w, sinks)

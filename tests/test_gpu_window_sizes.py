@@ -74,3 +74,11 @@ def test_bf16_long_rows_of_several_heads_d128():
     """Several long items per CTA, of one head and of pairs."""
     run_and_check(3, 1531, 8, 2, 128, torch.bfloat16, 200, 4, lens=[1531, 901, 1500], seed=3)
     run_and_check(4, 2000, 9, 3, 128, torch.bfloat16, 600, 0, seed=4)
+
+
+@pytest.mark.parametrize("B,n,hq,hkv,window,sinks,lens", [
+    (1, 6000, 4, 2, 20, 2500, None),                                       # pieces of many blocks
+    (4, 2500, 16, 8, 60, 2490, [2500, 2491, 70, 1300]),                    # enough blocks: none is cut
+    (1, 3000, 1, 1, 1, 3000, [2999])])
+def test_fp32_sinks_in_many_blocks(B, n, hq, hkv, window, sinks, lens):
+    run_and_check(B, n, hq, hkv, 64, torch.float32, window, sinks, lens=lens, seed=n)

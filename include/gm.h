@@ -525,12 +525,15 @@ gm_status gm_dense_refresh_edges(const void *q, const void *k, gm_dtype dtype, c
  *   lens      device int32 [B]: tokens of each sequence, taken as 0..n; NULL: n each
  *   window    >= 1 (n or more: every earlier token is visible)
  *   sinks     >= 0 first tokens that stay visible outside the window
+ *   scale     finite, also when multiplied by log2(e) (here and below)
  *   o         device, `dtype`, [B, n, hq, d], 16-byte aligned, written in full
  *   lse       device fp32 [B, n, hq], written in full; may be NULL. Outputs must not overlap the
  *             inputs or one another (here and below)
  *   limits    d in {64, 128}; any hq / hkv; n < 2^30, B * n * hq < 2^31
  * Scores, softmax statistics and sums are fp32; for GM_BF16 the probabilities are rounded to
- * bf16 before they meet v. Deterministic.
+ * bf16 before they meet v. Sums are divided by the softmax's own sum last, so scores, and 2^8
+ * times the sum of |v| over the keys a row sees, have to stay within fp32's range; weights below
+ * 2^-126 of a row's largest may count as 0 (both here and below). Deterministic.
  */
 gm_status gm_window_attention_forward(const void *q, const void *k, const void *v, gm_dtype dtype,
                                       const int32_t *lens, int B, int n, int hq, int hkv, int d,

@@ -44,12 +44,15 @@ template <auto KERNEL> bool raise_smem(size_t bytes, int regs = 0)
     return true;
 }
 
+// Kernels take exponentials in base 2: the factor with log2(e) in it has to be finite as well.
+bool good_scale(float scale) { return std::isfinite(scale * gm::LOG2E); }
+
 // ---- windowed attention -------------------------------------------------------------------------
 
 gm_status check_window(gm_dtype dtype, int B, int n, int hq, int hkv, int d, int window, int sinks, float scale)
 {
     if (B < 0 || n < 0 || hq < 1 || hkv < 1 || d < 1 || hq % hkv != 0) return GM_ERR_INVALID_ARG;
-    if (window < 1 || sinks < 0 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (window < 1 || sinks < 0 || !good_scale(scale)) return GM_ERR_INVALID_ARG;
     if (dtype != GM_F32 && dtype != GM_BF16) return GM_ERR_INVALID_ARG;
     if (d != 64 && d != 128) return GM_ERR_UNSUPPORTED;
     if (n >= (1 << 30) || (int64_t)B * n >= MAX_ROWS || (int64_t)B * n * hq >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
@@ -554,7 +557,7 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
     const gm_status st = check_cache(a.c, const_cast<void *>(kq), const_cast<void *>(vq), const_cast<float *>(kscale),
                                      const_cast<float *>(vscale), num_pages, page, table, max_pages, lens, B, t, hq, hkv,
                                      d, dtype);
-    if (window < 1 || sinks < 0 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (window < 1 || sinks < 0 || !good_scale(scale)) return GM_ERR_INVALID_ARG;
     if (st != GM_OK || (int64_t)B * t == 0) return st;
     if (!q || !o || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
     const Kv8Plan p = kv8_plan(B, t, hq, hkv, d, kv8_keys((int64_t)max_pages * page, window, sinks, t));
@@ -591,7 +594,7 @@ gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, 
     const gm_status st = check_cache(a.c, const_cast<void *>(kq), const_cast<void *>(vq), const_cast<float *>(kscale),
                                      const_cast<float *>(vscale), num_pages, page, table, max_pages, lens, B, t, hq, hkv,
                                      d, dtype);
-    if (s < 1 || s > 32 || !std::isfinite(scale)) return GM_ERR_INVALID_ARG;
+    if (s < 1 || s > 32 || !good_scale(scale)) return GM_ERR_INVALID_ARG;
     if (st != GM_OK || (int64_t)B * t == 0) return st;
     if (!q || !o || !idx || !w || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
     a.q = q;

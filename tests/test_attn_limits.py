@@ -86,3 +86,13 @@ def test_fp32_backward_workspace_does_not_grow_with_the_square():
     got = probe(*(f"{size}({bnd.GM_F32}, {', '.join(map(str, x))})" for x in shapes))
     for (B, n, hq, hkv, d, w, sinks), need in zip(shapes, got):
         assert 4 * B * n * hq <= need <= 4 * B * n * hq + 16 + 8 * 148 * 2 * 64 * d * 4, (B, n, hq, hkv, d, w, sinks)
+
+
+def test_scale_with_no_finite_factor_in_base_2_is_refused():
+    """3e38 is finite, 3e38 log2(e) is not: a score of 0 would become 0 times infinity."""
+    calls = []
+    for scale in ("3e38", "-3e38"):
+        calls += [f"A.{f}(lib, B=0, scale={scale})" for f in ("forward", "backward", "attention", "sea")]
+    fine = [f"A.{f}(lib, B=0, scale=2e38)" for f in ("forward", "backward", "attention", "sea")]
+    got = probe(*calls, *fine)
+    assert got == [bnd.GM_ERR_INVALID_ARG] * len(calls) + [bnd.GM_OK] * len(fine)

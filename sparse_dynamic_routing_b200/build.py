@@ -16,8 +16,11 @@ import glob
 import os
 import subprocess
 import sys
+import threading
+import time
 
-HERE = os.path.dirname(os.path.abspath(__file__))
+SELF = os.path.abspath(__file__)
+HERE = os.path.dirname(SELF)
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgm_b200.so")
@@ -50,43 +53,74 @@ def stale(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    return any(os.path.getmtime(s) > t for s in sources())
+    return any(os.path.getmtime(s) > t for s in [*sources(), SELF])
 
 
 def _object_is_stale(obj: str, dep: str) -> bool:
-    """Whether an object is older than a file named in its dependency list (as nvcc wrote it)."""
+    """Whether an object is older than this file (its flags) or than a file named in its dependency list
+    (as nvcc wrote it)."""
     if not os.path.exists(obj) or not os.path.exists(dep):
         return True
     t = os.path.getmtime(obj)
     with open(dep) as f:
         files = f.read().split(":", 1)[-1].replace("\\\n", " ").split()
-    return any(not os.path.exists(x) or os.path.getmtime(x) > t for x in files)
+    return any(not os.path.exists(x) or os.path.getmtime(x) > t for x in [*files, SELF])
 
 
-def _compile(src: str, variant: str, flags: list[str], force: bool) -> tuple[str, subprocess.Popen | None]:
-    """The object of one source, and the compiler process that is making it (None: up to date)."""
-    obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + variant + ".o")
-    dep = obj + ".d"
-    if not force and not _object_is_stale(obj, dep):
-        return obj, None
-    return obj, subprocess.Popen([nvcc(), *NVCC_FLAGS, *flags, "-MD", "-MF", dep, "-c", src, "-o", obj])
+class _Compile:
+    """The object of one source: up to date, or on its way in a compiler process of its own. The
+    compiler writes under names that no other build uses; a whole object takes its place by renaming."""
+
+    def __init__(self, src: str, variant: str, flags: list[str], force: bool):
+        self.obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + variant + ".o")
+        self.proc = None
+        if force or _object_is_stale(self.obj, self.obj + ".d"):
+            self.start = time.time()
+            self.tmp = f"{self.obj}.{os.getpid()}.{threading.get_ident()}.tmp"
+            self.proc = subprocess.Popen([nvcc(), *NVCC_FLAGS, *flags, "-MD", "-MF", self.tmp + ".d", "-c", src,
+                                          "-o", self.tmp])
+
+    def finish(self) -> None:
+        """Waits for the compiler; raises if it failed."""
+        if self.proc is None:
+            return
+        try:
+            if self.proc.wait() != 0:
+                raise subprocess.CalledProcessError(self.proc.returncode, self.proc.args)
+            # as old as its sources were when they were read: an edit made meanwhile is newer
+            os.utime(self.tmp, (self.start, self.start))
+            os.replace(self.tmp + ".d", self.obj + ".d")
+            os.replace(self.tmp, self.obj)
+        finally:
+            for left in (self.tmp, self.tmp + ".d"):
+                if os.path.exists(left):
+                    os.remove(left)
 
 
 def build(force: bool = False, verbose: bool = False, checked: bool = False) -> str:
     lib = CHECKED_LIB if checked else LIB
     if force or stale(lib):
         os.makedirs(OBJ_DIR, exist_ok=True)
+        start = time.time()
         flags = (["-DGM_CHECKED=1"] if checked else []) + (["-Xptxas", "-v"] if verbose else [])
-        made = [_compile(src, "_checked" if checked else "", flags, force)
+        made = [_Compile(src, "_checked" if checked else "", flags, force)
                 for src in sorted(glob.glob(os.path.join(CSRC, "*.cu")))]
-        for obj, proc in made:
-            if proc is not None and proc.wait() != 0:
-                if os.path.exists(obj):
-                    os.remove(obj)
-                raise subprocess.CalledProcessError(proc.returncode, proc.args)
-        tmp = lib + f".tmp{os.getpid()}"
-        subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *(obj for obj, _ in made), "-o", tmp], check=True)
-        os.replace(tmp, lib)
+        failed = None
+        for m in made:  # every compiler has ended before a failure is passed on
+            try:
+                m.finish()
+            except subprocess.CalledProcessError as e:
+                failed = failed or e
+        if failed is not None:
+            raise failed
+        tmp = os.path.join(OBJ_DIR, f"{os.path.basename(lib)}.{os.getpid()}.{threading.get_ident()}.tmp")
+        try:
+            subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", *(m.obj for m in made), "-o", tmp], check=True)
+            os.utime(tmp, (start, start))
+            os.replace(tmp, lib)
+        finally:
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return lib
 
 

@@ -103,9 +103,11 @@ __device__ __forceinline__ float ex2_ftz(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 2^x of two x <= 127 on the FMA pipe: 2^n p(f) with n = x rounded, f = x - n in [-1/2, 1/2] and p
-// of degree 5 with the least largest relative error there (7.5e-8 exact, 2.2e-7 evaluated in fp32;
-// ex2.approx: 2^-22). x below -126 gives 2^-126, NaN stays NaN.
+// 2^x of two x <= 127 on the FMA pipe: 2^n p(f) with n = x rounded, f = x - n in [-1/2, 1/2] (the
+// reduction of Cody and Waite, Software Manual for the Elementary Functions, 1980) and p of degree 5
+// with the least largest relative error there, fitted by reweighted least squares (Lawson, 1961) and
+// rounded to fp32 (1.6e-7 with these coefficients, 2.2e-7 evaluated in fp32; ex2.approx: 2^-22). An integer x
+// gives 2^x (1 + 2^-23). x below -126 gives 2^-126, NaN stays NaN.
 __device__ __forceinline__ float2 ex2_poly(float2 x)
 {
     constexpr float ROUND = 12582912.0f;  // 1.5 * 2^23: the sum's low bits are n

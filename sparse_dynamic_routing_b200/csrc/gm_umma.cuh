@@ -44,9 +44,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_bmn(int M, int N) { return
 // The functions below are executed by all lanes of a warp and act in the lane whose `lead` is not
 // 0. Nothing branches on the lane, so operands that are the same in every lane stay in uniform
 // registers, where the MMA instruction wants them: issued under `if (lane == 0)` each one first
-// moves its descriptors there, 100 to 140 cycles per instruction instead of the 64 that a
-// 128 x 128 x 16 product takes. Descriptors are given as their low word (sdesc_lo plus an offset in
-// 16-byte units) and their high word, the same for every operand here.
+// moves its descriptors there, 100 to 140 cycles per instruction instead of about 90, which a
+// 128 x 128 x 16 product takes at the rate that cuBLAS reaches (64 at the nominal peak). Descriptors
+// are given as their low word (sdesc_lo plus an offset in 16-byte units) and their high word, the
+// same for every operand here.
 
 __device__ __forceinline__ uint32_t elect_lead()
 {

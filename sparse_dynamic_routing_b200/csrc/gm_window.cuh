@@ -22,7 +22,10 @@
 // is two kernels without atomics: one per query block (dq) and one per key block (dk, dv, summed
 // over the group's heads in the block), so every gradient is written once, in a fixed order. Key
 // blocks with sinks, which every query sees, are cut into pieces of about the other blocks' length
-// whose sums a last kernel adds (B=4 n=1000 window 200, 2 sinks: 659 -> 349 us for the backward).
+// whose sums a last kernel adds (B=4 n=1000, 4/2 heads, d=128, window 200, 2 sinks: 659 -> 349 us for
+// the backward). At a size that fills the GPU, B=8 n=4096, 16/8 heads, d=128, window 512, 4 sinks:
+// forward 4.43 ms, backward 13.9 ms, 29 and 33 of the 74 TFLOP/s that the pipes have at 1965 MHz
+// (4 d and 14 d operations per visible pair and head).
 #pragma once
 
 #include <math.h>

@@ -16,20 +16,25 @@
 //         dV(j+1) and S(j+2).
 //
 // In both, two groups of four warps share the 128 lanes and take half of the columns each, each
-// keeping its bf16 results inside its own half of the fp32 tile. nl = -lse log2(e) and
-// delta = <dout, o> come from a pass over o and dout, laid out [B, hq, npad] with npad a
-// multiple of 128; rows at or past the sequence's end have nl = -inf (P <= 2^-126) and delta =
-// 0. Such rows of the tiles are zeroed in shared memory where a product sums over them. An eighth of
-// the exponentials runs on the FMA pipe (n = 16384 3661 -> 3547 us, window 1024 1266 -> 1254 us in
-// turn; three sixteenths 3609, 1262).
+// keeping its bf16 results inside its own half of the fp32 tile. P and dS are rounded to bf16, at most
+// half a step (2^-8) each, because both operands of a product have one type and the other one comes in
+// bf16: against 64 bits forward and backward together are off by 0.0024 in the 2-norm at window 1024,
+// in fp32 with one rounding at the end by 0.0017.
+//
+// nl = -lse log2(e) and delta = <dout, o> come from a pass over o and dout, laid out [B, hq, npad] with
+// npad a multiple of 128; rows at or past the sequence's end have nl = -inf (P <= 2^-126) and delta = 0.
+// Such rows of the tiles are zeroed in shared memory where a product sums over them. An eighth of the
+// exponentials runs on the FMA pipe (n = 16384 3661 -> 3547 us, window 1024 1266 -> 1254 us in turn;
+// three sixteenths 3609, 1262).
 //
 // The threads read scores and dP from TMEM 32 columns at a time, the next under the arithmetic of the
 // one before (window 1024 1207 -> 1163 us in turn; all 64 at once need fewer waits but hold every
 // warp at the same place).
 //
-// B=8 n=4096, 16/8 heads, d=128: window 512 800 us, window 1024 1150 us; B=1 n=16384 full 3440 us
-// (at the power limit). The tensor pipe is busy half of the time (dq 50 %): a step's products wait for its
-// elements and the other way round, at one CTA per SM.
+// 16/8 heads, d=128, 4 sinks beside a window; back to back on the same tensors (at the power limit), in
+// brackets a single call with a cold L2: B=8 n=4096 window 512 790 us (720), window 1024 1150 us (1030);
+// B=1 n=16384 full 3470 us (3060). The tensor pipe is busy half of the time (dq 50 %): a step's products
+// wait for its elements and the other way round, at one CTA per SM.
 //
 // Both kernels run one CTA per SM, which takes item after item from a counter in the workspace
 // (items differ in length, by the mask and by the sequences): the loads, S and dP of the next item

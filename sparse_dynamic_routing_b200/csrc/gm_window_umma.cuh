@@ -4,7 +4,10 @@
 // group over the same rows (groups of even size), or one head's next 256 rows. Per block of 128
 // keys and tile: S = Q K^T into TMEM; one thread per query row reads its scores, keeps the running
 // maximum and sum, and writes P as bf16 over S; O += P V with P as the TMEM operand. While one
-// tile's rows are in the softmax, the tensor cores work on the other's.
+// tile's rows are in the softmax, the tensor cores work on the other's. P is rounded because both
+// operands of a product have one type, and V comes in bf16: at most half a step, 2^-8, of a weight.
+// Against 64 bits the output is off by 0.0022 in the 2-norm at window 512, with P in fp32 it would be by
+// 0.0016 (the output's own rounding).
 //   warps 0-3, 4-7  softmax of tile 0, 1 (and their output)
 //   warp 8          TMA loads: Q per item, K and V through their stages
 //   warp 9          MMA issue
@@ -17,24 +20,26 @@
 // With the softmax replaced by nothing the kernel takes 738 us for n = 16384 (16 heads, full), with
 // it 935: the products (at 90 % of the measured bf16 rate when alone) bound it, then the wait for
 // each block's exponentials (16 per SM and cycle). A quarter of them therefore runs on the FMA pipe
-// (ex2_poly), in blocks that are seen whole: window 512 224 -> 206 us, n = 16384 1063 -> 1002 us in
-// turn; an eighth gives 223 and 1046, three eighths 206 and 1031. Blocks of 64 keys with two score
-// buffers per tile remove the wait but run the products at N = 64, 976 us alone.
+// (ex2_poly; the idea was published in 2025 for attention on this generation of GPUs), in blocks that
+// are seen whole: window 512 224 -> 206 us, n = 16384 1063 -> 1002 us in turn; an eighth gives 223 and
+// 1046, three eighths 206 and 1031. Blocks of 64 keys with two score buffers per tile remove the wait
+// but run the products at N = 64, 976 us alone.
 //
 // The grid is one CTA per SM; each takes item after item (longest first, every second round in
 // reverse order), so the next item's loads and first scores run under the output of the one
 // before (window 512, B=8 n=4096: 276 us with a CTA per item, 240 us at that time).
 //
-// B=8 n=4096, 16/8 heads, d=128: window 512 206 us, window 1024 305 us; B=1 n=16384 full 997 us
-// (1.1 PFLOP/s, at the power limit). At window 1024 the tensor pipe is busy 47 % of the time, the
-// exponential unit 34 %, the issue slots 38 %: what is left is the chain scores - maximum -
-// exponentials - product of one tile, which the other tile covers only in part, and the blocks seen
-// in part at both ends of a window.
+// 16/8 heads, d=128, 4 sinks beside a window; back to back on the same tensors, in brackets a single
+// call with a cold L2: B=8 n=4096 window 512 200 us (224), window 1024 307 us (314); B=1 n=16384 full
+// 1030 us (960; back to back it runs at the power limit, 1.1 PFLOP/s). At window 1024 the tensor pipe is
+// busy 47 % of the time, the exponential unit 34 %, the issue slots 38 %: what is left is the chain
+// scores - maximum - exponentials - product of one tile, which the other tile covers only in part, and
+// the blocks seen in part at both ends of a window.
 //
-// The running maximum is allowed to lag: O is rescaled only when a row's maximum has grown by
-// more than 2^8 since the last time (P then stays below 2^8, far inside fp32's and bf16's range),
-// so O rarely leaves TMEM before the end. Key blocks are the two ranges of gm_window.cuh; a block
-// narrower than 128 keys (a few sinks) takes only as many 32-column pieces as it has keys, and
+// The running maximum (the online softmax of Milakov and Gimelshein, 2018) is allowed to lag, an idea
+// published beside the one above: O is rescaled only when a row's maximum has grown by more than 2^8
+// since the last time (P then stays below 2^8, far inside fp32's and bf16's range), so O rarely leaves
+// TMEM before the end. Key blocks are the two ranges of gm_window.cuh; a block narrower than 128 keys (a few sinks) takes only as many 32-column pieces as it has keys, and
 // pieces that none of a warp's rows sees are skipped. The path of blocks that are seen in part
 // stays a rolled loop: unrolled like the other it costs more in instruction fetches than it saves
 // (225 against 243 us).

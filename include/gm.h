@@ -593,7 +593,8 @@ size_t gm_window_attention_backward_workspace_size(gm_dtype dtype, int B, int n,
  *   lens        device int32 [B]: tokens that each sequence holds before the call
  *   new_lens    device int32 [B]: rows of k and v that belong to the sequence, taken as 0..t;
  *               NULL: t each
- *   page        16, 32, 64 or 128 tokens; limits: d in {64, 128}, num_pages * hkv * page < 2^32
+ *   page        16, 32, 64 or 128 tokens; limits: d in {64, 128}, num_pages * hkv * page < 2^32,
+ *               max_pages * page < 2^31, B * t * hkv < 2^31
  * No two sequences may write the same page in one call (fork a page by copying it first). A
  * page outside [0, num_pages), a negative length, or a token past max_pages * page is not
  * written and raises the device index-range flag (gm_check_device_errors).
@@ -617,7 +618,10 @@ gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int
  *   workspace   device scratch owned by the caller, 16-byte aligned, at least
  *               gm_kv8_attention_workspace_size(...) bytes (NULL where that is 0); garbage on
  *               return. Calls that overlap on the GPU need one each
- *   limits      d in {64, 128}; any hq / hkv; page as gm_kv8_append
+ *   limits      d in {64, 128}; any hq / hkv; page as gm_kv8_append; B * t * hq and
+ *               max_pages * page < 2^31
+ * Made for few query rows: a KV head's keys are read once per 16 of them (t * hq / hkv), so a whole
+ * prompt with nothing cached before it is better served by gm_window_attention_forward.
  * fp32 scores, statistics and sums; for GM_BF16 probabilities are rounded to fp16 before they
  * meet the values, for GM_F32 queries and probabilities keep 22 bits. Deterministic. A page
  * outside [0, num_pages) or a length outside [0, max_pages * page] raises the device

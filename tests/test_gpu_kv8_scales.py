@@ -80,3 +80,25 @@ def test_value_scales_far_apart(gap, low, high, page, tail, dtype):
             off = (o[0, x, h].double().cpu() - want).abs()
             assert (off <= tol).all(), (x, h, float((off / tol).max()))
         assert abs(float(lse[0, x, 0]) - (gap * math.log(2) + math.log(float(p.sum())))) <= 2.0 ** -20 * (1 + gap)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gap,low,high", [(100, -100, 110), (120, -100, 20), (60, -100, 110), (125, 0, 110), (3, 110, -100),
+                                          (0, -100, 110), (40, -30, 60)])
+def test_sparse_edges_over_scales_far_apart(gap, low, high, dtype):
+    """Three edges of equal scores: weight 1 to the first page, 2^-gap to the second, and an unused slot."""
+    page = 16
+    c = two_blocks(gap, low, high, page, 3)
+    q = torch.zeros(1, 1, 2, D, dtype=dtype, device="cuda")
+    at = torch.tensor([5, page + 2, page + 9])
+    w = torch.tensor([1.0, 2.0 ** -gap, 2.0 ** -gap, 0.0])
+    idx = torch.tensor([*at, -1], dtype=torch.int32)
+    o, lse = gm.gm_kv8_sea_forward(q, idx.view(1, 1, 1, 4).cuda(), w.view(1, 1, 1, 4).cuda(), *(x.cuda() for x in args(c)))
+    gm.gm_check_device_errors()
+    v, p = R.cached(c, "v", 0, 0, int(c["lens"]))[at], w[:3].double()
+    part = p[:, None] * v
+    # logarithm, exponential and sums in fp32, weights in 22 bits, the result rounded once
+    tol = (8 * 2.0 ** -21 * (1 + gap) + R.half_step(dtype)) * part.sum(0) / p.sum()
+    for h in range(2):
+        assert ((o[0, 0, h].double().cpu() - part.sum(0) / p.sum()).abs() <= tol).all()
+    assert abs(float(lse[0, 0, 0]) - math.log(float(p.sum()))) <= 2.0 ** -20 * (1 + gap)

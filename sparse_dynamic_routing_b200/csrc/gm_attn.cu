@@ -18,8 +18,14 @@
 #define GM_CHECKED 0
 #endif
 
+// Whether this library's calls of this file were ever made: before the first, their error word needs no
+// reading (a copy from the device, 12 us, and the loading of their kernels).
+static std::atomic<bool> g_attn_used{false};
+
 bool gm_attn_take_errors(unsigned *flag)
 {
+    *flag = 0;
+    if (!g_attn_used.load()) return true;
     if (cudaMemcpyFromSymbol(flag, gm::g_error_flag, sizeof(*flag)) != cudaSuccess) return false;
     const unsigned zero = 0;
     return *flag == 0 || cudaMemcpyToSymbol(gm::g_error_flag, &zero, sizeof(zero)) == cudaSuccess;
@@ -471,6 +477,7 @@ gm_status gm_window_attention_forward(const void *q, const void *k, const void *
     if (st != GM_OK || (int64_t)B * n == 0) return st;
     if (!q || !k || !v || !o) return GM_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    g_attn_used = true;
     gm::WinArgs a = window_args(B, n, hq, hkv, window, sinks, scale, lens);
     a.q = q;
     a.k = k;
@@ -502,6 +509,7 @@ gm_status gm_window_attention_backward(const void *q, const void *k, const void 
         if (!aligned16(p)) return GM_ERR_INVALID_ARG;
     if (workspace_bytes < gm_window_attention_backward_workspace_size(dtype, B, n, hq, hkv, d, window, sinks))
         return GM_ERR_INVALID_ARG;
+    g_attn_used = true;
     gm::WinArgs a = window_args(B, n, hq, hkv, window, sinks, scale, lens);
     a.q = q;
     a.k = k;
@@ -526,6 +534,7 @@ gm_status gm_kv8_append(const void *k, const void *v, gm_dtype dtype, int B, int
                                      d, dtype);
     if (st != GM_OK || (int64_t)B * t == 0) return st;
     if (!k || !v || !aligned16(k) || !aligned16(v)) return GM_ERR_INVALID_ARG;
+    g_attn_used = true;
     a.k = k;
     a.v = v;
     a.new_lens = new_lens;
@@ -563,6 +572,7 @@ gm_status gm_kv8_attention_forward(const void *q, gm_dtype dtype, int B, int t, 
     const Kv8Plan p = kv8_plan(B, t, hq, hkv, d, kv8_keys((int64_t)max_pages * page, window, sinks, t));
     if (p.items * p.splits >= MAX_ROWS) return GM_ERR_UNSUPPORTED;
     if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return GM_ERR_INVALID_ARG;
+    g_attn_used = true;
     a.q = q;
     a.q_lens = q_lens;
     a.o = o;
@@ -597,6 +607,7 @@ gm_status gm_kv8_sea_forward(const void *q, gm_dtype dtype, const int32_t *idx, 
     if (s < 1 || s > 32 || !good_scale(scale)) return GM_ERR_INVALID_ARG;
     if (st != GM_OK || (int64_t)B * t == 0) return st;
     if (!q || !o || !idx || !w || !aligned16(q) || !aligned16(o)) return GM_ERR_INVALID_ARG;
+    g_attn_used = true;
     a.q = q;
     a.idx = idx;
     a.w = w;
